@@ -9,7 +9,10 @@ Entry points (same names as ``include/ar.h``): ar_allreduce, ar_allreduce_ws, ar
 ar_allreduce_workspace_size,
 ar_allreduce_buckets, ar_allreduce_tensors, ar_reduce_scatter, ar_all_gather, ar_bucket_plan, ar_bucket_pack,
 ar_bucket_unpack, ar_fp8_quant, ar_fp8_dequant, ar_auto_algo, ar_chunk_bounds, ar_status_string, ar_last_call,
-ar_version. Helpers: chunk_bounds, make_copy_descs, BucketedAllReduce.
+ar_version; next to the reduction in a transformer layer: ar_allreduce_rmsnorm, ar_allreduce_rmsnorm_bwd,
+ar_allreduce_rmsnorm_bwd_workspace_size, ar_expert_rows, ar_expert_sort, ar_expert_sort_workspace_size,
+ar_expert_dispatch, ar_expert_combine, ar_expert_combine_bwd. Helpers: chunk_bounds, make_copy_descs,
+BucketedAllReduce.
 """
 from __future__ import annotations
 
@@ -31,6 +34,9 @@ __all__ = [
     "ar_bucket_pack",
     "ar_bucket_unpack", "ar_fp8_quant", "ar_fp8_dequant", "ar_status_string", "ar_last_call", "ar_version",
     "make_copy_descs", "BucketedAllReduce", "dtype_code",
+    "AR_NORM_MAX_HIDDEN", "AR_MAX_EXPERTS", "ar_allreduce_rmsnorm", "ar_allreduce_rmsnorm_bwd",
+    "ar_allreduce_rmsnorm_bwd_workspace_size", "ar_expert_rows", "ar_expert_sort", "ar_expert_sort_workspace_size",
+    "ar_expert_dispatch", "ar_expert_combine", "ar_expert_combine_bwd",
 ]
 
 AR_OK, AR_ERR_INVALID, AR_ERR_UNSUPPORTED, AR_ERR_ALIAS, AR_ERR_WORKSPACE, AR_ERR_HIP = 0, 1, 2, 3, 4, 5
@@ -41,6 +47,8 @@ AR_ALGO_TREE, AR_ALGO_TREE_STEPWISE, AR_ALGO_AUTO = 6, 7, 8
 AR_AUTO_STEP_NS, AR_AUTO_LINK_GBPS = 1900, 153
 AR_MAX_RANKS = 64
 AR_FP8_BLOCK = 128
+AR_NORM_MAX_HIDDEN = 32768
+AR_MAX_EXPERTS = 1024
 AR_NOALLOC_WS_BYTES = 64 << 20
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -89,6 +97,16 @@ def lib():
         L.ar_auto_algo.argtypes = [i32, sz, i32]
         L.ar_chunk_bounds.argtypes = [i32, sz, vp]
         L.ar_epilogue.argtypes = [vp, vp, sz, i32, i32, i32, vp]
+        f32 = ctypes.c_float
+        L.ar_allreduce_rmsnorm.argtypes = [vp, i32, sz, sz, i32, vp, vp, i32, f32, vp, vp, vp, vp, vp, vp, vp]
+        L.ar_allreduce_rmsnorm_bwd_workspace_size.argtypes = [sz, sz, ctypes.POINTER(sz)]
+        L.ar_allreduce_rmsnorm_bwd.argtypes = [vp, i32, sz, sz, i32, vp, vp, vp, i32, vp, vp, vp, vp, vp, sz, vp]
+        L.ar_expert_rows.argtypes = [sz, i32, i32, i32, ctypes.POINTER(sz)]
+        L.ar_expert_sort_workspace_size.argtypes = [sz, i32, i32, ctypes.POINTER(sz)]
+        L.ar_expert_sort.argtypes = [vp, sz, i32, i32, i32, vp, vp, vp, vp, sz, vp, sz, vp]
+        L.ar_expert_dispatch.argtypes = [vp, vp, vp, vp, vp, sz, i32, i32, sz, i32, vp, vp, sz, vp]
+        L.ar_expert_combine.argtypes = [vp, vp, vp, vp, sz, i32, sz, i32, sz, vp, vp]
+        L.ar_expert_combine_bwd.argtypes = [vp, vp, vp, vp, vp, vp, sz, i32, i32, sz, i32, sz, vp, vp, vp]
         L.ar_status_string.argtypes = [i32]
         L.ar_status_string.restype = ctypes.c_char_p
         L.ar_last_call.argtypes = [ctypes.POINTER(_CallRecord)]
@@ -96,7 +114,10 @@ def lib():
                      "ar_allreduce_buckets",
                      "ar_allreduce_tensors", "ar_reduce_scatter", "ar_all_gather", "ar_bucket_plan", "ar_bucket_pack",
                      "ar_bucket_unpack", "ar_fp8_quant", "ar_fp8_dequant", "ar_last_call", "ar_version",
-                     "ar_auto_algo", "ar_chunk_bounds", "ar_epilogue"):
+                     "ar_auto_algo", "ar_chunk_bounds", "ar_epilogue", "ar_allreduce_rmsnorm",
+                     "ar_allreduce_rmsnorm_bwd", "ar_allreduce_rmsnorm_bwd_workspace_size", "ar_expert_rows",
+                     "ar_expert_sort", "ar_expert_sort_workspace_size", "ar_expert_dispatch", "ar_expert_combine",
+                     "ar_expert_combine_bwd"):
             getattr(L, name).restype = i32
         _lib = L
     return _lib
@@ -409,6 +430,223 @@ def ar_last_call():
 
 def ar_version() -> int:
     return lib().ar_version()
+
+
+# ------------------------------------------------------------------------------------------ block boundary
+def _addr(t, what, dtypes, shape, dev):
+    """The address of a tensor that must be contiguous, of one of `dtypes`, of `shape`, on GPU `dev` (an index)."""
+    if t.dtype not in dtypes:
+        raise ValueError(f"{what} must be {' or '.join(map(str, dtypes))}, not {t.dtype}")
+    if t.get_device() != dev or dev < 0:
+        raise ValueError(f"{what} must be a GPU tensor on the device of the others")
+    if t.shape != shape:
+        raise ValueError(f"{what} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    return t.data_ptr()
+
+
+def _opt(t, what, dtypes, shape, dev):
+    return None if t is None else _addr(t, what, dtypes, shape, dev)
+
+
+def _rank_addrs(ts, n, what, dtypes, shape, dev):
+    if len(ts) != n:
+        raise ValueError(f"{what} must hold one tensor per rank")
+    return (ctypes.c_void_p * n)(*[_addr(t, what, dtypes, shape, dev) for t in ts])
+
+
+_FLOATS = None
+
+
+def _kinds():
+    """(the dtypes of rows, of 8-bit rows, fp32 alone, int32 alone)"""
+    global _FLOATS
+    if _FLOATS is None:
+        import torch
+        _FLOATS = ((torch.float32, torch.bfloat16, torch.float16), (torch.uint8, torch.float8_e4m3fn),
+                   (torch.float32,), (torch.int32,))
+    return _FLOATS
+
+
+def _matrix(t, what):
+    rows_of = _kinds()[0]
+    if t.dim() != 2:
+        raise ValueError(f"{what} must be a matrix [rows, hidden]")
+    if t.dtype not in rows_of:
+        raise ValueError(f"{what} must be float32, bfloat16 or float16, not {t.dtype}")
+    return t.shape, t.dtype, t.get_device()
+
+
+def _workspace_arg(ws, dev):
+    if ws is None:
+        return None, 0
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError("workspace must be a contiguous GPU tensor on the device of the others")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def ar_allreduce_rmsnorm(ins, gamma, outs, residual=None, residual_out=None, rstd=None, out_scales=None, saved=None,
+                         saved_scales=None, eps=1e-5, stream=None):
+    """Sum of the ranks' partial products ins[r] plus the residual, and its root-mean-square norm to every outs[r].
+
+    ins: list of [rows, hidden] tensors, one per rank. gamma: [hidden] of their dtype or float32. outs: list of
+    [rows, hidden] tensors of the same dtype (outs[r] may be ins[r]), or, with out_scales (a list of float32
+    [rows, ceil(hidden/128)]), of uint8 / float8_e4m3fn codes. residual_out receives the new residual (it may be
+    `residual`), rstd float32 [rows], saved and saved_scales the new residual in 8 bits."""
+    kinds = _kinds()
+    shape, dt, dev = _matrix(ins[0], "ins") if len(ins) else (None, None, -1)
+    if shape is None:
+        raise ValueError("ins must hold one tensor per rank")
+    own, n = (dt,), len(ins)
+    rows, hidden = shape
+    nb = (rows, (hidden + AR_FP8_BLOCK - 1) // AR_FP8_BLOCK)
+    arr_in = _rank_addrs(ins, n, "ins", own, shape, dev)
+    arr_out = _rank_addrs(outs, n, "outs", own if out_scales is None else kinds[1], shape, dev)
+    arr_sc = None if out_scales is None else _rank_addrs(out_scales, n, "out_scales", kinds[2], nb, dev)
+    args = (_opt(residual, "residual", own, shape, dev),
+            _addr(gamma, "gamma", (dt, kinds[2][0]), (hidden,), dev), dtype_code(gamma.dtype), eps, arr_out, arr_sc,
+            _opt(residual_out, "residual_out", own, shape, dev), _opt(rstd, "rstd", kinds[2], (rows,), dev),
+            _opt(saved, "saved", kinds[1], shape, dev), _opt(saved_scales, "saved_scales", kinds[2], nb, dev))
+    device = ins[0].device
+    with _on(device):
+        _check(lib().ar_allreduce_rmsnorm(arr_in, n, rows, hidden, dtype_code(dt), *args, _stream(stream, device)),
+               "ar_allreduce_rmsnorm")
+
+
+def ar_allreduce_rmsnorm_bwd_workspace_size(rows, hidden) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().ar_allreduce_rmsnorm_bwd_workspace_size(rows, hidden, ctypes.byref(out)),
+           "ar_allreduce_rmsnorm_bwd_workspace_size")
+    return out.value
+
+
+def ar_allreduce_rmsnorm_bwd(ins, saved, gamma, rstd, outs, dgamma, saved_scales=None, residual_grad=None,
+                             workspace=None, stream=None):
+    """The gradient of ar_allreduce_rmsnorm: ins are the ranks' partial gradients of y, saved the forward's
+    residual_out (or its 8-bit `saved`, with saved_scales), rstd the forward's. outs[r] receives the gradient of
+    every rank's partial product and of the residual, dgamma (float32 [hidden]) the weight's. workspace: a GPU tensor
+    of ar_allreduce_rmsnorm_bwd_workspace_size(rows, hidden) bytes."""
+    kinds = _kinds()
+    shape, dt, dev = _matrix(ins[0], "ins") if len(ins) else (None, None, -1)
+    if shape is None:
+        raise ValueError("ins must hold one tensor per rank")
+    own, n = (dt,), len(ins)
+    rows, hidden = shape
+    nb = (rows, (hidden + AR_FP8_BLOCK - 1) // AR_FP8_BLOCK)
+    arr_in = _rank_addrs(ins, n, "ins", own, shape, dev)
+    arr_out = _rank_addrs(outs, n, "outs", own, shape, dev)
+    args = (_addr(saved, "saved", own if saved_scales is None else kinds[1], shape, dev),
+            _opt(saved_scales, "saved_scales", kinds[2], nb, dev),
+            _addr(gamma, "gamma", (dt, kinds[2][0]), (hidden,), dev), dtype_code(gamma.dtype),
+            _addr(rstd, "rstd", kinds[2], (rows,), dev), _opt(residual_grad, "residual_grad", own, shape, dev),
+            arr_out, _addr(dgamma, "dgamma", kinds[2], (hidden,), dev), *_workspace_arg(workspace, dev))
+    device = ins[0].device
+    with _on(device):
+        _check(lib().ar_allreduce_rmsnorm_bwd(arr_in, n, rows, hidden, dtype_code(dt), *args,
+                                              _stream(stream, device)), "ar_allreduce_rmsnorm_bwd")
+
+
+def ar_expert_rows(tokens, k, nexperts, align=1) -> int:
+    """The most rows that tokens * k slots take when sorted (what src and the sorted rows must hold)."""
+    out = ctypes.c_size_t(0)
+    _check(lib().ar_expert_rows(tokens, k, nexperts, align, ctypes.byref(out)), "ar_expert_rows")
+    return out.value
+
+
+def ar_expert_sort_workspace_size(tokens, k, nexperts) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().ar_expert_sort_workspace_size(tokens, k, nexperts, ctypes.byref(out)),
+           "ar_expert_sort_workspace_size")
+    return out.value
+
+
+def ar_expert_sort(ids, offsets, counts, pos, src, align=1, workspace=None, stream=None):
+    """Sort the slots ids[tokens, k] (int32; an id outside [0, experts) takes no row) by expert: offsets
+    [experts + 1], counts [experts], pos [tokens, k] (a slot's row or -1) and src [rows] (a row's slot or -1), all
+    int32. Segments start on multiples of `align`; rows >= ar_expert_rows(tokens, k, experts, align)."""
+    i32 = _kinds()[3]
+    if ids.dim() != 2:
+        raise ValueError("ids must be a matrix [tokens, k]")
+    tokens, k = ids.shape
+    dev = ids.get_device()
+    experts, rows = counts.numel(), src.numel()
+    args = (_addr(offsets, "offsets", i32, (experts + 1,), dev), _addr(counts, "counts", i32, (experts,), dev),
+            _addr(pos, "pos", i32, ids.shape, dev), _addr(src, "src", i32, (rows,), dev))
+    device = ids.device
+    at = _addr(ids, "ids", i32, ids.shape, dev)
+    with _on(device):
+        _check(lib().ar_expert_sort(at, tokens, k, experts, align, *args, rows, *_workspace_arg(workspace, dev),
+                                    _stream(stream, device)), "ar_expert_sort")
+
+
+def _pads(offsets, counts, dev):
+    """The addresses of offsets and counts (both or neither), and the number of experts."""
+    if (offsets is None) != (counts is None):
+        raise ValueError("offsets and counts go together")
+    if counts is None:
+        return None, None, 1
+    i32, experts = _kinds()[3], counts.numel()
+    return (_addr(offsets, "offsets", i32, (experts + 1,), dev), _addr(counts, "counts", i32, (experts,), dev), experts)
+
+
+def ar_expert_dispatch(x, pos, offsets, counts, xs, x_scales=None, xs_scales=None, stream=None):
+    """xs[pos[t, j]] = x[t] for the rows of x [tokens, hidden] (float32, bfloat16, float16, or uint8 /
+    float8_e4m3fn with x_scales, whose rows go to xs_scales). The pad rows that offsets and counts describe are
+    zeroed (both None: there are none)."""
+    kinds = _kinds()
+    if x.dim() != 2 or xs.dim() != 2 or pos.dim() != 2:
+        raise ValueError("x, xs and pos must be matrices")
+    dt, dev = x.dtype, x.get_device()
+    if dt not in (kinds[1] if x_scales is not None else kinds[0]):
+        raise ValueError(f"x must be 8-bit rows with x_scales, or float32, bfloat16 or float16 without, not {dt}")
+    if (x_scales is None) != (xs_scales is None):
+        raise ValueError("x_scales and xs_scales go together")
+    tokens, hidden = x.shape
+    rows, k, nb = xs.shape[0], pos.shape[1], (hidden + AR_FP8_BLOCK - 1) // AR_FP8_BLOCK
+    at = (_addr(x, "x", (dt,), x.shape, dev), _opt(x_scales, "x_scales", kinds[2], (tokens, nb), dev),
+          _addr(pos, "pos", kinds[3], (tokens, k), dev))
+    off, cnt, experts = _pads(offsets, counts, dev)
+    to = (_addr(xs, "xs", (dt,), (rows, hidden), dev), _opt(xs_scales, "xs_scales", kinds[2], (rows, nb), dev))
+    device = x.device
+    with _on(device):
+        _check(lib().ar_expert_dispatch(*at, off, cnt, tokens, k, experts, hidden, x.element_size(), *to, rows,
+                                        _stream(stream, device)), "ar_expert_dispatch")
+
+
+def ar_expert_combine(ys, pos, out, weights=None, addend=None, stream=None):
+    """out[t] = sum_j weights[t, j] ys[pos[t, j]] + addend[t]; weights float32 [tokens, k] (None: 1, the gradient of
+    ar_expert_dispatch), addend [tokens, hidden] (may be `out`)."""
+    kinds = _kinds()
+    shape, dt, dev = _matrix(out, "out")
+    if ys.dim() != 2 or pos.dim() != 2:
+        raise ValueError("ys and pos must be matrices")
+    (tokens, hidden), rows, k = shape, ys.shape[0], pos.shape[1]
+    at = (_addr(ys, "ys", (dt,), (rows, hidden), dev), _addr(pos, "pos", kinds[3], (tokens, k), dev),
+          _opt(weights, "weights", kinds[2], (tokens, k), dev), _opt(addend, "addend", (dt,), shape, dev))
+    device = out.device
+    to = _addr(out, "out", (dt,), shape, dev)
+    with _on(device):
+        _check(lib().ar_expert_combine(*at, tokens, k, hidden, dtype_code(dt), rows, to, _stream(stream, device)),
+               "ar_expert_combine")
+
+
+def ar_expert_combine_bwd(dout, ys, pos, weights, offsets, counts, dys, dweights, stream=None):
+    """The gradient of ar_expert_combine: dys[pos[t, j]] = weights[t, j] dout[t] (pad rows zeroed as in
+    ar_expert_dispatch; dys may be ys) and dweights[t, j] = <dout[t], ys[pos[t, j]]> (float32 [tokens, k])."""
+    kinds = _kinds()
+    shape, dt, dev = _matrix(dout, "dout")
+    if ys.dim() != 2 or pos.dim() != 2:
+        raise ValueError("ys and pos must be matrices")
+    (tokens, hidden), rows, k = shape, ys.shape[0], pos.shape[1]
+    at = (_addr(dout, "dout", (dt,), shape, dev), _addr(ys, "ys", (dt,), (rows, hidden), dev),
+          _addr(pos, "pos", kinds[3], (tokens, k), dev), _addr(weights, "weights", kinds[2], (tokens, k), dev))
+    off, cnt, experts = _pads(offsets, counts, dev)
+    to = (_addr(dys, "dys", (dt,), (rows, hidden), dev), _addr(dweights, "dweights", kinds[2], (tokens, k), dev))
+    device = dout.device
+    with _on(device):
+        _check(lib().ar_expert_combine_bwd(*at, off, cnt, tokens, k, experts, hidden, dtype_code(dt), rows, *to,
+                                           _stream(stream, device)), "ar_expert_combine_bwd")
 
 
 # ------------------------------------------------------------------------------------------ bucketing

@@ -11,6 +11,7 @@
 #include <mutex>
 
 #include "ar.h"
+#include "ar_block.h"
 #include "ar_internal.h"
 
 namespace ar {
@@ -527,6 +528,329 @@ int ar_fp8_dequant(const uint8_t* codes, const float* scales, size_t count, void
   if (!codes || !scales || !out || count > static_cast<size_t>(INT64_MAX / 8)) return done(AR_ERR_INVALID);
   hipError_t e = ar::launch_fp8_dequant(codes, scales, static_cast<int64_t>(count), out, out_dtype,
                                         static_cast<hipStream_t>(stream));
+  return done(e == hipSuccess ? AR_OK : AR_ERR_HIP);
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------------------------------ block boundary
+namespace {
+
+// The address ranges of one call, collected and then checked together. A range given twice as the same in-place pair
+// is added once by its caller.
+struct Ranges {
+  Range r[3 * AR_MAX_RANKS + 16];
+  int m = 0;
+  bool bad = false;  // a required pointer is NULL, misaligned, or its range wraps
+  void add(const void* p, size_t bytes, size_t align, bool required = true) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+    if (!a) {
+      bad = bad || required;
+      return;
+    }
+    if (a % align != 0 || a > UINTPTR_MAX - bytes) bad = true;
+    else if (bytes > 0) r[m++] = Range{a, a + bytes};
+  }
+};
+
+bool mul(size_t a, size_t b, size_t* out) { return !__builtin_mul_overflow(a, b, out) && *out <= (size_t(1) << 62); }
+
+size_t blocks_of(size_t hidden) { return (hidden + AR_FP8_BLOCK - 1) / AR_FP8_BLOCK; }
+
+// What both norm entry points check of their common arguments; AR_OK goes on.
+int norm_common(int nranks, size_t rows, size_t hidden, int dtype, int gamma_dtype, size_t* bytes) {
+  if (!valid_dtype(dtype) || !valid_dtype(gamma_dtype) || nranks < 1 || nranks > AR_MAX_RANKS || hidden == 0)
+    return AR_ERR_INVALID;
+  if (gamma_dtype != dtype && gamma_dtype != AR_F32) return AR_ERR_INVALID;
+  if (dtype == AR_I32 || hidden > AR_NORM_MAX_HIDDEN) return AR_ERR_UNSUPPORTED;
+  size_t e;
+  if (!mul(rows, hidden, &e) || !mul(e, static_cast<size_t>(esize_of(dtype)), bytes)) return AR_ERR_INVALID;
+  return AR_OK;
+}
+
+bool rows_fit(size_t tokens, int k, int nexperts, int align, size_t* rows) {
+  if (k < 1 || nexperts < 1 || nexperts > AR_MAX_EXPERTS || align < 1) return false;
+  size_t slots;
+  if (!mul(tokens, static_cast<size_t>(k), &slots) || slots > INT32_MAX) return false;
+  const size_t used = slots < static_cast<size_t>(nexperts) ? slots : static_cast<size_t>(nexperts);
+  *rows = slots + used * static_cast<size_t>(align - 1);
+  return *rows <= INT32_MAX;
+}
+
+}  // namespace
+
+extern "C" {
+
+int ar_allreduce_rmsnorm(const void* const* in_bufs, int nranks, size_t rows, size_t hidden, int dtype,
+                         const void* residual, const void* gamma, int gamma_dtype, float eps, void* const* out_bufs,
+                         float* const* out_scales, void* residual_out, float* rstd, uint8_t* saved,
+                         float* saved_scales, void* stream) {
+  size_t bytes = 0;
+  auto done = [&](int st) { return finish("ar_allreduce_rmsnorm", nranks, rows * hidden, dtype, AR_SUM, -1, st); };
+  const int st = norm_common(nranks, rows, hidden, dtype, gamma_dtype, &bytes);
+  if (st != AR_OK) return done(st);
+  if (!(eps >= 0.0f) || !(eps <= 3.402823466e38f)) return done(AR_ERR_INVALID);
+  if (rows == 0) return done(AR_OK);
+  if (!in_bufs || !out_bufs || (saved == nullptr) != (saved_scales == nullptr)) return done(AR_ERR_INVALID);
+  const size_t es = static_cast<size_t>(esize_of(dtype)), codes = rows * hidden, scales = rows * blocks_of(hidden) * 4;
+  Ranges g;
+  ar::NormArgs a;
+  std::memset(&a, 0, sizeof(a));
+  for (int r = 0; r < nranks; ++r) {
+    g.add(in_bufs[r], bytes, es);
+    if (out_scales) {
+      g.add(out_bufs[r], codes, 1);
+      g.add(out_scales[r], scales, 4);
+      a.out_scales[r] = out_scales[r];
+    } else if (out_bufs[r] != in_bufs[r]) {
+      g.add(out_bufs[r], bytes, es);
+    }
+    a.in[r] = in_bufs[r];
+    a.out[r] = out_bufs[r];
+  }
+  g.add(residual, bytes, es, false);
+  if (residual_out != residual) g.add(residual_out, bytes, es, false);
+  g.add(gamma, hidden * static_cast<size_t>(esize_of(gamma_dtype)), static_cast<size_t>(esize_of(gamma_dtype)));
+  g.add(rstd, rows * 4, 4, false);
+  g.add(saved, codes, 1, false);
+  g.add(saved_scales, scales, 4, false);
+  if (g.bad) return done(AR_ERR_INVALID);
+  if (any_overlap(g.r, g.m)) return done(AR_ERR_ALIAS);
+  a.residual = residual;
+  a.residual_out = residual_out;
+  a.gamma = gamma;
+  a.codes = saved;
+  a.scales = saved_scales;
+  a.rstd = rstd;
+  a.rows = static_cast<int64_t>(rows);
+  a.hidden = static_cast<int>(hidden);
+  a.n = nranks;
+  a.gamma_f32 = gamma_dtype == AR_F32;
+  a.out8 = out_scales != nullptr;
+  a.eps = eps;
+  return done(ar::launch_rmsnorm(a, dtype, static_cast<hipStream_t>(stream)) == hipSuccess ? AR_OK : AR_ERR_HIP);
+}
+
+int ar_allreduce_rmsnorm_bwd_workspace_size(size_t rows, size_t hidden, size_t* bytes) {
+  auto done = [&](int st) {
+    return finish("ar_allreduce_rmsnorm_bwd_workspace_size", 0, rows * hidden, AR_F32, -1, -1, st);
+  };
+  if (!bytes || hidden == 0 || rows > static_cast<size_t>(INT64_MAX)) return done(AR_ERR_INVALID);
+  if (hidden > AR_NORM_MAX_HIDDEN) return done(AR_ERR_UNSUPPORTED);
+  *bytes = static_cast<size_t>(ar::rmsnorm_bwd_groups(static_cast<int64_t>(rows), static_cast<int64_t>(hidden))) *
+           hidden * 4;
+  return done(AR_OK);
+}
+
+int ar_allreduce_rmsnorm_bwd(const void* const* in_bufs, int nranks, size_t rows, size_t hidden, int dtype,
+                             const void* saved, const float* saved_scales, const void* gamma, int gamma_dtype,
+                             const float* rstd, const void* residual_grad, void* const* out_bufs, float* dgamma,
+                             void* workspace, size_t ws_bytes, void* stream) {
+  size_t bytes = 0;
+  auto done = [&](int st) { return finish("ar_allreduce_rmsnorm_bwd", nranks, rows * hidden, dtype, AR_SUM, -1, st); };
+  const int st = norm_common(nranks, rows, hidden, dtype, gamma_dtype, &bytes);
+  if (st != AR_OK) return done(st);
+  if (!dgamma || (rows > 0 && (!in_bufs || !out_bufs))) return done(AR_ERR_INVALID);
+  const size_t es = static_cast<size_t>(esize_of(dtype));
+  const size_t need = static_cast<size_t>(ar::rmsnorm_bwd_groups(static_cast<int64_t>(rows),
+                                                                 static_cast<int64_t>(hidden))) * hidden * 4;
+  Ranges g;
+  ar::NormArgs a;
+  std::memset(&a, 0, sizeof(a));
+  g.add(dgamma, hidden * 4, 4);
+  if (rows > 0) {
+    bool in_place = false;
+    for (int r = 0; r < nranks; ++r) {
+      g.add(in_bufs[r], bytes, es);
+      if (out_bufs[r] == residual_grad && residual_grad && !in_place) in_place = true;  // one of them at most
+      else if (out_bufs[r] != in_bufs[r]) g.add(out_bufs[r], bytes, es);
+      a.in[r] = in_bufs[r];
+      a.out[r] = out_bufs[r];
+    }
+    if (saved_scales) {
+      g.add(saved, rows * hidden, 1);
+      g.add(saved_scales, rows * blocks_of(hidden) * 4, 4);
+    } else {
+      g.add(saved, bytes, es);
+    }
+    g.add(gamma, hidden * static_cast<size_t>(esize_of(gamma_dtype)), static_cast<size_t>(esize_of(gamma_dtype)));
+    g.add(rstd, rows * 4, 4);
+    g.add(residual_grad, bytes, es, false);
+    if (g.bad) return done(AR_ERR_INVALID);
+    if (!workspace || ws_bytes < need) return done(AR_ERR_WORKSPACE);
+    g.add(workspace, need, 256);
+  }
+  if (g.bad) return done(AR_ERR_INVALID);
+  if (any_overlap(g.r, g.m)) return done(AR_ERR_ALIAS);
+  a.residual = residual_grad;
+  a.gamma = gamma;
+  a.saved = saved;
+  a.saved_scales = saved_scales;
+  a.rstd_in = rstd;
+  a.partial = static_cast<float*>(workspace);
+  a.rows = static_cast<int64_t>(rows);
+  a.hidden = static_cast<int>(hidden);
+  a.n = nranks;
+  a.gamma_f32 = gamma_dtype == AR_F32;
+  const hipError_t e = ar::launch_rmsnorm_bwd(a, dtype, dgamma, static_cast<hipStream_t>(stream));
+  return done(e == hipSuccess ? AR_OK : AR_ERR_HIP);
+}
+
+int ar_expert_rows(size_t tokens, int k, int nexperts, int align, size_t* rows) {
+  auto done = [&](int st) { return finish("ar_expert_rows", 0, tokens, AR_I32, -1, -1, st); };
+  size_t r = 0;
+  if (!rows || !rows_fit(tokens, k, nexperts, align, &r)) return done(AR_ERR_INVALID);
+  *rows = r;
+  return done(AR_OK);
+}
+
+int ar_expert_sort_workspace_size(size_t tokens, int k, int nexperts, size_t* bytes) {
+  auto done = [&](int st) { return finish("ar_expert_sort_workspace_size", 0, tokens, AR_I32, -1, -1, st); };
+  size_t r = 0;
+  if (!bytes || !rows_fit(tokens, k, nexperts, 1, &r)) return done(AR_ERR_INVALID);
+  *bytes = static_cast<size_t>(ar::sort_workspace(static_cast<int64_t>(r), nexperts));
+  return done(AR_OK);
+}
+
+int ar_expert_sort(const int32_t* ids, size_t tokens, int k, int nexperts, int align, int32_t* offsets,
+                   int32_t* counts, int32_t* pos, int32_t* src, size_t rows, void* workspace, size_t ws_bytes,
+                   void* stream) {
+  auto done = [&](int st) { return finish("ar_expert_sort", 0, tokens, AR_I32, -1, -1, st); };
+  size_t most = 0;
+  if (!rows_fit(tokens, k, nexperts, align, &most) || rows < most || rows > INT32_MAX) return done(AR_ERR_INVALID);
+  const size_t slots = tokens * static_cast<size_t>(k);
+  const size_t need = static_cast<size_t>(ar::sort_workspace(static_cast<int64_t>(slots), nexperts));
+  Ranges g;
+  g.add(ids, slots * 4, 4, slots > 0);
+  g.add(offsets, (static_cast<size_t>(nexperts) + 1) * 4, 4);
+  g.add(counts, static_cast<size_t>(nexperts) * 4, 4);
+  g.add(pos, slots * 4, 4, slots > 0);
+  g.add(src, rows * 4, 4, rows > 0);
+  if (g.bad) return done(AR_ERR_INVALID);
+  if (need > 0) {
+    if (!workspace || ws_bytes < need) return done(AR_ERR_WORKSPACE);
+    g.add(workspace, need, 256);
+    if (g.bad) return done(AR_ERR_INVALID);
+  }
+  if (any_overlap(g.r, g.m)) return done(AR_ERR_ALIAS);
+  const ar::SortArgs a{ids, offsets, counts, pos, src, static_cast<int32_t*>(workspace), static_cast<int64_t>(slots),
+                       static_cast<int64_t>(rows), nexperts, align};
+  return done(ar::launch_expert_sort(a, static_cast<hipStream_t>(stream)) == hipSuccess ? AR_OK : AR_ERR_HIP);
+}
+
+int ar_expert_dispatch(const void* x, const float* x_scales, const int32_t* pos, const int32_t* offsets,
+                       const int32_t* counts, size_t tokens, int k, int nexperts, size_t hidden, int elem_size,
+                       void* xs, float* xs_scales, size_t rows, void* stream) {
+  auto done = [&](int st) { return finish("ar_expert_dispatch", 0, tokens, elem_size, -1, -1, st); };
+  size_t most = 0, xe = 0, xb = 0, ye = 0, yb = 0;
+  if (!rows_fit(tokens, k, nexperts, 1, &most) || hidden == 0 || rows > INT32_MAX) return done(AR_ERR_INVALID);
+  if (elem_size != 1 && elem_size != 2 && elem_size != 4) return done(AR_ERR_INVALID);
+  if ((x_scales == nullptr) != (xs_scales == nullptr) || (x_scales && elem_size != 1)) return done(AR_ERR_INVALID);
+  if ((offsets == nullptr) != (counts == nullptr)) return done(AR_ERR_INVALID);
+  const size_t es = static_cast<size_t>(elem_size), nb = blocks_of(hidden) * 4;
+  if (!mul(tokens, hidden, &xe) || !mul(xe, es, &xb) || !mul(rows, hidden, &ye) || !mul(ye, es, &yb))
+    return done(AR_ERR_INVALID);
+  if (tokens == 0) return done(AR_OK);
+  Ranges g;
+  g.add(x, xb, es);
+  g.add(x_scales, tokens * nb, 4, false);
+  g.add(pos, tokens * static_cast<size_t>(k) * 4, 4);
+  g.add(offsets, (static_cast<size_t>(nexperts) + 1) * 4, 4, false);
+  g.add(counts, static_cast<size_t>(nexperts) * 4, 4, false);
+  g.add(xs, yb, es, rows > 0);
+  g.add(xs_scales, rows * nb, 4, false);
+  if (g.bad) return done(AR_ERR_INVALID);
+  if (any_overlap(g.r, g.m)) return done(AR_ERR_ALIAS);
+  ar::MoveArgs a{};
+  a.x = x;
+  a.y = xs;
+  a.x_scales = x_scales;
+  a.y_scales = xs_scales;
+  a.pos = pos;
+  a.offsets = offsets;
+  a.counts = counts;
+  a.tokens = static_cast<int64_t>(tokens);
+  a.rows = static_cast<int64_t>(rows);
+  a.hidden = static_cast<int64_t>(hidden);
+  a.k = k;
+  a.experts = nexperts;
+  const hipError_t e = ar::launch_expert_dispatch(a, elem_size, static_cast<hipStream_t>(stream));
+  return done(e == hipSuccess ? AR_OK : AR_ERR_HIP);
+}
+
+int ar_expert_combine(const void* ys, const int32_t* pos, const float* weights, const void* addend, size_t tokens,
+                      int k, size_t hidden, int dtype, size_t rows, void* out, void* stream) {
+  auto done = [&](int st) { return finish("ar_expert_combine", 0, tokens, dtype, AR_SUM, -1, st); };
+  size_t most = 0, oe = 0, ob = 0, ye = 0, yb = 0;
+  if (!valid_dtype(dtype) || !rows_fit(tokens, k, 1, 1, &most) || hidden == 0 || rows > INT32_MAX)
+    return done(AR_ERR_INVALID);
+  if (dtype == AR_I32) return done(AR_ERR_UNSUPPORTED);
+  const size_t es = static_cast<size_t>(esize_of(dtype));
+  if (!mul(tokens, hidden, &oe) || !mul(oe, es, &ob) || !mul(rows, hidden, &ye) || !mul(ye, es, &yb))
+    return done(AR_ERR_INVALID);
+  if (tokens == 0) return done(AR_OK);
+  Ranges g;
+  g.add(ys, yb, es, rows > 0);
+  g.add(pos, tokens * static_cast<size_t>(k) * 4, 4);
+  g.add(weights, tokens * static_cast<size_t>(k) * 4, 4, false);
+  g.add(addend, ob, es, false);
+  if (!out) return done(AR_ERR_INVALID);
+  if (out != addend) g.add(out, ob, es);
+  if (g.bad) return done(AR_ERR_INVALID);
+  if (any_overlap(g.r, g.m)) return done(AR_ERR_ALIAS);
+  ar::MoveArgs a{};
+  a.x = ys;
+  a.y = out;
+  a.pos = pos;
+  a.weights = weights;
+  a.extra = addend;
+  a.tokens = static_cast<int64_t>(tokens);
+  a.rows = static_cast<int64_t>(rows);
+  a.hidden = static_cast<int64_t>(hidden);
+  a.k = k;
+  const hipError_t e = ar::launch_expert_combine(a, dtype, static_cast<hipStream_t>(stream));
+  return done(e == hipSuccess ? AR_OK : AR_ERR_HIP);
+}
+
+int ar_expert_combine_bwd(const void* dout, const void* ys, const int32_t* pos, const float* weights,
+                          const int32_t* offsets, const int32_t* counts, size_t tokens, int k, int nexperts,
+                          size_t hidden, int dtype, size_t rows, void* dys, float* dweights, void* stream) {
+  auto done = [&](int st) { return finish("ar_expert_combine_bwd", 0, tokens, dtype, AR_SUM, -1, st); };
+  size_t most = 0, oe = 0, ob = 0, ye = 0, yb = 0;
+  if (!valid_dtype(dtype) || !rows_fit(tokens, k, nexperts, 1, &most) || hidden == 0 || rows > INT32_MAX)
+    return done(AR_ERR_INVALID);
+  if (dtype == AR_I32) return done(AR_ERR_UNSUPPORTED);
+  if ((offsets == nullptr) != (counts == nullptr)) return done(AR_ERR_INVALID);
+  const size_t es = static_cast<size_t>(esize_of(dtype));
+  if (!mul(tokens, hidden, &oe) || !mul(oe, es, &ob) || !mul(rows, hidden, &ye) || !mul(ye, es, &yb))
+    return done(AR_ERR_INVALID);
+  if (tokens == 0) return done(AR_OK);
+  Ranges g;
+  g.add(dout, ob, es);
+  g.add(ys, yb, es, rows > 0);
+  g.add(pos, tokens * static_cast<size_t>(k) * 4, 4);
+  g.add(weights, tokens * static_cast<size_t>(k) * 4, 4);
+  g.add(offsets, (static_cast<size_t>(nexperts) + 1) * 4, 4, false);
+  g.add(counts, static_cast<size_t>(nexperts) * 4, 4, false);
+  if (dys != ys) g.add(dys, yb, es, rows > 0);
+  g.add(dweights, tokens * static_cast<size_t>(k) * 4, 4);
+  if (g.bad) return done(AR_ERR_INVALID);
+  if (any_overlap(g.r, g.m)) return done(AR_ERR_ALIAS);
+  ar::MoveArgs a{};
+  a.x = ys;
+  a.y = dys;
+  a.pos = pos;
+  a.weights = weights;
+  a.extra = dout;
+  a.dweights = dweights;
+  a.offsets = offsets;
+  a.counts = counts;
+  a.tokens = static_cast<int64_t>(tokens);
+  a.rows = static_cast<int64_t>(rows);
+  a.hidden = static_cast<int64_t>(hidden);
+  a.k = k;
+  a.experts = nexperts;
+  const hipError_t e = ar::launch_expert_combine_bwd(a, dtype, static_cast<hipStream_t>(stream));
   return done(e == hipSuccess ? AR_OK : AR_ERR_HIP);
 }
 

@@ -46,6 +46,8 @@ extern "C" {
 #define AR_VERSION 10000   /* major*10000 + minor*100 + patch */
 #define AR_MAX_RANKS 64
 #define AR_FP8_BLOCK 128   /* elements per E4M3 scaling block */
+#define AR_NORM_MAX_HIDDEN 32768 /* widest row of the norm entry points */
+#define AR_MAX_EXPERTS 1024
 
 enum ar_status {
     AR_OK = 0,
@@ -304,6 +306,94 @@ int ar_bucket_unpack(const ar_copy_desc* d_descs, int ndescs, int dtype, void* s
  * Errors: AR_ERR_INVALID (NULL, dtype), AR_ERR_HIP. count == 0 enqueues nothing. */
 int ar_fp8_quant(const void* in, int in_dtype, size_t count, uint8_t* codes, float* scales, void* stream);
 int ar_fp8_dequant(const uint8_t* codes, const float* scales, size_t count, void* out, int out_dtype, void* stream);
+
+/* ------------------------------------------------------------------------------------------------ */
+/* What stands next to the reduction in a transformer layer ([V] "All-Reduceは全rankの値を集約して全rankへ返す": the
+ * partial products of a tensor-parallel layer are summed over the ranks before the next layer reads them): the residual
+ * and the norm behind it, with the gradients, and the experts' rows before and after them. Matrices are row-major and
+ * dense: row t of a [rows][hidden] matrix starts t * hidden elements in. Any alignment that is a multiple of the
+ * element size. dtype: AR_F32, AR_BF16 or AR_F16. 8-bit rows are E4M3 codes uint8[rows][hidden] with scales
+ * float[rows][ceil(hidden / AR_FP8_BLOCK)]: the block rule of AR_ALGO_RING_FP8, with blocks that tile every row from
+ * its start. */
+
+/* All-reduce, residual and root-mean-square norm in one pass. With x_r the N rank buffers,
+ *   h = x_0 + x_1 + ... + x_{N-1} + residual   (fp32, in that order: the order of AR_ALGO_FUSED)
+ *   rstd = 1 / sqrt(mean over the row of h^2 + eps),   y = h * rstd * gamma
+ * y goes to every rank. Statistics and y are taken of h before it is rounded into dtype; y is rounded once. nranks 1 is
+ * the plain residual norm.
+ *   in_bufs: host array of nranks device pointers to [rows][hidden].   residual: [rows][hidden] or NULL.
+ *   gamma: [hidden] of gamma_dtype, which is dtype or AR_F32.          eps: finite, not negative.
+ *   out_bufs: host array of nranks device pointers. out_scales NULL: y as [rows][hidden] of dtype, and out_bufs[r] may
+ *     equal in_bufs[r]. Otherwise out_scales is a host array of nranks device pointers, and y leaves in 8 bits.
+ *   residual_out: h rounded into dtype, or NULL; may equal residual.   rstd: float[rows], or NULL.
+ *   saved, saved_scales: h in 8 bits, for ar_allreduce_rmsnorm_bwd; both or neither NULL.
+ * rows == 0 returns AR_OK and enqueues nothing.
+ * Errors: AR_ERR_INVALID (enum, nranks, NULL, eps, alignment, hidden 0, sizes past 2^62 bytes), AR_ERR_UNSUPPORTED
+ * (AR_I32; hidden above AR_NORM_MAX_HIDDEN), AR_ERR_ALIAS (any other overlap), AR_ERR_HIP. */
+int ar_allreduce_rmsnorm(const void* const* in_bufs, int nranks, size_t rows, size_t hidden, int dtype,
+                         const void* residual, const void* gamma, int gamma_dtype, float eps, void* const* out_bufs,
+                         float* const* out_scales, void* residual_out, float* rstd, uint8_t* saved,
+                         float* saved_scales, void* stream);
+
+/* The gradient of ar_allreduce_rmsnorm. With dy = dy_0 + ... + dy_{N-1} (the ranks' partial gradients of y, fp32, in
+ * rank order), h as saved and xhat = h * rstd:
+ *   g = dy * gamma,   dx = rstd * (g - xhat * mean over the row of g * xhat) + residual_grad
+ *   dgamma = sum over the rows of dy * xhat   (fp32; the order is fixed by rows and hidden alone)
+ * dx is the gradient of every x_r and of the residual; it goes to every rank.
+ *   in_bufs: host array of nranks device pointers to [rows][hidden], the dy_r.
+ *   saved: saved_scales NULL: h as [rows][hidden] of dtype (the forward's residual_out). Otherwise its 8-bit form.
+ *   rstd: float[rows], the forward's.      residual_grad: the gradient of residual_out, [rows][hidden], or NULL.
+ *   out_bufs: host array of nranks device pointers to [rows][hidden]; out_bufs[r] may equal in_bufs[r] or
+ *     residual_grad.      dgamma: float[hidden], overwritten.
+ *   workspace: ar_allreduce_rmsnorm_bwd_workspace_size() bytes, 256-byte aligned, disjoint from all else; clobbered.
+ * rows == 0 sets dgamma to zero. Errors as ar_allreduce_rmsnorm, and AR_ERR_WORKSPACE. */
+int ar_allreduce_rmsnorm_bwd_workspace_size(size_t rows, size_t hidden, size_t* bytes);
+int ar_allreduce_rmsnorm_bwd(const void* const* in_bufs, int nranks, size_t rows, size_t hidden, int dtype,
+                             const void* saved, const float* saved_scales, const void* gamma, int gamma_dtype,
+                             const float* rstd, const void* residual_grad, void* const* out_bufs, float* dgamma,
+                             void* workspace, size_t ws_bytes, void* stream);
+
+/* Tokens sorted by expert ([V] title and the All-to-All section: every token's row goes to the expert that its router
+ * chose). Slot q = t * k + j is choice j of token t. A slot whose id is in [0, nexperts) takes a row: the slots of one
+ * expert take consecutive rows in slot order, and every expert's segment starts on a multiple of align (the rows that a
+ * matrix product takes at a time). A slot with any other id (say -1: an expert elsewhere) takes none.
+ *   ids: int32[tokens][k].          offsets: int32[nexperts + 1], the first row of every segment and the end.
+ *   counts: int32[nexperts], the slots of every expert.       pos: int32[tokens][k], the slot's row or -1.
+ *   src: int32[rows], the row's slot or -1; rows at least ar_expert_rows(), the most rows that any ids take:
+ *     tokens * k + min(nexperts, tokens * k) * (align - 1).
+ *   workspace: ar_expert_sort_workspace_size() bytes, 256-byte aligned; NULL when that is 0 (small calls).
+ * Errors: AR_ERR_INVALID (NULL, alignment, nexperts outside 1..AR_MAX_EXPERTS, k or align below 1, more than
+ * 2^31 - 1 slots or rows, too few rows), AR_ERR_WORKSPACE, AR_ERR_ALIAS, AR_ERR_HIP. */
+int ar_expert_rows(size_t tokens, int k, int nexperts, int align, size_t* rows);
+int ar_expert_sort_workspace_size(size_t tokens, int k, int nexperts, size_t* bytes);
+int ar_expert_sort(const int32_t* ids, size_t tokens, int k, int nexperts, int align, int32_t* offsets,
+                   int32_t* counts, int32_t* pos, int32_t* src, size_t rows, void* workspace, size_t ws_bytes,
+                   void* stream);
+
+/* Rows into the experts' order: xs[pos[t][j]] = x[t]. The pad rows inside the segments are zeroed (offsets and counts
+ * as ar_expert_sort wrote them; both NULL where there are none). Rows from offsets[nexperts] on are not written.
+ *   x: [tokens][hidden] of elem_size bytes each (4, 2, or 1 for 8-bit rows).       xs: [rows][hidden].
+ *   x_scales, xs_scales: the scales of 8-bit rows, moved along with them; both or neither NULL, elem_size 1 only.
+ *   pos: int32[tokens][k]; an entry outside [0, rows) is a slot without a row. Two slots never share a row.
+ * Errors: AR_ERR_INVALID (NULL, alignment, sizes), AR_ERR_ALIAS (any overlap), AR_ERR_HIP. tokens == 0 enqueues
+ * nothing. */
+int ar_expert_dispatch(const void* x, const float* x_scales, const int32_t* pos, const int32_t* offsets,
+                       const int32_t* counts, size_t tokens, int k, int nexperts, size_t hidden, int elem_size,
+                       void* xs, float* xs_scales, size_t rows, void* stream);
+
+/* Rows back to their tokens: out[t] = sum over j in order of weights[t][j] * ys[pos[t][j]], + addend[t] (fp32, rounded
+ * once). A slot without a row adds nothing. weights float[tokens][k], or NULL for 1: then this is the gradient of
+ * ar_expert_dispatch. addend: [tokens][hidden] of dtype or NULL; out may equal addend. Other arguments and errors as
+ * ar_expert_dispatch; AR_ERR_UNSUPPORTED for AR_I32. */
+int ar_expert_combine(const void* ys, const int32_t* pos, const float* weights, const void* addend, size_t tokens,
+                      int k, size_t hidden, int dtype, size_t rows, void* out, void* stream);
+
+/* The gradient of ar_expert_combine: dys[pos[t][j]] = weights[t][j] * dout[t], pad rows zeroed as ar_expert_dispatch
+ * does it; dweights[t][j] = <dout[t], ys[pos[t][j]]> (fp32), 0 for a slot without a row. (The addend's gradient is
+ * dout.) dys may equal ys. */
+int ar_expert_combine_bwd(const void* dout, const void* ys, const int32_t* pos, const float* weights,
+                          const int32_t* offsets, const int32_t* counts, size_t tokens, int k, int nexperts,
+                          size_t hidden, int dtype, size_t rows, void* dys, float* dweights, void* stream);
 
 /* ------------------------------------------------------------------------------------------------ */
 /* Diagnostics ([V] "hangをtimeoutだけで再起動しない": keep the last collective entered, its sequence number,

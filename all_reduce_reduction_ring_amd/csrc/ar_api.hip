@@ -750,6 +750,7 @@ int ar_expert_dispatch(const void* x, const float* x_scales, const int32_t* pos,
   const size_t es = static_cast<size_t>(elem_size), nb = blocks_of(hidden) * 4;
   if (!mul(tokens, hidden, &xe) || !mul(xe, es, &xb) || !mul(rows, hidden, &ye) || !mul(ye, es, &yb))
     return done(AR_ERR_INVALID);
+  if (hidden > INT32_MAX / es) return done(AR_ERR_UNSUPPORTED);
   if (tokens == 0) return done(AR_OK);
   Ranges g;
   g.add(x, xb, es);
@@ -771,7 +772,7 @@ int ar_expert_dispatch(const void* x, const float* x_scales, const int32_t* pos,
   a.counts = counts;
   a.tokens = static_cast<int64_t>(tokens);
   a.rows = static_cast<int64_t>(rows);
-  a.hidden = static_cast<int64_t>(hidden);
+  a.hidden = static_cast<int>(hidden);
   a.k = k;
   a.experts = nexperts;
   const hipError_t e = ar::launch_expert_dispatch(a, elem_size, static_cast<hipStream_t>(stream));
@@ -788,6 +789,7 @@ int ar_expert_combine(const void* ys, const int32_t* pos, const float* weights, 
   const size_t es = static_cast<size_t>(esize_of(dtype));
   if (!mul(tokens, hidden, &oe) || !mul(oe, es, &ob) || !mul(rows, hidden, &ye) || !mul(ye, es, &yb))
     return done(AR_ERR_INVALID);
+  if (hidden > INT32_MAX / es) return done(AR_ERR_UNSUPPORTED);
   if (tokens == 0) return done(AR_OK);
   Ranges g;
   g.add(ys, yb, es, rows > 0);
@@ -806,7 +808,7 @@ int ar_expert_combine(const void* ys, const int32_t* pos, const float* weights, 
   a.extra = addend;
   a.tokens = static_cast<int64_t>(tokens);
   a.rows = static_cast<int64_t>(rows);
-  a.hidden = static_cast<int64_t>(hidden);
+  a.hidden = static_cast<int>(hidden);
   a.k = k;
   const hipError_t e = ar::launch_expert_combine(a, dtype, static_cast<hipStream_t>(stream));
   return done(e == hipSuccess ? AR_OK : AR_ERR_HIP);
@@ -824,6 +826,7 @@ int ar_expert_combine_bwd(const void* dout, const void* ys, const int32_t* pos, 
   const size_t es = static_cast<size_t>(esize_of(dtype));
   if (!mul(tokens, hidden, &oe) || !mul(oe, es, &ob) || !mul(rows, hidden, &ye) || !mul(ye, es, &yb))
     return done(AR_ERR_INVALID);
+  if (hidden > INT32_MAX / es) return done(AR_ERR_UNSUPPORTED);
   if (tokens == 0) return done(AR_OK);
   Ranges g;
   g.add(dout, ob, es);
@@ -847,7 +850,7 @@ int ar_expert_combine_bwd(const void* dout, const void* ys, const int32_t* pos, 
   a.counts = counts;
   a.tokens = static_cast<int64_t>(tokens);
   a.rows = static_cast<int64_t>(rows);
-  a.hidden = static_cast<int64_t>(hidden);
+  a.hidden = static_cast<int>(hidden);
   a.k = k;
   a.experts = nexperts;
   const hipError_t e = ar::launch_expert_combine_bwd(a, dtype, static_cast<hipStream_t>(stream));

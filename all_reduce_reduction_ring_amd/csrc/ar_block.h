@@ -63,7 +63,7 @@ struct MoveArgs {
   const int32_t* counts;
   int64_t tokens;
   int64_t rows;
-  int64_t hidden;
+  int hidden;              // rows are below 2^31 bytes
   int k;
   int experts;
 };
@@ -84,11 +84,94 @@ __device__ __forceinline__ u32x4 ldu16_nt(const void* p) { return __builtin_nont
 __device__ __forceinline__ void stu16(void* p, const u32x4& v) { *gptr<u32x4_a1>(p) = v; }
 __device__ __forceinline__ void stu16_nt(void* p, const u32x4& v) { __builtin_nontemporal_store(v, gptr<u32x4_a1>(p)); }
 
-// Sum over the 64 lanes of a wave, in every lane. All lanes must be active.
-__device__ __forceinline__ float wave_sum(float v) {
+// Rows are handled in vectors of V elements. The vector that would run past a row's end is read from the place of the
+// last whole one instead, so loads need no branch and stay together, and the values are moved down once they are fp32
+// (sums of such vectors too), with zeros behind them. For rows of at least V elements.
+template <int V> __device__ __forceinline__ uint32_t clamped(int e, int hidden) {
+  return static_cast<uint32_t>(e + V <= hidden ? e : hidden - V);
+}
+template <int V> __device__ __forceinline__ void drop_past_end(float* v, int e, int hidden) {
+  const int m = e + V - hidden;  // values that belong to elements before e
+  if (m <= 0) return;
 #pragma unroll
-  for (int m = 32; m > 0; m >>= 1) v += __shfl_xor(v, m, 64);
+  for (int d = V / 2; d > 0; d >>= 1) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = (m & d) ? (i + d < V ? v[i + d] : 0.0f) : v[i];
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) v[i] = m < V ? v[i] : 0.0f;
+}
+
+// 16 bytes at byte offset `at` of a row. The offset is hidden from the optimiser so that it stays a 32-bit register
+// next to the row's scalar address in every access (global addresses of the form base + 32-bit offset): worked out as
+// 64-bit addresses once for each of the many streams of a kernel, they took most of its registers.
+__device__ __forceinline__ uint32_t opaque(uint32_t v) {
+  asm volatile("" : "+v"(v));
   return v;
+}
+// The loads of v have returned when this is passed.
+__device__ __forceinline__ void arrived(u32x4& v) { asm volatile("" : "+v"(v)); }
+__device__ __forceinline__ u32x4 ld_row(const void* row, uint32_t at) {
+  return ldu16(static_cast<const char*>(row) + opaque(at));
+}
+__device__ __forceinline__ void st_row(void* row, uint32_t at, const u32x4& w) {
+  stu16_nt(static_cast<char*>(row) + opaque(at), w);
+}
+// The first n < 16 bytes of a vector, n a multiple of SIZE.
+template <int SIZE> __device__ __forceinline__ void st_row_part(void* row, uint32_t at, u32x4 w, int n) {
+  char* p = static_cast<char*>(row) + at;
+#pragma unroll 1
+  for (int i = 0; i < n; i += SIZE) {
+    if constexpr (SIZE == 4) {
+      *gptr<uint32_t>(p + i) = w[0];
+      w = u32x4{w[1], w[2], w[3], 0};
+    } else if constexpr (SIZE == 2) {
+      *gptr<uint16_t>(p + i) = static_cast<uint16_t>(w[0]);
+      w = u32x4{w[0] >> 16 | w[1] << 16, w[1] >> 16 | w[2] << 16, w[2] >> 16 | w[3] << 16, 0};
+    } else {
+      *gptr<uint8_t>(p + i) = static_cast<uint8_t>(w[0]);
+      w = u32x4{w[0] >> 8 | w[1] << 24, w[1] >> 8 | w[2] << 24, w[2] >> 8 | w[3] << 24, 0};
+    }
+  }
+}
+
+// Elements [e, e + kVec) of a row as stored, from the clamped place. EXACT: the vector that the row's end cuts element by
+// element, in its own place; for rows shorter than a vector, and where another lane may by then have written the
+// elements before e (results in place of what is read).
+template <int DT, bool EXACT> __device__ __forceinline__ u32x4 load_vec(const void* row, int e, int hidden) {
+  constexpr int V = Traits<DT>::kVec;
+  if constexpr (!EXACT) return ld_row(row, clamped<V>(e, hidden) * Traits<DT>::kSize);
+  if (e + V <= hidden) return ld_row(row, static_cast<uint32_t>(e) * Traits<DT>::kSize);
+  u32x4 w = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const uint32_t bits = e + i < hidden ? load_elem<DT>(row, e + i) : 0;
+    if constexpr (Traits<DT>::kSize == 2) w[i >> 1] |= bits << (16 * (i & 1));
+    else w[i % 4] = bits;
+  }
+  return w;
+}
+// Such a vector's values once they are fp32, moved where they belong.
+template <int DT, bool EXACT> __device__ __forceinline__ void settle_vec(float* v, int e, int hidden) {
+  if constexpr (!EXACT) drop_past_end<Traits<DT>::kVec>(v, e, hidden);
+}
+// Elements [e, e + kVec) to a row, as far as it goes.
+template <int DT> __device__ __forceinline__ void store_vec(void* row, int e, int hidden, const u32x4& w) {
+  constexpr int kSize = Traits<DT>::kSize;
+  if (e + Traits<DT>::kVec <= hidden) st_row(row, static_cast<uint32_t>(e) * kSize, w);
+  else if (e < hidden) st_row_part<kSize>(row, static_cast<uint32_t>(e) * kSize, w, (hidden - e) * kSize);
+}
+
+// Sum over the 64 lanes of a wave, the same in every lane; all lanes must be active. Four steps inside the 16-lane
+// rows, then the four rows through scalar registers: no LDS round trip.
+__device__ __forceinline__ float wave_sum(float v) {
+  auto step = [](float x, int y) { return x + __int_as_float(y); };
+  v = step(v, __builtin_amdgcn_update_dpp(0, __float_as_int(v), 0xB1, 0xF, 0xF, false));   // quad_perm [1,0,3,2]
+  v = step(v, __builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x4E, 0xF, 0xF, false));   // quad_perm [2,3,0,1]
+  v = step(v, __builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x141, 0xF, 0xF, false));  // row_half_mirror
+  v = step(v, __builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x140, 0xF, 0xF, false));  // row_mirror
+  auto row = [&](int l) { return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), l)); };
+  return (row(0) + row(16)) + (row(32) + row(48));
 }
 
 }  // namespace ar

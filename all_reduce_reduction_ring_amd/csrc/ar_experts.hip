@@ -18,6 +18,7 @@ namespace {
 constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
 constexpr int kMaxExperts = AR_MAX_EXPERTS;
+constexpr int kTileBatch = 8;             // histograms read together
 constexpr int64_t kOneGroupSlots = 8192;  // up to here one workgroup sorts everything in one launch
 
 // The lanes of the wave that hold the same expert as this one (0 for a lane whose slot goes nowhere). All lanes take
@@ -77,6 +78,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_hist_kernel(SortArgs a, int
 // histograms for itself, so the tiles need no order among each other.
 __global__ __launch_bounds__(kSortThreads) void sort_kernel(SortArgs a, int64_t tile) {
   __shared__ int next[kSortWaves][kMaxExperts];  // first the waves' counts, then the next row of (wave, expert)
+  __shared__ int part[2][kSortThreads];
   __shared__ int scan[kSortWaves];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   int bits = 0;
@@ -97,16 +99,36 @@ __global__ __launch_bounds__(kSortThreads) void sort_kernel(SortArgs a, int64_t 
   // thread e: its expert's slots in all tiles, in the tiles before this one, and the segment's start
   const int e = threadIdx.x;
   int total = 0, before = 0;
-  if (e < a.experts) {
-    if (a.hist) {
-      for (int64_t t = 0; t < gridDim.x; ++t) {
-        const int c = gptr<int32_t>(a.hist)[t * a.experts + e];
-        total += c;
-        if (t < blockIdx.x) before += c;
+  if (a.hist) {
+    // the tiles' histograms, an equal part of the tiles for each of the 1024 >> bits threads of an expert
+    const int x = threadIdx.x & ((1 << bits) - 1), tiles = static_cast<int>(gridDim.x);
+    if (x < a.experts) {
+      for (int t0 = threadIdx.x >> bits; t0 < tiles; t0 += kTileBatch * (kSortThreads >> bits)) {
+        int c[kTileBatch];
+#pragma unroll
+        for (int u = 0; u < kTileBatch; ++u) {
+          const int t = t0 + u * (kSortThreads >> bits);
+          c[u] = t < tiles ? gptr<int32_t>(a.hist)[static_cast<int64_t>(t) * a.experts + x] : 0;
+        }
+#pragma unroll
+        for (int u = 0; u < kTileBatch; ++u) {
+          total += c[u];
+          if (t0 + u * (kSortThreads >> bits) < static_cast<int>(blockIdx.x)) before += c[u];
+        }
       }
-    } else {
-      for (int w = 0; w < kSortWaves; ++w) total += next[w][e];
     }
+    part[0][threadIdx.x] = total;
+    part[1][threadIdx.x] = before;
+    __syncthreads();
+    total = before = 0;
+    if (e < a.experts) {
+      for (int i = e; i < kSortThreads; i += 1 << bits) {
+        total += part[0][i];
+        before += part[1][i];
+      }
+    }
+  } else if (e < a.experts) {
+    for (int w = 0; w < kSortWaves; ++w) total += next[w][e];
   }
   const int padded = (total + a.align - 1) / a.align * a.align;
   int rows = 0;
@@ -146,196 +168,256 @@ __global__ __launch_bounds__(kSortThreads) void sort_kernel(SortArgs a, int64_t 
 }
 
 // ------------------------------------------------------------------------------------------ rows
-constexpr int kThreads = 256;
+// A workgroup of LANES threads (64, 128 or 256) takes a token. What it knows about the token's rows is kept in scalar
+// registers: the rows' addresses and the tests whether they are there.
 constexpr int kChoices = 8;  // choices of a token handled together
 
-// The rows of choices j0 .. j0 + 7 (-1: none).
+// The rows of choices j0 .. j0 + 7 of token t (-1: none); in scalar registers. One load for all of them.
 __device__ __forceinline__ void load_rows(const MoveArgs& a, int64_t t, int j0, int (&p)[kChoices]) {
+  const int lane = threadIdx.x & 63;
+  int v = -1;
+  if (lane < kChoices && j0 + lane < a.k) v = gptr<int32_t>(a.pos + t * a.k)[j0 + lane];
+  v = v >= 0 && v < a.rows ? v : -1;
 #pragma unroll
-  for (int j = 0; j < kChoices; ++j) {
-    const int v = j0 + j < a.k ? gptr<int32_t>(a.pos)[t * a.k + j0 + j] : -1;
-    p[j] = v >= 0 && v < a.rows ? v : -1;
-  }
+  for (int j = 0; j < kChoices; ++j) p[j] = __builtin_amdgcn_readlane(v, j);
+}
+// Their weights, 0 where there is no row.
+__device__ __forceinline__ void load_weights(const MoveArgs& a, int64_t t, int j0, const int (&p)[kChoices],
+                                             float (&w)[kChoices]) {
+  const int lane = threadIdx.x & 63;
+  float v = 1.0f;
+  if (a.weights && lane < kChoices && j0 + lane < a.k) v = gptr<float>(a.weights + t * a.k)[j0 + lane];
+#pragma unroll
+  for (int j = 0; j < kChoices; ++j)
+    w[j] = p[j] >= 0 ? __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), j)) : 0.0f;
 }
 
-// Copy a row of `bytes` bytes (a multiple of the element size) to the rows p of `to`, by `lanes` lanes.
-__device__ __forceinline__ void spread_row(const char* from, char* to, int64_t bytes, const int (&p)[kChoices],
-                                           int lane, int lanes) {
-  for (int64_t b = lane * 16; b < bytes; b += lanes * 16) {
-    if (b + 16 <= bytes) {
-      const u32x4 v = ldu16(from + b);
-#pragma unroll
-      for (int j = 0; j < kChoices; ++j)
-        if (p[j] >= 0) stu16_nt(to + p[j] * bytes + b, v);
-    } else {
-      for (int64_t c = b; c < bytes; ++c) {
-        const uint8_t v = gptr<uint8_t>(from)[c];
-#pragma unroll
-        for (int j = 0; j < kChoices; ++j)
-          if (p[j] >= 0) gptr<uint8_t>(to)[p[j] * bytes + c] = v;
-      }
-    }
-  }
-}
-
-__device__ __forceinline__ void zero_bytes(char* to, int64_t bytes) {
-  for (int64_t b = threadIdx.x * 16; b < bytes; b += kThreads * 16) {
+__device__ __forceinline__ void zero_bytes(char* to, int64_t bytes, int64_t part, int64_t parts) {
+  const int64_t threads = blockDim.x;
+  for (int64_t b = (part * threads + threadIdx.x) * 16; b < bytes; b += parts * threads * 16) {
     if (b + 16 <= bytes) stu16_nt(to + b, u32x4{0, 0, 0, 0});
     else
       for (int64_t c = b; c < bytes; ++c) gptr<uint8_t>(to)[c] = 0;
   }
 }
 
-// The pad rows of expert e's segment, zeroed by one workgroup.
-__device__ __forceinline__ void zero_pads(const MoveArgs& a, int e, int64_t row_bytes, int64_t scale_bytes) {
+// The pad rows of one expert's segment, zeroed by `parts` workgroups.
+__device__ __forceinline__ void zero_pads(const MoveArgs& a, int group, int parts, int64_t row_bytes,
+                                          int64_t scale_bytes) {
+  const int e = group / parts, part = group % parts;
   int64_t lo = static_cast<int64_t>(gptr<int32_t>(a.offsets)[e]) + gptr<int32_t>(a.counts)[e];
   int64_t hi = gptr<int32_t>(a.offsets)[e + 1];
   if (lo < 0) lo = 0;
   if (hi > a.rows) hi = a.rows;
   if (lo >= hi) return;
-  zero_bytes(static_cast<char*>(a.y) + lo * row_bytes, (hi - lo) * row_bytes);
-  if (scale_bytes) zero_bytes(static_cast<char*>(a.y_scales) + lo * scale_bytes, (hi - lo) * scale_bytes);
+  zero_bytes(static_cast<char*>(a.y) + lo * row_bytes, (hi - lo) * row_bytes, part, parts);
+  if (scale_bytes)
+    zero_bytes(static_cast<char*>(a.y_scales) + lo * scale_bytes, (hi - lo) * scale_bytes, part, parts);
 }
 
-// LANES lanes take a token, tokens in steps of the token workgroups' number.
-template <int LANES> __device__ __forceinline__ int64_t first_token() {
-  return static_cast<int64_t>(blockIdx.x) * (kThreads / LANES) + threadIdx.x / LANES;
-}
-
-// Workgroups past the tokens' zero the experts' pad rows.
-template <int LANES>
-__global__ __launch_bounds__(kThreads) void dispatch_kernel(MoveArgs a, int64_t row_bytes, int64_t scale_bytes,
-                                                            int64_t token_groups) {
-  if (static_cast<int64_t>(blockIdx.x) >= token_groups) {
-    zero_pads(a, static_cast<int>(blockIdx.x - token_groups), row_bytes, scale_bytes);
+// The first pad_groups workgroups zero the experts' pad rows (first, so that none of them is left running alone at the
+// end), the others copy their tokens' rows. U 16-byte vectors a lane at a time. The last vector of a row is moved up to
+// end with it (its first bytes are then written twice, with the same values); rows below 16 bytes go byte by byte.
+constexpr int kCopyLanes = 128, kCopyUnroll = 4;
+__global__ __launch_bounds__(kCopyLanes) void dispatch_kernel(MoveArgs a, int row_bytes, int scale_bytes, int pad_groups,
+                                                              int pad_parts) {
+  constexpr int LANES = kCopyLanes, U = kCopyUnroll;
+  if (static_cast<int>(blockIdx.x) < pad_groups) {
+    zero_pads(a, static_cast<int>(blockIdx.x), pad_parts, row_bytes, scale_bytes);
     return;
   }
-  const int lane = threadIdx.x % LANES;
-  for (int64_t t = first_token<LANES>(); t < a.tokens; t += token_groups * (kThreads / LANES)) {
+  const int lane = threadIdx.x;
+  for (int64_t t = blockIdx.x - pad_groups; t < a.tokens; t += gridDim.x - pad_groups) {
+    const char* from = static_cast<const char*>(a.x) + t * row_bytes;
     for (int j0 = 0; j0 < a.k; j0 += kChoices) {
       int p[kChoices];
       load_rows(a, t, j0, p);
-      spread_row(static_cast<const char*>(a.x) + t * row_bytes, static_cast<char*>(a.y), row_bytes, p, lane, LANES);
-      if (scale_bytes)
-        spread_row(static_cast<const char*>(a.x_scales) + t * scale_bytes, static_cast<char*>(a.y_scales), scale_bytes,
-                   p, lane, LANES);
-    }
-  }
-}
-
-// A 16-byte vector of a row from element e on (zeros past its end), and its store.
-template <int DT>
-__device__ __forceinline__ void load_vec(const void* row, int64_t e, int64_t hidden, float (&v)[Traits<DT>::kVec]) {
-  if (e + Traits<DT>::kVec <= hidden) {
-    Slot<DT>::unpack(ldu16(static_cast<const char*>(row) + e * Traits<DT>::kSize), v);
-  } else {
+      if (row_bytes >= 16) {
+        for (int b0 = lane * 16; b0 < row_bytes; b0 += LANES * U * 16) {
+          u32x4 v[U];
+          uint32_t at[U];
 #pragma unroll
-    for (int i = 0; i < Traits<DT>::kVec; ++i) v[i] = e + i < hidden ? widen<DT>(load_elem<DT>(row, e + i)) : 0.0f;
-  }
-}
-template <int DT>
-__device__ __forceinline__ void store_vec(void* row, int64_t e, int64_t hidden, const float (&v)[Traits<DT>::kVec]) {
-  if (e + Traits<DT>::kVec <= hidden) {
-    stu16_nt(static_cast<char*>(row) + e * Traits<DT>::kSize, Slot<DT>::pack(v));
-  } else {
+          for (int u = 0; u < U; ++u) {
+            at[u] = clamped<16>(b0 + u * LANES * 16, row_bytes);
+            v[u] = ld_row(from, at[u]);
+          }
 #pragma unroll
-    for (int i = 0; i < Traits<DT>::kVec; ++i)
-      if (e + i < hidden) store_elem<DT>(row, e + i, narrow<DT>(v[i]));
-  }
-}
-
-// The sum runs in fp32 over the choices in order, the addend last, and is rounded once.
-template <int DT, int LANES>
-__global__ __launch_bounds__(kThreads) void combine_kernel(MoveArgs a) {
-  constexpr int V = Traits<DT>::kVec;
-  const int64_t row = a.hidden * Traits<DT>::kSize;
-  for (int64_t t = first_token<LANES>(); t < a.tokens; t += static_cast<int64_t>(gridDim.x) * (kThreads / LANES)) {
-    for (int64_t e = threadIdx.x % LANES * V; e < a.hidden; e += LANES * V) {
-      float acc[V];
+          for (int j = 0; j < kChoices; ++j) {
+            if (p[j] < 0) continue;
+            char* to = static_cast<char*>(a.y) + p[j] * static_cast<int64_t>(row_bytes);
 #pragma unroll
-      for (int i = 0; i < V; ++i) acc[i] = 0.0f;
-      for (int j0 = 0; j0 < a.k; j0 += kChoices) {
-        int p[kChoices];
-        load_rows(a, t, j0, p);
-        float v[kChoices][V];
+            for (int u = 0; u < U; ++u)
+              if (b0 + u * LANES * 16 < row_bytes) st_row(to, at[u], v[u]);
+          }
+        }
+      } else if (lane < row_bytes) {
+        const uint8_t v = gptr<uint8_t>(from)[lane];
 #pragma unroll
         for (int j = 0; j < kChoices; ++j)
-          if (p[j] >= 0) load_vec<DT>(static_cast<const char*>(a.x) + p[j] * row, e, a.hidden, v[j]);
-#pragma unroll
-        for (int j = 0; j < kChoices; ++j) {
-          if (p[j] < 0) continue;
-          const float w = a.weights ? gptr<float>(a.weights)[t * a.k + j0 + j] : 1.0f;
-#pragma unroll
-          for (int i = 0; i < V; ++i) acc[i] = fmaf(w, v[j][i], acc[i]);
-        }
+          if (p[j] >= 0) gptr<uint8_t>(static_cast<char*>(a.y) + p[j] * static_cast<int64_t>(row_bytes))[lane] = v;
       }
-      if (a.extra) {
-        float v[V];
-        load_vec<DT>(static_cast<const char*>(a.extra) + t * row, e, a.hidden, v);
+      for (int b = lane * 4; b < scale_bytes; b += LANES * 4) {
+        const uint32_t v = *gptr<uint32_t>(static_cast<const char*>(a.x_scales) + t * scale_bytes + opaque(b));
 #pragma unroll
-        for (int i = 0; i < V; ++i) acc[i] += v[i];
+        for (int j = 0; j < kChoices; ++j)
+          if (p[j] >= 0)
+            *gptr<uint32_t>(static_cast<char*>(a.y_scales) + p[j] * static_cast<int64_t>(scale_bytes) + opaque(b)) = v;
       }
-      store_vec<DT>(static_cast<char*>(a.y) + t * row, e, a.hidden, acc);
     }
   }
 }
 
-// LANES is 64 (a wave per token) or 256 (a workgroup per token, the waves' dot products joined in LDS).
-template <int DT, int LANES>
-__global__ __launch_bounds__(kThreads) void combine_bwd_kernel(MoveArgs a, int64_t token_groups) {
+// First element of the wave's part of a row, and this lane's offset from it. The loops over a row run on the wave's
+// first element, so that all lanes stay in them (load_rows reads lanes 0 to 7); lanes past the end read clamped places.
+template <int DT> __device__ __forceinline__ int wave_first() {
+  return __builtin_amdgcn_readfirstlane(threadIdx.x / 64) * 64 * Traits<DT>::kVec;
+}
+template <int DT> __device__ __forceinline__ int lane_elem() { return static_cast<int>(threadIdx.x & 63) * Traits<DT>::kVec; }
+
+// The sum runs in fp32 over the choices in order, the addend last, and is rounded once. A slot without a row adds
+// nothing: its row is not read. The rows of up to eight choices, U vectors of each, are on their way together.
+template <int DT, int LANES, int U, bool EXACT>
+__global__ __launch_bounds__(LANES) void combine_kernel(MoveArgs a) {
   constexpr int V = Traits<DT>::kVec;
-  __shared__ float lds[kThreads / 64][kChoices];
-  const int64_t row = a.hidden * Traits<DT>::kSize;
-  if (static_cast<int64_t>(blockIdx.x) >= token_groups) {
-    zero_pads(a, static_cast<int>(blockIdx.x - token_groups), row, 0);
-    return;
-  }
-  const int lane = threadIdx.x % LANES;
-  // whole waves take the loop together; with 256 lanes the whole workgroup
-  for (int64_t t = first_token<LANES>(); t < a.tokens; t += token_groups * (kThreads / LANES)) {
-    for (int j0 = 0; j0 < a.k; j0 += kChoices) {
-      int p[kChoices];
-      load_rows(a, t, j0, p);
-      float w[kChoices], dot[kChoices];
+  const int64_t row = static_cast<int64_t>(a.hidden) * Traits<DT>::kSize;
+  for (int64_t t = blockIdx.x; t < a.tokens; t += gridDim.x) {
+    int p[kChoices];
+    float w[kChoices];
+    load_rows(a, t, 0, p);
+    load_weights(a, t, 0, p, w);
+    for (int b0 = wave_first<DT>(); b0 < a.hidden; b0 += LANES * V * U) {
+      float acc[U][V];
+      u32x4 add[U];
 #pragma unroll
-      for (int j = 0; j < kChoices; ++j) {
-        w[j] = p[j] >= 0 ? gptr<float>(a.weights)[t * a.k + j0 + j] : 0.0f;
-        dot[j] = 0.0f;
+      for (int u = 0; u < U; ++u) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[u][i] = 0.0f;
+        if (a.extra && b0 + u * LANES * V < a.hidden)
+          add[u] = load_vec<DT, EXACT>(static_cast<const char*>(a.extra) + t * row, b0 + u * LANES * V + lane_elem<DT>(),
+                                       a.hidden);
       }
-      for (int64_t e = lane * V; e < a.hidden; e += LANES * V) {
-        float g[V];
-        load_vec<DT>(static_cast<const char*>(a.extra) + t * row, e, a.hidden, g);
+      for (int j0 = 0; j0 < a.k; j0 += kChoices) {
+        if (a.k > kChoices) {
+          load_rows(a, t, j0, p);
+          load_weights(a, t, j0, p, w);
+        }
+        u32x4 x[kChoices][U];
 #pragma unroll
         for (int j = 0; j < kChoices; ++j) {
           if (p[j] < 0) continue;
-          float v[V], d[V];
-          load_vec<DT>(static_cast<const char*>(a.x) + p[j] * row, e, a.hidden, v);
 #pragma unroll
-          for (int i = 0; i < V; ++i) {
-            dot[j] = fmaf(g[i], v[i], dot[j]);
-            d[i] = w[j] * g[i];
+          for (int u = 0; u < U; ++u)
+            if (b0 + u * LANES * V < a.hidden)
+              x[j][u] = load_vec<DT, EXACT>(static_cast<const char*>(a.x) + p[j] * row,
+                                            b0 + u * LANES * V + lane_elem<DT>(), a.hidden);
+        }
+#pragma unroll
+        for (int j = 0; j < kChoices; ++j) {
+          if (p[j] < 0) continue;
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            if (b0 + u * LANES * V >= a.hidden) continue;
+            float v[V];
+            Slot<DT>::unpack(x[j][u], v);
+#pragma unroll
+            for (int i = 0; i < V; ++i) acc[u][i] = fmaf(w[j], v[i], acc[u][i]);
           }
-          store_vec<DT>(static_cast<char*>(a.y) + p[j] * row, e, a.hidden, d);
         }
       }
 #pragma unroll
-      for (int j = 0; j < kChoices; ++j) dot[j] = wave_sum(dot[j]);
-      if constexpr (LANES == kThreads) {
-        __syncthreads();  // the sums of the step before are read
+      for (int u = 0; u < U; ++u) {
+        if (b0 + u * LANES * V >= a.hidden) continue;
+        const int e = b0 + u * LANES * V + lane_elem<DT>();
+        if (a.extra) {
+          float v[V];
+          Slot<DT>::unpack(add[u], v);
+#pragma unroll
+          for (int i = 0; i < V; ++i) acc[u][i] += v[i];
+        }
+        settle_vec<DT, EXACT>(acc[u], e, a.hidden);
+        store_vec<DT>(static_cast<char*>(a.y) + t * row, e, a.hidden, Slot<DT>::pack(acc[u]));
+      }
+    }
+  }
+}
+
+// The waves' dot products are joined in LDS. The first pad_groups workgroups zero the pad rows.
+template <int DT, int LANES, int U, bool EXACT>
+__global__ __launch_bounds__(LANES) void combine_bwd_kernel(MoveArgs a, int pad_groups, int pad_parts) {
+  constexpr int V = Traits<DT>::kVec;
+  constexpr int kWaves = LANES / 64;
+  __shared__ float lds[2][kWaves][kChoices];
+  const int64_t row = static_cast<int64_t>(a.hidden) * Traits<DT>::kSize;
+  if (static_cast<int>(blockIdx.x) < pad_groups) {
+    zero_pads(a, static_cast<int>(blockIdx.x), pad_parts, row, 0);
+    return;
+  }
+  int flip = 0;
+  for (int64_t t = blockIdx.x - pad_groups; t < a.tokens; t += gridDim.x - pad_groups) {
+    for (int j0 = 0; j0 < a.k; j0 += kChoices, flip ^= 1) {
+      int p[kChoices];
+      float w[kChoices], dot[kChoices];
+      load_rows(a, t, j0, p);
+      load_weights(a, t, j0, p, w);
+#pragma unroll
+      for (int j = 0; j < kChoices; ++j) dot[j] = 0.0f;
+      for (int b0 = wave_first<DT>(); b0 < a.hidden; b0 += LANES * V * U) {
+        u32x4 d[U], x[kChoices][U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (b0 + u * LANES * V < a.hidden)
+            d[u] = load_vec<DT, EXACT>(static_cast<const char*>(a.extra) + t * row, b0 + u * LANES * V + lane_elem<DT>(),
+                                       a.hidden);
+#pragma unroll
+        for (int j = 0; j < kChoices; ++j) {
+          if (p[j] < 0) continue;
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+            if (b0 + u * LANES * V < a.hidden)
+              x[j][u] = load_vec<DT, EXACT>(static_cast<const char*>(a.x) + p[j] * row,
+                                            b0 + u * LANES * V + lane_elem<DT>(), a.hidden);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (b0 + u * LANES * V >= a.hidden) continue;
+          const int e = b0 + u * LANES * V + lane_elem<DT>();
+          float dv[V];
+          Slot<DT>::unpack(d[u], dv);
+          settle_vec<DT, EXACT>(dv, e, a.hidden);
+#pragma unroll
+          for (int j = 0; j < kChoices; ++j) {
+            if (p[j] < 0) continue;
+            float v[V], y[V];
+            Slot<DT>::unpack(x[j][u], v);
+            settle_vec<DT, EXACT>(v, e, a.hidden);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+              dot[j] = fmaf(dv[i], v[i], dot[j]);
+              y[i] = w[j] * dv[i];
+            }
+            store_vec<DT>(static_cast<char*>(a.y) + p[j] * row, e, a.hidden, Slot<DT>::pack(y));
+          }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kChoices; ++j)
+        if (p[j] >= 0) dot[j] = wave_sum(dot[j]);
+      if constexpr (kWaves > 1) {
         if ((threadIdx.x & 63) == 0) {
 #pragma unroll
-          for (int j = 0; j < kChoices; ++j) lds[threadIdx.x >> 6][j] = dot[j];
+          for (int j = 0; j < kChoices; ++j) lds[flip][threadIdx.x >> 6][j] = dot[j];
         }
-        __syncthreads();
+        __syncthreads();  // one buffer is read while the next step fills the other
         if (threadIdx.x < kChoices && j0 + static_cast<int>(threadIdx.x) < a.k) {
           float sum = 0.0f;
-          for (int u = 0; u < kThreads / 64; ++u) sum += lds[u][threadIdx.x];
-          gptr<float>(a.dweights)[t * a.k + j0 + threadIdx.x] = sum;
+#pragma unroll
+          for (int u = 0; u < kWaves; ++u) sum += lds[flip][u][threadIdx.x];
+          gptr<float>(a.dweights + t * a.k)[j0 + threadIdx.x] = sum;
         }
-      } else if (lane == 0) {
+      } else if (threadIdx.x == 0) {
 #pragma unroll
         for (int j = 0; j < kChoices; ++j)
-          if (j0 + j < a.k) gptr<float>(a.dweights)[t * a.k + j0 + j] = dot[j];
+          if (j0 + j < a.k) gptr<float>(a.dweights + t * a.k)[j0 + j] = dot[j];
       }
     }
   }
@@ -348,30 +430,61 @@ int64_t sort_tile(int64_t slots) {
   return even <= 2048 ? 2048 : (even + kSortThreads - 1) / kSortThreads * kSortThreads;
 }
 
-// Lanes per token: a workgroup for rows of 128 vectors and more, a wave below, 16 lanes up to 16 vectors.
-int lanes_for(int64_t vectors) { return vectors >= 128 ? 256 : vectors > 16 ? 64 : 16; }
-int64_t groups_for(int64_t tokens, int lanes) {
-  const int64_t groups = (tokens + kThreads / lanes - 1) / (kThreads / lanes);
-  return groups < (1 << 22) ? groups : (1 << 22);  // a launch has fewer than 2^32 threads
+constexpr int kUnroll = 2;  // vectors of a row a lane takes at a time
+
+// Lanes per token: as many as have two vectors each, up to 256; with few tokens, twice as many.
+int lanes_for(int64_t vectors, int64_t tokens) {
+  if (tokens < 2048) vectors *= 2;
+  return vectors > 256 ? 256 : vectors > 128 ? 128 : 64;
+}
+// A launch has fewer than 2^32 threads.
+int64_t groups_for(int64_t tokens) { return tokens < (1 << 23) ? tokens : (1 << 23); }
+
+// Workgroups per expert that zero its pad rows: one for every 64 KiB that an expert's pads can have on average.
+int pad_parts(const MoveArgs& a, int64_t row_bytes) {
+  const int64_t spare = (a.rows - a.tokens * a.k) * row_bytes / a.experts >> 16;
+  return spare < 1 ? 1 : spare > 16 ? 16 : static_cast<int>(spare);
 }
 
+template <int DT, int LANES, int U, bool EXACT> hipError_t combine_run(const MoveArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL((combine_kernel<DT, LANES, U, EXACT>), dim3(static_cast<unsigned>(groups_for(a.tokens))),
+                     dim3(LANES), 0, s, a);
+  return hipGetLastError();
+}
 template <int DT> hipError_t combine_dt(const MoveArgs& a, hipStream_t s) {
-  const int lanes = lanes_for((a.hidden + Traits<DT>::kVec - 1) / Traits<DT>::kVec);
-  const dim3 grid(static_cast<unsigned>(groups_for(a.tokens, lanes))), block(kThreads);
-  if (lanes == 256) hipLaunchKernelGGL((combine_kernel<DT, 256>), grid, block, 0, s, a);
-  else if (lanes == 64) hipLaunchKernelGGL((combine_kernel<DT, 64>), grid, block, 0, s, a);
-  else hipLaunchKernelGGL((combine_kernel<DT, 16>), grid, block, 0, s, a);
-  return hipGetLastError();
+  constexpr int V = Traits<DT>::kVec;
+  if (a.hidden < V || (a.extra == a.y && a.hidden % V != 0)) return combine_run<DT, 64, 1, true>(a, s);
+  switch (lanes_for((a.hidden + V - 1) / V, a.tokens)) {
+    case 256: return combine_run<DT, 256, kUnroll, false>(a, s);
+    case 128: return combine_run<DT, 128, kUnroll, false>(a, s);
+    default:
+#ifdef EXP_S1
+    if (a.hidden <= 64 * V) return combine_run<DT, 64, 1, false>(a, s);
+#endif
+    return combine_run<DT, 64, kUnroll, false>(a, s);
+  }
 }
 
-template <int DT> hipError_t combine_bwd_dt(const MoveArgs& a, hipStream_t s) {
-  int lanes = lanes_for((a.hidden + Traits<DT>::kVec - 1) / Traits<DT>::kVec);
-  if (lanes < 64) lanes = 64;
-  const int64_t groups = groups_for(a.tokens, lanes);
-  const dim3 grid(static_cast<unsigned>(groups + (a.offsets ? a.experts : 0))), block(kThreads);
-  if (lanes == 256) hipLaunchKernelGGL((combine_bwd_kernel<DT, 256>), grid, block, 0, s, a, groups);
-  else hipLaunchKernelGGL((combine_bwd_kernel<DT, 64>), grid, block, 0, s, a, groups);
+template <int DT, int LANES, int U, bool EXACT> hipError_t combine_bwd_run(const MoveArgs& a, hipStream_t s) {
+  const int parts = pad_parts(a, static_cast<int64_t>(a.hidden) * Traits<DT>::kSize);
+  const int pads = a.offsets ? a.experts * parts : 0;
+  hipLaunchKernelGGL((combine_bwd_kernel<DT, LANES, U, EXACT>),
+                     dim3(static_cast<unsigned>(groups_for(a.tokens) + pads)), dim3(LANES), 0, s, a, pads, parts);
   return hipGetLastError();
+}
+template <int DT> hipError_t combine_bwd_dt(const MoveArgs& a, hipStream_t s) {
+  constexpr int V = Traits<DT>::kVec;
+  const int lanes = lanes_for((a.hidden + V - 1) / V, a.tokens);
+  if (a.hidden < V || (a.x == a.y && a.hidden % V != 0)) {  // the same lanes, so that dweights has the same bits
+    if (lanes == 256) return combine_bwd_run<DT, 256, 1, true>(a, s);
+    if (lanes == 128) return combine_bwd_run<DT, 128, 1, true>(a, s);
+    return combine_bwd_run<DT, 64, 1, true>(a, s);
+  }
+  switch (lanes) {
+    case 256: return combine_bwd_run<DT, 256, kUnroll, false>(a, s);
+    case 128: return combine_bwd_run<DT, 128, kUnroll, false>(a, s);
+    default: return combine_bwd_run<DT, 64, kUnroll, false>(a, s);
+  }
 }
 
 }  // namespace
@@ -400,14 +513,11 @@ hipError_t launch_expert_sort(const SortArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_expert_dispatch(const MoveArgs& a, int esize, hipStream_t s) {
-  const int64_t row = a.hidden * esize, scale = a.x_scales ? (a.hidden + AR_FP8_BLOCK - 1) / AR_FP8_BLOCK * 4 : 0;
-  const int lanes = lanes_for((row + 15) / 16);
-  const int64_t groups = groups_for(a.tokens, lanes);
-  const dim3 grid(static_cast<unsigned>(groups + (a.offsets ? a.experts : 0))), block(kThreads);
-  if (grid.x == 0) return hipSuccess;
-  if (lanes == 256) hipLaunchKernelGGL(dispatch_kernel<256>, grid, block, 0, s, a, row, scale, groups);
-  else if (lanes == 64) hipLaunchKernelGGL(dispatch_kernel<64>, grid, block, 0, s, a, row, scale, groups);
-  else hipLaunchKernelGGL(dispatch_kernel<16>, grid, block, 0, s, a, row, scale, groups);
+  const int row = a.hidden * esize, scale = a.x_scales ? (a.hidden + AR_FP8_BLOCK - 1) / AR_FP8_BLOCK * 4 : 0;
+  const int parts = pad_parts(a, row);
+  const int pads = a.offsets ? a.experts * parts : 0;
+  hipLaunchKernelGGL(dispatch_kernel, dim3(static_cast<unsigned>(groups_for(a.tokens) + pads)), dim3(kCopyLanes), 0, s,
+                     a, row, scale, pads, parts);
   return hipGetLastError();
 }
 

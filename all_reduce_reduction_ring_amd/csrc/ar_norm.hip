@@ -16,128 +16,155 @@
 namespace ar {
 namespace {
 
-// A lane's slot: 2-byte types, elements [8 i, 8 i + 8) for slot index i (one 16-byte access); fp32, elements
-// [128 b + 4 l, + 4) and the same + 64 for i = 16 b + l (two 16-byte accesses, each covering whole lines per wave).
+// A lane's slot of 8 elements is kVecs vectors: 2-byte types, elements [8 i, 8 i + 8) for slot index i; fp32, elements
+// [128 b + 4 l, + 4) and the same + 64 for i = 16 b + l, so that each access of a wave covers whole lines.
+template <int DT> constexpr int kVecs = Traits<DT>::kSize == 2 ? 1 : 2;
 template <int DT> __device__ __forceinline__ int first_of(int i) {
   if constexpr (Traits<DT>::kSize == 2) return i * 8;
   else return (i >> 4) * kBlock + (i & 15) * 4;
 }
-// Element k of the slot that starts at e0.
-template <int DT> __device__ __forceinline__ int elem_of(int e0, int k) {
-  if constexpr (Traits<DT>::kSize == 2) return e0 + k;
-  else return e0 + k + (k < 4 ? 0 : kBlock / 2 - 4);
-}
-template <int DT> __device__ __forceinline__ bool whole_slot(int e0, int hidden) {
-  return elem_of<DT>(e0, kPerLane - 1) < hidden;
-}
+// The first element of vector v of the slot that starts at e0.
+__device__ __forceinline__ int vec_at(int e0, int v) { return e0 + v * (kBlock / 2); }
 
-// The slot's 8 values of a row (zeros past its end).
-template <int DT>
-__device__ __forceinline__ void load8(const void* row, int e0, int hidden, float (&v)[kPerLane]) {
-  if (whole_slot<DT>(e0, hidden)) {
-    if constexpr (Traits<DT>::kSize == 2) {
-      Slot<DT>::unpack(ldu16(static_cast<const uint16_t*>(row) + e0), v);
-    } else {
-      const u32x4 a = ldu16(static_cast<const float*>(row) + e0);
-      const u32x4 b = ldu16(static_cast<const float*>(row) + e0 + kBlock / 2);
+template <int DT> struct Raw {
+  u32x4 w[kVecs<DT>];
+};
+
+// A slot of a row as stored, from the clamped places.
+template <int DT, bool EXACT> __device__ __forceinline__ Raw<DT> load_raw(const void* row, int e0, int hidden) {
+  Raw<DT> r;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        v[k] = __uint_as_float(a[k]);
-        v[k + 4] = __uint_as_float(b[k]);
-      }
-    }
+  for (int v = 0; v < kVecs<DT>; ++v) r.w[v] = load_vec<DT, EXACT>(row, vec_at(e0, v), hidden);
+  return r;
+}
+template <int DT> __device__ __forceinline__ void unpack_raw(const Raw<DT>& r, float (&v)[kPerLane]) {
+  if constexpr (kVecs<DT> == 1) {
+    Slot<DT>::unpack(r.w[0], v);
   } else {
 #pragma unroll
-    for (int k = 0; k < kPerLane; ++k) {
-      const int e = elem_of<DT>(e0, k);
-      v[k] = e < hidden ? widen<DT>(load_elem<DT>(row, e)) : 0.0f;
+    for (int k = 0; k < kPerLane; ++k) v[k] = __uint_as_float(r.w[k / 4][k % 4]);
+  }
+}
+// Values read from clamped places, moved where they belong.
+template <int DT, bool EXACT> __device__ __forceinline__ void settle(float (&v)[kPerLane], int e0, int hidden) {
+#pragma unroll
+  for (int i = 0; i < kVecs<DT>; ++i) settle_vec<DT, EXACT>(v + i * Traits<DT>::kVec, vec_at(e0, i), hidden);
+}
+
+template <int NR, typename F> __device__ __forceinline__ void each_rank(int n, F f) {
+  if constexpr (NR > 0) {
+#pragma unroll
+    for (int r = 0; r < NR; ++r) f(r);
+  } else {
+    for (int r = 0; r < n; ++r) f(r);
+  }
+}
+
+// A slot rounded into the type and stored to the row `to(r)` of every rank.
+template <int DT, int NR, typename F>
+__device__ __forceinline__ void store_slot(const float (&v)[kPerLane], int e0, int hidden, int n, F to) {
+  constexpr int V = Traits<DT>::kVec, kSize = Traits<DT>::kSize;
+#pragma unroll
+  for (int i = 0; i < kVecs<DT>; ++i) {
+    float x[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) x[k] = v[i * V + k];
+    const u32x4 w = Slot<DT>::pack(x);
+    const int e = vec_at(e0, i);
+    const uint32_t at = static_cast<uint32_t>(e) * kSize;
+    if (e + V <= hidden) each_rank<NR>(n, [&](int r) { st_row(to(r), at, w); });
+    else if (e < hidden) {
+#pragma unroll 1
+      for (int r = 0; r < n; ++r) st_row_part<kSize>(to(r), at, w, (hidden - e) * kSize);
     }
   }
 }
 
-template <int DT>
-__device__ __forceinline__ void store8(void* row, int e0, int hidden, const float (&v)[kPerLane]) {
-  if (whole_slot<DT>(e0, hidden)) {
-    if constexpr (Traits<DT>::kSize == 2) {
-      stu16_nt(static_cast<uint16_t*>(row) + e0, Slot<DT>::pack(v));
-    } else {
-      u32x4 a, b;
+// A slot's 8 codes, as two words (elements 0-3 and 4-7), to the row `to(r)` of every rank.
+template <int DT, int NR, typename F>
+__device__ __forceinline__ void store_codes(const uint32_t (&w)[2], int e0, int hidden, int n, F to) {
+  constexpr int V = Traits<DT>::kVec;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        a[k] = __float_as_uint(v[k]);
-        b[k] = __float_as_uint(v[k + 4]);
-      }
-      stu16_nt(static_cast<float*>(row) + e0, a);
-      stu16_nt(static_cast<float*>(row) + e0 + kBlock / 2, b);
-    }
-  } else {
-#pragma unroll
-    for (int k = 0; k < kPerLane; ++k) {
-      const int e = elem_of<DT>(e0, k);
-      if (e < hidden) store_elem<DT>(row, e, narrow<DT>(v[k]));
+  for (int i = 0; i < kVecs<DT>; ++i) {
+    const int e = vec_at(e0, i);
+    if (e + V <= hidden) {
+      each_rank<NR>(n, [&](int r) {
+        uint8_t* p = to(r) + opaque(e);
+        if constexpr (V == 8) __builtin_nontemporal_store(u32x2{w[0], w[1]}, gptr<u32x2_a1>(p));
+        else __builtin_nontemporal_store(w[i], gptr<u32_a1>(p));
+      });
+    } else if (e < hidden) {
+#pragma unroll 1
+      for (int r = 0; r < n; ++r) st_row_part<1>(to(r), e, u32x4{V == 8 ? w[0] : w[i], w[1], 0, 0}, hidden - e);
     }
   }
 }
 
-// The slot's 8 codes, as two words (elements 0-3 and 4-7).
-template <int DT>
-__device__ __forceinline__ void store_codes(uint8_t* row, int e0, int hidden, uint32_t w0, uint32_t w1) {
-  if (whole_slot<DT>(e0, hidden)) {
-    if constexpr (Traits<DT>::kSize == 2) {
-      __builtin_nontemporal_store(u32x2{w0, w1}, gptr<u32x2_a1>(row + e0));
-    } else {
-      __builtin_nontemporal_store(w0, gptr<u32_a1>(row + e0));
-      __builtin_nontemporal_store(w1, gptr<u32_a1>(row + e0 + kBlock / 2));
-    }
+struct RawCodes {
+  uint32_t w[2];
+  float scale;
+};
+template <int DT, bool EXACT>
+__device__ __forceinline__ RawCodes load_codes(const uint8_t* row, const float* scales, int e0, int hidden) {
+  constexpr int V = Traits<DT>::kVec;
+  RawCodes r{{0, 0}, 0.0f};
+  if constexpr (EXACT) {
+    for (int k = 0; k < V; ++k)
+      if (e0 + k < hidden) r.w[k >> 2] |= static_cast<uint32_t>(gptr<uint8_t>(row)[e0 + k]) << (8 * (k & 3));
+  } else if constexpr (V == 8) {
+    const u32x2 p = *gptr<u32x2_a1>(row + opaque(clamped<8>(e0, hidden)));
+    r.w[0] = p[0];
+    r.w[1] = p[1];
   } else {
-#pragma unroll
-    for (int k = 0; k < kPerLane; ++k) {
-      const int e = elem_of<DT>(e0, k);
-      if (e < hidden) gptr<uint8_t>(row)[e] = static_cast<uint8_t>((k < 4 ? w0 : w1) >> (8 * (k & 3)));
-    }
+    r.w[0] = *gptr<u32_a1>(row + opaque(clamped<4>(vec_at(e0, 0), hidden)));
+    r.w[1] = *gptr<u32_a1>(row + opaque(clamped<4>(vec_at(e0, 1), hidden)));
   }
+  r.scale = *gptr<float>(scales + opaque((e0 < hidden ? e0 : hidden - 1) / kBlock));
+  return r;
 }
-
-template <int DT>
-__device__ __forceinline__ void load_codes(const uint8_t* row, const float* scales, int e0, int hidden,
-                                           float (&v)[kPerLane]) {
-  uint32_t w[2] = {0, 0};
-  if (whole_slot<DT>(e0, hidden)) {
-    if constexpr (Traits<DT>::kSize == 2) {
-      const u32x2 p = *gptr<u32x2_a1>(row + e0);
-      w[0] = p[0];
-      w[1] = p[1];
-    } else {
-      w[0] = *gptr<u32_a1>(row + e0);
-      w[1] = *gptr<u32_a1>(row + e0 + kBlock / 2);
-    }
-  } else {
-#pragma unroll
-    for (int k = 0; k < kPerLane; ++k) {
-      const int e = elem_of<DT>(e0, k);
-      if (e < hidden) w[k >> 2] |= static_cast<uint32_t>(gptr<uint8_t>(row)[e]) << (8 * (k & 3));
-    }
-  }
-  const float sc = e0 < hidden ? gptr<float>(scales)[e0 / kBlock] : 0.0f;
+__device__ __forceinline__ void unpack_codes(const RawCodes& r, float (&v)[kPerLane]) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const f32x2 lo = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(w[i]), false);
-    const f32x2 hi = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(w[i]), true);
-    v[4 * i] = lo[0] * sc;
-    v[4 * i + 1] = lo[1] * sc;
-    v[4 * i + 2] = hi[0] * sc;
-    v[4 * i + 3] = hi[1] * sc;
+    const f32x2 lo = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(r.w[i]), false);
+    const f32x2 hi = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(r.w[i]), true);
+    v[4 * i] = lo[0] * r.scale;
+    v[4 * i + 1] = lo[1] * r.scale;
+    v[4 * i + 2] = hi[0] * r.scale;
+    v[4 * i + 3] = hi[1] * r.scale;
   }
 }
 
-template <int DT>
-__device__ __forceinline__ void load_gamma(const void* gamma, int f32, int e0, int hidden, float (&v)[kPerLane]) {
-  if (Traits<DT>::kSize == 2 && f32) {
+// A slot of gamma as stored (fp32 whatever the type, where gamma_f32 says so), and its values, zeros past the row's end.
+struct RawGamma {
+  u32x4 w[2];
+};
+template <int DT, bool EXACT> __device__ __forceinline__ RawGamma load_gamma(const NormArgs& a, int e0) {
+  RawGamma r;
+  if (Traits<DT>::kSize == 2 && a.gamma_f32) {
+    const uint32_t at = clamped<kPerLane>(e0, a.hidden) * 4;
+    if constexpr (EXACT) {
 #pragma unroll
-    for (int k = 0; k < kPerLane; ++k) v[k] = e0 + k < hidden ? gptr<float>(gamma)[e0 + k] : 0.0f;
+      for (int k = 0; k < kPerLane; ++k) r.w[k >> 2][k & 3] = e0 + k < a.hidden ? gptr<uint32_t>(a.gamma)[e0 + k] : 0;
+    } else {
+      r.w[0] = ld_row(a.gamma, at);
+      r.w[1] = ld_row(a.gamma, at + 16);
+    }
   } else {
-    load8<DT>(gamma, e0, hidden, v);
+    const Raw<DT> x = load_raw<DT, EXACT>(a.gamma, e0, a.hidden);
+#pragma unroll
+    for (int v = 0; v < kVecs<DT>; ++v) r.w[v] = x.w[v];
   }
+  return r;
+}
+template <int DT, bool EXACT>
+__device__ __forceinline__ void unpack_gamma(const NormArgs& a, const RawGamma& r, int e0, float (&v)[kPerLane]) {
+  if (Traits<DT>::kSize == 2 && !a.gamma_f32) {
+    Slot<Traits<DT>::kSize == 2 ? DT : AR_BF16>::unpack(r.w[0], v);
+  } else {
+#pragma unroll
+    for (int k = 0; k < kPerLane; ++k) v[k] = __uint_as_float(r.w[k / 4][k % 4]);
+  }
+  settle<DT, EXACT>(v, e0, a.hidden);
 }
 
 // Sum over the workgroup, in every thread; `lds` holds one float per wave and is free again two barriers later, so
@@ -154,203 +181,314 @@ __device__ __forceinline__ float group_sum(float v, float* lds) {
 }
 
 constexpr int kMaxThreads = 1024;
+constexpr int kRankBatch = 4;
 
-// The sum of the ranks' slot in rank order.
-template <int DT>
-__device__ __forceinline__ void sum_ranks(const NormArgs& a, int64_t at, int e0, float (&h)[kPerLane]) {
-  const int64_t off = at * Traits<DT>::kSize;
-  load8<DT>(static_cast<const char*>(a.in[0]) + off, e0, a.hidden, h);
-  for (int r = 1; r < a.n; ++r) {
-    float v[kPerLane];
-    load8<DT>(static_cast<const char*>(a.in[r]) + off, e0, a.hidden, v);
+// The ranks' slots of a row (NR: their number if known; otherwise `batch` of them from rank r0 on), and their sum in
+// rank order onto h.
+template <int DT, int NR, bool EXACT> struct RankSlots {
+  static constexpr int kBatch = NR > 0 ? NR : kRankBatch;
+  Raw<DT> raw[kBatch];
+  __device__ __forceinline__ void load(const NormArgs& a, int64_t off, int e0, int r0) {
 #pragma unroll
-    for (int k = 0; k < kPerLane; ++k) h[k] += v[k];
+    for (int r = 0; r < kBatch; ++r)
+      if (NR > 0 || r0 + r < a.n)
+        raw[r] = load_raw<DT, EXACT>(static_cast<const char*>(a.in[r0 + r]) + off, e0, a.hidden);
+  }
+  __device__ __forceinline__ void add(const NormArgs& a, int r0, float (&h)[kPerLane]) const {
+#pragma unroll
+    for (int r = 0; r < kBatch; ++r) {
+      if (NR > 0 || r0 + r < a.n) {
+        float v[kPerLane];
+        unpack_raw<DT>(raw[r], v);
+#pragma unroll
+        for (int k = 0; k < kPerLane; ++k) h[k] = r0 + r == 0 ? v[k] : h[k] + v[k];
+      }
+    }
+  }
+};
+
+// h = the sum of the ranks' slots, the first ones already on their way.
+template <int DT, int NR, bool EXACT>
+__device__ __forceinline__ void sum_ranks(const NormArgs& a, const RankSlots<DT, NR, EXACT>& first, int64_t off, int e0,
+                                          float (&h)[kPerLane]) {
+  first.add(a, 0, h);
+  if constexpr (NR == 0) {
+    for (int r0 = kRankBatch; r0 < a.n; r0 += kRankBatch) {
+      RankSlots<DT, NR, EXACT> more;
+      more.load(a, off, e0, r0);
+      more.add(a, r0, h);
+    }
   }
 }
 
 // One row's slot as codes: the scale per block by the codec's rule. All 64 lanes take part.
-template <int DT>
-__device__ __forceinline__ void quant8(const float (&v)[kPerLane], float* scale, uint32_t* w0, uint32_t* w1) {
+__device__ __forceinline__ void quant8(const float (&v)[kPerLane], float* scale, uint32_t (&w)[2]) {
   const BlockScale s = block_scale(v);
   float q[kPerLane], r[kPerLane];
 #pragma unroll
   for (int k = 0; k < kPerLane; ++k) q[k] = v[k] * s.inv;
-  e4m3_round4(q, r, w0);
-  e4m3_round4(q + 4, r + 4, w1);
-  *w0 = canonical_nan_codes(*w0);
-  *w1 = canonical_nan_codes(*w1);
+  e4m3_round4(q, r, &w[0]);
+  e4m3_round4(q + 4, r + 4, &w[1]);
+  w[0] = canonical_nan_codes(w[0]);
+  w[1] = canonical_nan_codes(w[1]);
   *scale = s.scale;
 }
 
-template <int DT, int S>
-__global__ __launch_bounds__(kMaxThreads) void rmsnorm_kernel(NormArgs a) {
-  __shared__ float lds[2][kMaxThreads / 64];
+#ifndef NORM_WPE
+#define NORM_WPE
+#endif
+#ifndef NORM_PF
+#define NORM_PF (S == 1 && NR == 1)
+#endif
+// One workgroup, one row.
+template <int DT, int S, int NR, bool EXACT>
+__global__ __launch_bounds__(kMaxThreads) void rmsnorm_kernel(NormArgs a, int64_t row0) {
+  __shared__ float lds[kMaxThreads / 64];
   constexpr int kSize = Traits<DT>::kSize;
-  const int nb = (a.hidden + kBlock - 1) / kBlock;
-  int flip = 0;
-  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, flip ^= 1) {
-    const int64_t at = row * a.hidden;
-    float h[S][kPerLane];
-    float ss = 0.0f;
+  const int nb = (a.hidden + kBlock - 1) / kBlock, threads = static_cast<int>(blockDim.x);
+  const int64_t row = row0 + blockIdx.x;
+  const int64_t at = row * a.hidden;
+  float h[S][kPerLane];
+  RawGamma gam[S];
+  float ss = 0.0f;
 #pragma unroll
-    for (int s = 0; s < S; ++s) {
-      const int e0 = first_of<DT>(s * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x));
-      sum_ranks<DT>(a, at, e0, h[s]);
-      if (a.residual) {
-        float v[kPerLane];
-        load8<DT>(static_cast<const char*>(a.residual) + at * kSize, e0, a.hidden, v);
+  for (int s = 0; s < S; ++s) gam[s] = load_gamma<DT, EXACT>(a, first_of<DT>(s * threads + static_cast<int>(threadIdx.x)));
 #pragma unroll
-        for (int k = 0; k < kPerLane; ++k) h[s][k] += v[k];
-      }
+  for (int s = 0; s < S; ++s) {
+    const int e0 = first_of<DT>(s * threads + static_cast<int>(threadIdx.x));
+    RankSlots<DT, NR, EXACT> first;
+    Raw<DT> res;
+    first.load(a, at * kSize, e0, 0);
+    if (a.residual) res = load_raw<DT, EXACT>(static_cast<const char*>(a.residual) + at * kSize, e0, a.hidden);
+    sum_ranks<DT, NR, EXACT>(a, first, at * kSize, e0, h[s]);
+    if (a.residual) {
+      float v[kPerLane];
+      unpack_raw<DT>(res, v);
 #pragma unroll
-      for (int k = 0; k < kPerLane; ++k) ss += h[s][k] * h[s][k];
+      for (int k = 0; k < kPerLane; ++k) h[s][k] += v[k];
     }
-    const float mean = group_sum(ss, lds[flip]) / static_cast<float>(a.hidden);
-    const float rstd = 1.0f / sqrtf(mean + a.eps);
-    if (a.rstd && threadIdx.x == 0) gptr<float>(a.rstd)[row] = rstd;
+    settle<DT, EXACT>(h[s], e0, a.hidden);
 #pragma unroll
-    for (int s = 0; s < S; ++s) {
-      const int i = s * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x);
-      const int e0 = first_of<DT>(i);
-      const bool block_lane = (i & 15) == 0 && e0 < a.hidden;
-      if (a.residual_out) store8<DT>(static_cast<char*>(a.residual_out) + at * kSize, e0, a.hidden, h[s]);
-      if (a.codes) {
-        float sc;
-        uint32_t w0, w1;
-        quant8<DT>(h[s], &sc, &w0, &w1);
-        store_codes<DT>(a.codes + at, e0, a.hidden, w0, w1);
-        if (block_lane) gptr<float>(a.scales)[row * nb + (i >> 4)] = sc;
-      }
-      float y[kPerLane];
-      load_gamma<DT>(a.gamma, a.gamma_f32, e0, a.hidden, y);
+    for (int k = 0; k < kPerLane; ++k) ss += h[s][k] * h[s][k];
+  }
+  const float mean = group_sum(ss, lds) / static_cast<float>(a.hidden);
+  const float rstd = 1.0f / sqrtf(mean + a.eps);
+  if (a.rstd && threadIdx.x == 0) gptr<float>(a.rstd)[row] = rstd;
 #pragma unroll
-      for (int k = 0; k < kPerLane; ++k) y[k] = h[s][k] * rstd * y[k];
-      if (a.out8) {
-        float sc;
-        uint32_t w0, w1;
-        quant8<DT>(y, &sc, &w0, &w1);
-        for (int r = 0; r < a.n; ++r) {
-          store_codes<DT>(static_cast<uint8_t*>(a.out[r]) + at, e0, a.hidden, w0, w1);
-          if (block_lane) gptr<float>(a.out_scales[r])[row * nb + (i >> 4)] = sc;
-        }
-      } else {
-        for (int r = 0; r < a.n; ++r) store8<DT>(static_cast<char*>(a.out[r]) + at * kSize, e0, a.hidden, y);
-      }
+  for (int s = 0; s < S; ++s) {
+    const int i = s * threads + static_cast<int>(threadIdx.x);
+    const int e0 = first_of<DT>(i);
+    const bool block_lane = (i & 15) == 0 && e0 < a.hidden;
+    if (a.residual_out)
+      store_slot<DT, 1>(h[s], e0, a.hidden, 1, [&](int) { return static_cast<char*>(a.residual_out) + at * kSize; });
+    if (a.codes) {
+      float sc;
+      uint32_t w[2];
+      quant8(h[s], &sc, w);
+      store_codes<DT, 1>(w, e0, a.hidden, 1, [&](int) { return a.codes + at; });
+      if (block_lane) gptr<float>(a.scales + row * nb)[i >> 4] = sc;
+    }
+    float y[kPerLane];
+    unpack_gamma<DT, EXACT>(a, gam[s], e0, y);
+#pragma unroll
+    for (int k = 0; k < kPerLane; ++k) y[k] = h[s][k] * rstd * y[k];
+    if (a.out8) {
+      float sc;
+      uint32_t w[2];
+      quant8(y, &sc, w);
+      store_codes<DT, NR>(w, e0, a.hidden, a.n, [&](int r) { return static_cast<uint8_t*>(a.out[r]) + at; });
+      if (block_lane) each_rank<NR>(a.n, [&](int r) { *gptr<float>(a.out_scales[r] + row * nb + opaque(i >> 4)) = sc; });
+    } else {
+      store_slot<DT, NR>(y, e0, a.hidden, a.n, [&](int r) { return static_cast<char*>(a.out[r]) + at * kSize; });
     }
   }
 }
 
+// What a lane reads of one slot of a row in the backward pass.
+template <int DT, int NR, bool EXACT> struct BwdSlot {
+  RankSlots<DT, NR, EXACT> first;
+  Raw<DT> saved, res;
+  RawCodes codes;
+  __device__ __forceinline__ void load(const NormArgs& a, int64_t row, int e0) {
+    constexpr int kSize = Traits<DT>::kSize;
+    const int64_t at = row * a.hidden;
+    first.load(a, at * kSize, e0, 0);
+    if (a.saved_scales)
+      codes = load_codes<DT, EXACT>(static_cast<const uint8_t*>(a.saved) + at,
+                                    a.saved_scales + row * ((a.hidden + kBlock - 1) / kBlock), e0, a.hidden);
+    else
+      saved = load_raw<DT, EXACT>(static_cast<const char*>(a.saved) + at * kSize, e0, a.hidden);
+    if (a.residual) res = load_raw<DT, EXACT>(static_cast<const char*>(a.residual) + at * kSize, e0, a.hidden);
+  }
+};
+
 // A workgroup takes rows blockIdx, blockIdx + groups, ...; its threads keep their columns' sums of dy xhat in
 // registers over all of them and leave one row of partial sums behind, which dgamma_kernel adds up in order.
-template <int DT, int S>
-__global__ __launch_bounds__(kMaxThreads) void rmsnorm_bwd_kernel(NormArgs a) {
+template <int DT, int S, int NR, bool EXACT>
+__global__ __launch_bounds__(kMaxThreads) NORM_WPE void rmsnorm_bwd_kernel(NormArgs a) {
   __shared__ float lds[2][kMaxThreads / 64];
   constexpr int kSize = Traits<DT>::kSize;
-  const int nb = (a.hidden + kBlock - 1) / kBlock;
+  constexpr bool kAhead = NORM_PF;
+  const int threads = static_cast<int>(blockDim.x);
   float dg[S][kPerLane];
+  RawGamma gam[S];
 #pragma unroll
-  for (int s = 0; s < S; ++s)
+  for (int s = 0; s < S; ++s) {
+    if (S < 4) gam[s] = load_gamma<DT, EXACT>(a, first_of<DT>(s * threads + static_cast<int>(threadIdx.x)));
 #pragma unroll
     for (int k = 0; k < kPerLane; ++k) dg[s][k] = 0.0f;
+  }
   int flip = 0;
+  BwdSlot<DT, NR, EXACT> next;
+  float rstd_next = 0.0f;
+  if (kAhead) {
+    next.load(a, blockIdx.x, first_of<DT>(static_cast<int>(threadIdx.x)));
+    rstd_next = gptr<float>(a.rstd_in)[blockIdx.x];
+  }
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, flip ^= 1) {
     const int64_t at = row * a.hidden;
-    const float rstd = gptr<float>(a.rstd_in)[row];
+    const float rstd = kAhead ? rstd_next : gptr<float>(a.rstd_in)[row];
     float g[S][kPerLane], xh[S][kPerLane];
+    Raw<DT> res[S];
     float dot = 0.0f;
 #pragma unroll
     for (int s = 0; s < S; ++s) {
-      const int e0 = first_of<DT>(s * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x));
-      sum_ranks<DT>(a, at, e0, g[s]);
-      if (a.saved_scales) load_codes<DT>(static_cast<const uint8_t*>(a.saved) + at, a.saved_scales + row * nb, e0, a.hidden, xh[s]);
-      else load8<DT>(static_cast<const char*>(a.saved) + at * kSize, e0, a.hidden, xh[s]);
-      float gam[kPerLane];
-      load_gamma<DT>(a.gamma, a.gamma_f32, e0, a.hidden, gam);
+      const int e0 = first_of<DT>(s * threads + static_cast<int>(threadIdx.x));
+      BwdSlot<DT, NR, EXACT> x;
+      if (kAhead) x = next;
+      else x.load(a, row, e0);
+      sum_ranks<DT, NR, EXACT>(a, x.first, at * kSize, e0, g[s]);
+      settle<DT, EXACT>(g[s], e0, a.hidden);
+      if (a.saved_scales) unpack_codes(x.codes, xh[s]);
+      else unpack_raw<DT>(x.saved, xh[s]);
+      settle<DT, EXACT>(xh[s], e0, a.hidden);
+      res[s] = x.res;
+      float y[kPerLane];
+      unpack_gamma<DT, EXACT>(a, S < 4 ? gam[s] : load_gamma<DT, EXACT>(a, e0), e0, y);
 #pragma unroll
       for (int k = 0; k < kPerLane; ++k) {
         xh[s][k] *= rstd;
         dg[s][k] += g[s][k] * xh[s][k];
-        g[s][k] *= gam[k];
+        g[s][k] *= y[k];
         dot += g[s][k] * xh[s][k];
       }
+    }
+    if (kAhead && row + gridDim.x < a.rows) {
+      next.load(a, row + gridDim.x, first_of<DT>(static_cast<int>(threadIdx.x)));
+      rstd_next = gptr<float>(a.rstd_in)[row + gridDim.x];
+    }
+    // The clamped vectors reach into other lanes' elements, which are overwritten behind group_sum where a result goes
+    // in place. All else has been used by then; the residual's gradient has to have arrived.
+    if (a.residual) {
+#pragma unroll
+      for (int s = 0; s < S; ++s)
+#pragma unroll
+        for (int v = 0; v < kVecs<DT>; ++v) arrived(res[s].w[v]);
     }
     const float mean = group_sum(dot, lds[flip]) / static_cast<float>(a.hidden);
 #pragma unroll
     for (int s = 0; s < S; ++s) {
-      const int e0 = first_of<DT>(s * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x));
+      const int e0 = first_of<DT>(s * threads + static_cast<int>(threadIdx.x));
 #pragma unroll
       for (int k = 0; k < kPerLane; ++k) g[s][k] = rstd * (g[s][k] - xh[s][k] * mean);
       if (a.residual) {
         float v[kPerLane];
-        load8<DT>(static_cast<const char*>(a.residual) + at * kSize, e0, a.hidden, v);
+        unpack_raw<DT>(res[s], v);
+        settle<DT, EXACT>(v, e0, a.hidden);
 #pragma unroll
         for (int k = 0; k < kPerLane; ++k) g[s][k] += v[k];
       }
-      for (int r = 0; r < a.n; ++r) store8<DT>(static_cast<char*>(a.out[r]) + at * kSize, e0, a.hidden, g[s]);
+      store_slot<DT, NR>(g[s], e0, a.hidden, a.n, [&](int r) { return static_cast<char*>(a.out[r]) + at * kSize; });
     }
   }
+  float* to = a.partial + static_cast<int64_t>(blockIdx.x) * a.hidden;
 #pragma unroll
   for (int s = 0; s < S; ++s) {
-    const int e0 = first_of<DT>(s * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x));
+    const int e0 = first_of<DT>(s * threads + static_cast<int>(threadIdx.x));
 #pragma unroll
     for (int k = 0; k < kPerLane; ++k) {
-      const int e = elem_of<DT>(e0, k);
-      if (e < a.hidden) gptr<float>(a.partial)[static_cast<int64_t>(blockIdx.x) * a.hidden + e] = dg[s][k];
+      const int e = vec_at(e0, k / Traits<DT>::kVec) + k % Traits<DT>::kVec;
+      if (e < a.hidden) gptr<float>(to)[e] = dg[s][k];
     }
   }
 }
 
-// dgamma[c] = the sum over the groups' partial sums of column c: 32 columns a workgroup, 32 threads to a column.
+// dgamma[c] = the sum over the groups' partial sums of column c: 16 columns a workgroup, 64 threads to a column.
+constexpr int kSumColumns = 16, kSumParts = 1024 / kSumColumns, kSumBatch = 8;
 __global__ __launch_bounds__(1024) void dgamma_kernel(const float* partial, int64_t groups, int hidden, float* dgamma) {
-  __shared__ float lds[32][33];
-  const int col = blockIdx.x * 32 + (threadIdx.x & 31), part = threadIdx.x >> 5;
+  __shared__ float lds[kSumParts][kSumColumns + 1];
+  const int c = threadIdx.x % kSumColumns, part = threadIdx.x / kSumColumns;
+  const int col = blockIdx.x * kSumColumns + c;
   float t = 0.0f;
-  if (col < hidden)
-    for (int64_t g = part; g < groups; g += 32) t += gptr<float>(partial)[g * hidden + col];
-  lds[part][threadIdx.x & 31] = t;
+  if (col < hidden) {
+    for (int64_t g0 = part; g0 < groups; g0 += kSumBatch * kSumParts) {
+      float x[kSumBatch];
+#pragma unroll
+      for (int u = 0; u < kSumBatch; ++u) {
+        const int64_t g = g0 + u * kSumParts;
+        x[u] = g < groups ? gptr<float>(partial)[g * hidden + col] : 0.0f;
+      }
+#pragma unroll
+      for (int u = 0; u < kSumBatch; ++u) t += x[u];
+    }
+  }
+  lds[part][c] = t;
   __syncthreads();
   if (part == 0 && col < hidden) {
     float sum = 0.0f;
-    for (int p = 0; p < 32; ++p) sum += lds[p][threadIdx.x];
+#pragma unroll 8
+    for (int p = 0; p < kSumParts; ++p) sum += lds[p][c];
     gptr<float>(dgamma)[col] = sum;
   }
 }
 
-// Threads and slots per thread for a row of `hidden` elements: one slot of 8 while 256 threads cover the row, then
-// 2 and 4 slots, then more threads.
+// Threads and slots per thread for a row of `hidden` elements: one slot of 8 a lane, two or four only where 1024
+// threads do not cover the row.
 struct Shape {
   int threads, slots;
 };
 Shape shape_of(int hidden) {
   const int slots = (hidden + kBlock - 1) / kBlock * 16;  // whole blocks: 16 lanes each
-  int per = slots > 512 ? 4 : slots > 256 ? 2 : 1;
-  int threads = (slots + per - 1) / per;
-  threads = (threads + 63) / 64 * 64;
-  return Shape{threads, per};
+  const int per = slots <= kMaxThreads ? 1 : slots <= 2 * kMaxThreads ? 2 : 4;
+  return Shape{((slots + per - 1) / per + 63) / 64 * 64, per};
 }
 
 constexpr int64_t kMaxGroups = 1024;
 
-template <int DT> hipError_t launch_fwd(const NormArgs& a, hipStream_t s) {
-  const Shape sh = shape_of(a.hidden);
-  const dim3 grid(static_cast<unsigned>(a.rows < (1 << 20) ? a.rows : (1 << 20))), block(sh.threads);
-  switch (sh.slots) {
-    case 1: hipLaunchKernelGGL((rmsnorm_kernel<DT, 1>), grid, block, 0, s, a); break;
-    case 2: hipLaunchKernelGGL((rmsnorm_kernel<DT, 2>), grid, block, 0, s, a); break;
-    default: hipLaunchKernelGGL((rmsnorm_kernel<DT, 4>), grid, block, 0, s, a); break;
+constexpr int64_t kMaxGrid = 1 << 21;  // a launch has fewer than 2^32 threads
+
+template <int DT, int S, int NR, bool EXACT>
+hipError_t run(const NormArgs& a, bool bwd, int64_t groups, int threads, hipStream_t s) {
+  if (bwd) {
+    hipLaunchKernelGGL((rmsnorm_bwd_kernel<DT, S, NR, EXACT>), dim3(static_cast<unsigned>(groups)), dim3(threads), 0, s, a);
+    return hipGetLastError();
   }
-  return hipGetLastError();
+  for (int64_t row = 0; row < a.rows; row += kMaxGrid) {
+    const int64_t rows = a.rows - row < kMaxGrid ? a.rows - row : kMaxGrid;
+    hipLaunchKernelGGL((rmsnorm_kernel<DT, S, NR, EXACT>), dim3(static_cast<unsigned>(rows)), dim3(threads), 0, s, a, row);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+template <int DT, int S>
+hipError_t run_n(const NormArgs& a, bool bwd, int64_t groups, int threads, hipStream_t s) {
+  switch (a.n) {
+    case 1: return run<DT, S, 1, false>(a, bwd, groups, threads, s);
+    case 2: return run<DT, S, 2, false>(a, bwd, groups, threads, s);
+    case 3: return run<DT, S, 3, false>(a, bwd, groups, threads, s);
+    case 4: return run<DT, S, 4, false>(a, bwd, groups, threads, s);
+    case 8: return run<DT, S, 8, false>(a, bwd, groups, threads, s);
+    default: return run<DT, S, 0, false>(a, bwd, groups, threads, s);
+  }
 }
 
-template <int DT> hipError_t launch_bwd(const NormArgs& a, int64_t groups, hipStream_t s) {
+template <int DT> hipError_t launch(const NormArgs& a, bool bwd, int64_t groups, hipStream_t s) {
+  if (a.hidden < Traits<DT>::kVec) return run<DT, 1, 0, true>(a, bwd, groups, 64, s);
   const Shape sh = shape_of(a.hidden);
-  const dim3 grid(static_cast<unsigned>(groups)), block(sh.threads);
-  switch (sh.slots) {
-    case 1: hipLaunchKernelGGL((rmsnorm_bwd_kernel<DT, 1>), grid, block, 0, s, a); break;
-    case 2: hipLaunchKernelGGL((rmsnorm_bwd_kernel<DT, 2>), grid, block, 0, s, a); break;
-    default: hipLaunchKernelGGL((rmsnorm_bwd_kernel<DT, 4>), grid, block, 0, s, a); break;
-  }
-  return hipGetLastError();
+  if (sh.slots == 1) return run_n<DT, 1>(a, bwd, groups, sh.threads, s);
+  if (sh.slots == 2) return run_n<DT, 2>(a, bwd, groups, sh.threads, s);
+  return run_n<DT, 4>(a, bwd, groups, sh.threads, s);
 }
 
 }  // namespace
@@ -359,9 +497,9 @@ int64_t rmsnorm_bwd_groups(int64_t rows, int64_t) { return rows < kMaxGroups ? r
 
 hipError_t launch_rmsnorm(const NormArgs& a, int dtype, hipStream_t s) {
   switch (dtype) {
-    case AR_F32: return launch_fwd<AR_F32>(a, s);
-    case AR_BF16: return launch_fwd<AR_BF16>(a, s);
-    case AR_F16: return launch_fwd<AR_F16>(a, s);
+    case AR_F32: return launch<AR_F32>(a, false, 0, s);
+    case AR_BF16: return launch<AR_BF16>(a, false, 0, s);
+    case AR_F16: return launch<AR_F16>(a, false, 0, s);
     default: return hipErrorInvalidValue;
   }
 }
@@ -371,14 +509,14 @@ hipError_t launch_rmsnorm_bwd(const NormArgs& a, int dtype, float* dgamma, hipSt
   hipError_t e = hipSuccess;
   if (groups > 0) {
     switch (dtype) {
-      case AR_F32: e = launch_bwd<AR_F32>(a, groups, s); break;
-      case AR_BF16: e = launch_bwd<AR_BF16>(a, groups, s); break;
-      case AR_F16: e = launch_bwd<AR_F16>(a, groups, s); break;
+      case AR_F32: e = launch<AR_F32>(a, true, groups, s); break;
+      case AR_BF16: e = launch<AR_BF16>(a, true, groups, s); break;
+      case AR_F16: e = launch<AR_F16>(a, true, groups, s); break;
       default: return hipErrorInvalidValue;
     }
   }
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(dgamma_kernel, dim3((a.hidden + 31) / 32), dim3(1024), 0, s, a.partial, groups, a.hidden, dgamma);
+  hipLaunchKernelGGL(dgamma_kernel, dim3((a.hidden + kSumColumns - 1) / kSumColumns), dim3(1024), 0, s, a.partial, groups, a.hidden, dgamma);
   return hipGetLastError();
 }
 

@@ -637,7 +637,7 @@ int ar_allreduce_rmsnorm_bwd_workspace_size(size_t rows, size_t hidden, size_t* 
   };
   if (!bytes || hidden == 0 || rows > static_cast<size_t>(INT64_MAX)) return done(AR_ERR_INVALID);
   if (hidden > AR_NORM_MAX_HIDDEN) return done(AR_ERR_UNSUPPORTED);
-  *bytes = static_cast<size_t>(ar::rmsnorm_bwd_groups(static_cast<int64_t>(rows), static_cast<int64_t>(hidden))) *
+  *bytes = static_cast<size_t>(ar::rmsnorm_bwd_groups(static_cast<int64_t>(rows), static_cast<int64_t>(hidden), 1)) *
            hidden * 4;
   return done(AR_OK);
 }
@@ -653,7 +653,7 @@ int ar_allreduce_rmsnorm_bwd(const void* const* in_bufs, int nranks, size_t rows
   if (!dgamma || (rows > 0 && (!in_bufs || !out_bufs))) return done(AR_ERR_INVALID);
   const size_t es = static_cast<size_t>(esize_of(dtype));
   const size_t need = static_cast<size_t>(ar::rmsnorm_bwd_groups(static_cast<int64_t>(rows),
-                                                                 static_cast<int64_t>(hidden))) * hidden * 4;
+                                                                 static_cast<int64_t>(hidden), 1)) * hidden * 4;
   Ranges g;
   ar::NormArgs a;
   std::memset(&a, 0, sizeof(a));

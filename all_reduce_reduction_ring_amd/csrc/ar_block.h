@@ -31,8 +31,9 @@ struct NormArgs {
 
 hipError_t launch_rmsnorm(const NormArgs& a, int dtype, hipStream_t s);
 hipError_t launch_rmsnorm_bwd(const NormArgs& a, int dtype, float* dgamma, hipStream_t s);
-// Workgroups (and so partial sums of dgamma) of the backward kernel; a function of the sizes alone.
-int64_t rmsnorm_bwd_groups(int64_t rows, int64_t hidden);
+// Workgroups (and so partial sums of dgamma) of the backward kernel for n ranks; a function of the sizes alone. Most with
+// one rank.
+int64_t rmsnorm_bwd_groups(int64_t rows, int64_t hidden, int n);
 
 // ------------------------------------------------------------------------------------------ experts
 struct SortArgs {

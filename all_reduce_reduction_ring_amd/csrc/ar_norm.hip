@@ -182,6 +182,8 @@ __device__ __forceinline__ float group_sum(float v, float* lds) {
 
 constexpr int kMaxThreads = 1024;
 constexpr int kRankBatch = 4;
+constexpr int kTeamThreads = 512;  // a backward workgroup of several teams
+constexpr int kMaxTeams = 8;
 
 // The ranks' slots of a row (NR: their number if known; otherwise `batch` of them from rank r0 on), and their sum in
 // rank order onto h.
@@ -234,12 +236,6 @@ __device__ __forceinline__ void quant8(const float (&v)[kPerLane], float* scale,
   *scale = s.scale;
 }
 
-#ifndef NORM_WPE
-#define NORM_WPE
-#endif
-#ifndef NORM_PF
-#define NORM_PF (S == 1 && NR == 1)
-#endif
 // One workgroup, one row.
 template <int DT, int S, int NR, bool EXACT>
 __global__ __launch_bounds__(kMaxThreads) void rmsnorm_kernel(NormArgs a, int64_t row0) {
@@ -322,73 +318,93 @@ template <int DT, int NR, bool EXACT> struct BwdSlot {
   }
 };
 
-// A workgroup takes rows blockIdx, blockIdx + groups, ...; its threads keep their columns' sums of dy xhat in
-// registers over all of them and leave one row of partial sums behind, which dgamma_kernel adds up in order.
+// A workgroup holds R teams of threads, each of which takes a row at a time: team i of workgroup b the rows
+// b R + i, + groups R, + 2 groups R, ... Every thread keeps its columns' sums of dy xhat in registers over all its rows;
+// the teams' sums are joined in LDS and leave as one row of partial sums per workgroup, which dgamma_kernel adds up in
+// order. One slot a lane (S = 1): the next row is read while this one's dot product is joined and its results are
+// stored. Wider rows (S > 1) have one team and read their row when its turn comes.
 template <int DT, int S, int NR, bool EXACT>
-__global__ __launch_bounds__(kMaxThreads) NORM_WPE void rmsnorm_bwd_kernel(NormArgs a) {
+__global__ __launch_bounds__(kMaxThreads) void rmsnorm_bwd_kernel(NormArgs a, int team_threads) {
+  constexpr bool kAhead = S == 1 && (Traits<DT>::kSize == 2 || NR < 8);
   __shared__ float lds[2][kMaxThreads / 64];
+  __shared__ float join[S == 1 ? kTeamThreads * kPerLane : 1];
   constexpr int kSize = Traits<DT>::kSize;
-  constexpr bool kAhead = NORM_PF;
-  const int threads = static_cast<int>(blockDim.x);
+  const int teams = S == 1 ? static_cast<int>(blockDim.x) / team_threads : 1;
+  const int team = S == 1 ? __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / team_threads) : 0;
+  const int tid = static_cast<int>(threadIdx.x) - team * team_threads;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * teams;
   float dg[S][kPerLane];
   RawGamma gam[S];
 #pragma unroll
   for (int s = 0; s < S; ++s) {
-    if (S < 4) gam[s] = load_gamma<DT, EXACT>(a, first_of<DT>(s * threads + static_cast<int>(threadIdx.x)));
+    if (S < 4) gam[s] = load_gamma<DT, EXACT>(a, first_of<DT>(s * team_threads + tid));
 #pragma unroll
     for (int k = 0; k < kPerLane; ++k) dg[s][k] = 0.0f;
   }
   int flip = 0;
   BwdSlot<DT, NR, EXACT> next;
   float rstd_next = 0.0f;
-  if (kAhead) {
-    next.load(a, blockIdx.x, first_of<DT>(static_cast<int>(threadIdx.x)));
-    rstd_next = gptr<float>(a.rstd_in)[blockIdx.x];
+  int64_t base = static_cast<int64_t>(blockIdx.x) * teams;
+  if (kAhead && base + team < a.rows) {
+    next.load(a, base + team, first_of<DT>(tid));
+    rstd_next = gptr<float>(a.rstd_in)[base + team];
   }
-  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, flip ^= 1) {
-    const int64_t at = row * a.hidden;
-    const float rstd = kAhead ? rstd_next : gptr<float>(a.rstd_in)[row];
+  for (; base < a.rows; base += step, flip ^= 1) {  // all teams stay in the loop for the barriers in it
+    const int64_t row = base + team, at = row * a.hidden;
+    const bool active = S > 1 || row < a.rows;
     float g[S][kPerLane], xh[S][kPerLane];
     Raw<DT> res[S];
-    float dot = 0.0f;
+    float dot = 0.0f, rstd = 0.0f;
+    if (active) {
+      rstd = kAhead ? rstd_next : gptr<float>(a.rstd_in)[row];
 #pragma unroll
-    for (int s = 0; s < S; ++s) {
-      const int e0 = first_of<DT>(s * threads + static_cast<int>(threadIdx.x));
-      BwdSlot<DT, NR, EXACT> x;
-      if (kAhead) x = next;
-      else x.load(a, row, e0);
-      sum_ranks<DT, NR, EXACT>(a, x.first, at * kSize, e0, g[s]);
-      settle<DT, EXACT>(g[s], e0, a.hidden);
-      if (a.saved_scales) unpack_codes(x.codes, xh[s]);
-      else unpack_raw<DT>(x.saved, xh[s]);
-      settle<DT, EXACT>(xh[s], e0, a.hidden);
-      res[s] = x.res;
-      float y[kPerLane];
-      unpack_gamma<DT, EXACT>(a, S < 4 ? gam[s] : load_gamma<DT, EXACT>(a, e0), e0, y);
+      for (int s = 0; s < S; ++s) {
+        const int e0 = first_of<DT>(s * team_threads + tid);
+        BwdSlot<DT, NR, EXACT> x;
+        if (kAhead) x = next;
+        else x.load(a, row, e0);
+        sum_ranks<DT, NR, EXACT>(a, x.first, at * kSize, e0, g[s]);
+        settle<DT, EXACT>(g[s], e0, a.hidden);
+        if (a.saved_scales) unpack_codes(x.codes, xh[s]);
+        else unpack_raw<DT>(x.saved, xh[s]);
+        settle<DT, EXACT>(xh[s], e0, a.hidden);
+        res[s] = x.res;
+        float y[kPerLane];
+        unpack_gamma<DT, EXACT>(a, S < 4 ? gam[s] : load_gamma<DT, EXACT>(a, e0), e0, y);
 #pragma unroll
-      for (int k = 0; k < kPerLane; ++k) {
-        xh[s][k] *= rstd;
-        dg[s][k] += g[s][k] * xh[s][k];
-        g[s][k] *= y[k];
-        dot += g[s][k] * xh[s][k];
+        for (int k = 0; k < kPerLane; ++k) {
+          xh[s][k] *= rstd;
+          dg[s][k] += g[s][k] * xh[s][k];
+          g[s][k] *= y[k];
+          dot += g[s][k] * xh[s][k];
+        }
+      }
+      // The clamped vectors reach into other lanes' elements, which are overwritten behind the barrier where a result
+      // goes in place. All else has been used by then; the residual's gradient has to have arrived.
+      if (a.residual) {
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+#pragma unroll
+          for (int v = 0; v < kVecs<DT>; ++v) arrived(res[s].w[v]);
+      }
+      if (kAhead && row + step < a.rows) {
+        next.load(a, row + step, first_of<DT>(tid));
+        rstd_next = gptr<float>(a.rstd_in)[row + step];
       }
     }
-    if (kAhead && row + gridDim.x < a.rows) {
-      next.load(a, row + gridDim.x, first_of<DT>(static_cast<int>(threadIdx.x)));
-      rstd_next = gptr<float>(a.rstd_in)[row + gridDim.x];
+    dot = wave_sum(dot);
+    if (team_threads > 64) {
+      if ((threadIdx.x & 63) == 0) lds[flip][threadIdx.x >> 6] = dot;
+      __syncthreads();
+      dot = 0.0f;
+      const int w0 = team * (team_threads >> 6);
+      for (int w = 0; w < team_threads >> 6; ++w) dot += lds[flip][w0 + w];
     }
-    // The clamped vectors reach into other lanes' elements, which are overwritten behind group_sum where a result goes
-    // in place. All else has been used by then; the residual's gradient has to have arrived.
-    if (a.residual) {
-#pragma unroll
-      for (int s = 0; s < S; ++s)
-#pragma unroll
-        for (int v = 0; v < kVecs<DT>; ++v) arrived(res[s].w[v]);
-    }
-    const float mean = group_sum(dot, lds[flip]) / static_cast<float>(a.hidden);
+    if (!active) continue;
+    const float mean = dot / static_cast<float>(a.hidden);
 #pragma unroll
     for (int s = 0; s < S; ++s) {
-      const int e0 = first_of<DT>(s * threads + static_cast<int>(threadIdx.x));
+      const int e0 = first_of<DT>(s * team_threads + tid);
 #pragma unroll
       for (int k = 0; k < kPerLane; ++k) g[s][k] = rstd * (g[s][k] - xh[s][k] * mean);
       if (a.residual) {
@@ -401,10 +417,23 @@ __global__ __launch_bounds__(kMaxThreads) NORM_WPE void rmsnorm_bwd_kernel(NormA
       store_slot<DT, NR>(g[s], e0, a.hidden, a.n, [&](int r) { return static_cast<char*>(a.out[r]) + at * kSize; });
     }
   }
+  if (teams > 1) {
+    const int others = team_threads * (teams - 1);
+    if (team > 0) {
+#pragma unroll
+      for (int k = 0; k < kPerLane; ++k) join[k * others + (team - 1) * team_threads + tid] = dg[0][k];
+    }
+    __syncthreads();
+    if (team > 0) return;
+    for (int t = 0; t < teams - 1; ++t) {
+#pragma unroll
+      for (int k = 0; k < kPerLane; ++k) dg[0][k] += join[k * others + t * team_threads + tid];
+    }
+  }
   float* to = a.partial + static_cast<int64_t>(blockIdx.x) * a.hidden;
 #pragma unroll
   for (int s = 0; s < S; ++s) {
-    const int e0 = first_of<DT>(s * threads + static_cast<int>(threadIdx.x));
+    const int e0 = first_of<DT>(s * team_threads + tid);
 #pragma unroll
     for (int k = 0; k < kPerLane; ++k) {
       const int e = vec_at(e0, k / Traits<DT>::kVec) + k % Traits<DT>::kVec;
@@ -453,14 +482,33 @@ Shape shape_of(int hidden) {
   return Shape{((slots + per - 1) / per + 63) / 64 * 64, per};
 }
 
-constexpr int64_t kMaxGroups = 1024;
+// Backward: teams per workgroup, as many as make 512 threads while there are rows for 256 workgroups (129 rows of 1003
+// fp16, 2 ranks: 6.4 us with one team, 7.9 us with four; 16,384 rows of 256 bf16: 28.5 us with one, 17.9 us with eight).
+int teams_of(int64_t rows, const Shape& sh) {
+  int64_t teams = kTeamThreads / sh.threads;
+  if (teams > rows / 256) teams = rows / 256;
+  return sh.slots > 1 || teams < 1 ? 1 : teams > kMaxTeams ? kMaxTeams : static_cast<int>(teams);
+}
+// Workgroups: for 16 waves on each of the 256 compute units, or for 8 where a wave's own loads are many (6 ranks and
+// more: 8 x 8192 x 4096 bf16 232 us, against 244 us with 16 waves; one rank, 16,384 x 2048: 83 us against 59 us); one
+// for every CU at least, no more than there are rows for. Each leaves a row of partial sums.
+int64_t groups_of(int64_t rows, const Shape& sh, int n) {
+  const int teams = teams_of(rows, sh);
+  int64_t most = (n >= 6 ? 2048 : 4096) / (teams * sh.threads / 64) / 256 * 256;
+  if (most < 256) most = 256;
+  if (most > 1024) most = 1024;
+  const int64_t all = (rows + teams - 1) / teams;
+  return all < most ? all : most;
+}
 
 constexpr int64_t kMaxGrid = 1 << 21;  // a launch has fewer than 2^32 threads
 
 template <int DT, int S, int NR, bool EXACT>
-hipError_t run(const NormArgs& a, bool bwd, int64_t groups, int threads, hipStream_t s) {
+hipError_t run(const NormArgs& a, bool bwd, const Shape& sh, hipStream_t s) {
+  const int threads = sh.threads;
   if (bwd) {
-    hipLaunchKernelGGL((rmsnorm_bwd_kernel<DT, S, NR, EXACT>), dim3(static_cast<unsigned>(groups)), dim3(threads), 0, s, a);
+    hipLaunchKernelGGL((rmsnorm_bwd_kernel<DT, S, NR, EXACT>), dim3(static_cast<unsigned>(groups_of(a.rows, sh, a.n))),
+                       dim3(threads * teams_of(a.rows, sh)), 0, s, a, threads);
     return hipGetLastError();
   }
   for (int64_t row = 0; row < a.rows; row += kMaxGrid) {
@@ -472,46 +520,48 @@ hipError_t run(const NormArgs& a, bool bwd, int64_t groups, int threads, hipStre
   return hipSuccess;
 }
 template <int DT, int S>
-hipError_t run_n(const NormArgs& a, bool bwd, int64_t groups, int threads, hipStream_t s) {
+hipError_t run_n(const NormArgs& a, bool bwd, const Shape& sh, hipStream_t s) {
   switch (a.n) {
-    case 1: return run<DT, S, 1, false>(a, bwd, groups, threads, s);
-    case 2: return run<DT, S, 2, false>(a, bwd, groups, threads, s);
-    case 3: return run<DT, S, 3, false>(a, bwd, groups, threads, s);
-    case 4: return run<DT, S, 4, false>(a, bwd, groups, threads, s);
-    case 8: return run<DT, S, 8, false>(a, bwd, groups, threads, s);
-    default: return run<DT, S, 0, false>(a, bwd, groups, threads, s);
+    case 1: return run<DT, S, 1, false>(a, bwd, sh, s);
+    case 2: return run<DT, S, 2, false>(a, bwd, sh, s);
+    case 3: return run<DT, S, 3, false>(a, bwd, sh, s);
+    case 4: return run<DT, S, 4, false>(a, bwd, sh, s);
+    case 8: return run<DT, S, 8, false>(a, bwd, sh, s);
+    default: return run<DT, S, 0, false>(a, bwd, sh, s);
   }
 }
 
-template <int DT> hipError_t launch(const NormArgs& a, bool bwd, int64_t groups, hipStream_t s) {
-  if (a.hidden < Traits<DT>::kVec) return run<DT, 1, 0, true>(a, bwd, groups, 64, s);
+template <int DT> hipError_t launch(const NormArgs& a, bool bwd, hipStream_t s) {
   const Shape sh = shape_of(a.hidden);
-  if (sh.slots == 1) return run_n<DT, 1>(a, bwd, groups, sh.threads, s);
-  if (sh.slots == 2) return run_n<DT, 2>(a, bwd, groups, sh.threads, s);
-  return run_n<DT, 4>(a, bwd, groups, sh.threads, s);
+  if (a.hidden < Traits<DT>::kVec) return run<DT, 1, 0, true>(a, bwd, sh, s);
+  if (sh.slots == 1) return run_n<DT, 1>(a, bwd, sh, s);
+  if (sh.slots == 2) return run_n<DT, 2>(a, bwd, sh, s);
+  return run_n<DT, 4>(a, bwd, sh, s);
 }
 
 }  // namespace
 
-int64_t rmsnorm_bwd_groups(int64_t rows, int64_t) { return rows < kMaxGroups ? rows : kMaxGroups; }
+int64_t rmsnorm_bwd_groups(int64_t rows, int64_t hidden, int n) {
+  return groups_of(rows, shape_of(static_cast<int>(hidden)), n);
+}
 
 hipError_t launch_rmsnorm(const NormArgs& a, int dtype, hipStream_t s) {
   switch (dtype) {
-    case AR_F32: return launch<AR_F32>(a, false, 0, s);
-    case AR_BF16: return launch<AR_BF16>(a, false, 0, s);
-    case AR_F16: return launch<AR_F16>(a, false, 0, s);
+    case AR_F32: return launch<AR_F32>(a, false, s);
+    case AR_BF16: return launch<AR_BF16>(a, false, s);
+    case AR_F16: return launch<AR_F16>(a, false, s);
     default: return hipErrorInvalidValue;
   }
 }
 
 hipError_t launch_rmsnorm_bwd(const NormArgs& a, int dtype, float* dgamma, hipStream_t s) {
-  const int64_t groups = rmsnorm_bwd_groups(a.rows, a.hidden);
+  const int64_t groups = rmsnorm_bwd_groups(a.rows, a.hidden, a.n);
   hipError_t e = hipSuccess;
   if (groups > 0) {
     switch (dtype) {
-      case AR_F32: e = launch<AR_F32>(a, true, groups, s); break;
-      case AR_BF16: e = launch<AR_BF16>(a, true, groups, s); break;
-      case AR_F16: e = launch<AR_F16>(a, true, groups, s); break;
+      case AR_F32: e = launch<AR_F32>(a, true, s); break;
+      case AR_BF16: e = launch<AR_BF16>(a, true, s); break;
+      case AR_F16: e = launch<AR_F16>(a, true, s); break;
       default: return hipErrorInvalidValue;
     }
   }

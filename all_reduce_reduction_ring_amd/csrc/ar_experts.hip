@@ -19,7 +19,10 @@ constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
 constexpr int kMaxExperts = AR_MAX_EXPERTS;
 constexpr int kTileBatch = 8;             // histograms read together
-constexpr int64_t kOneGroupSlots = 8192;  // up to here one workgroup sorts everything in one launch
+constexpr int kHeld = 4;  // slots a thread reads at a time; a thread's first ones stay in registers between the passes
+// Up to here one workgroup sorts everything in one launch (4096 slots, 64 experts: 7.7 us against 7.9 us in two; 8192:
+// 11.4 against 8.1 us).
+constexpr int64_t kOneGroupSlots = kSortThreads * kHeld;
 
 // The lanes of the wave that hold the same expert as this one (0 for a lane whose slot goes nowhere). All lanes take
 // part; `bits` covers every expert number.
@@ -32,10 +35,15 @@ __device__ __forceinline__ uint64_t same_expert(int e, bool in, int bits) {
   return in ? m : 0;
 }
 
-__device__ __forceinline__ int expert_of(const int32_t* ids, int64_t q, int64_t slots, int experts, bool* in) {
-  const int e = q < slots ? gptr<int32_t>(ids)[q] : -1;
-  *in = e >= 0 && e < experts;
-  return *in ? e : 0;
+// The experts of slots q0 + lane, q0 + 64 + lane, ... (-1: none, or past `end`).
+__device__ __forceinline__ void load_experts(const SortArgs& a, int64_t q0, int64_t end, int (&e)[kHeld]) {
+#pragma unroll
+  for (int u = 0; u < kHeld; ++u) {
+    const int64_t q = q0 + u * 64 + (threadIdx.x & 63);
+    e[u] = q < end ? gptr<int32_t>(a.ids)[q] : -1;
+  }
+#pragma unroll
+  for (int u = 0; u < kHeld; ++u) e[u] = e[u] < a.experts ? (e[u] < 0 ? -1 : e[u]) : -1;
 }
 
 // Exclusive sum over the workgroup's threads; `lds` holds one value per wave. Returns the total in *total.
@@ -65,9 +73,8 @@ __global__ __launch_bounds__(kSortThreads) void sort_hist_kernel(SortArgs a, int
   __syncthreads();
   const int64_t lo = static_cast<int64_t>(blockIdx.x) * tile;
   for (int64_t q = lo + threadIdx.x; q < lo + tile && q < a.slots; q += kSortThreads) {
-    bool in;
-    const int e = expert_of(a.ids, q, a.slots, a.experts, &in);
-    if (in) atomicAdd(&hist[e], 1);
+    const int e = gptr<int32_t>(a.ids)[q];
+    if (e >= 0 && e < a.experts) atomicAdd(&hist[e], 1);
   }
   __syncthreads();
   for (int e = threadIdx.x; e < a.experts; e += kSortThreads)
@@ -90,10 +97,16 @@ __global__ __launch_bounds__(kSortThreads) void sort_kernel(SortArgs a, int64_t 
   const int64_t hi = lo + tile < a.slots ? lo + tile : a.slots;
   const int64_t per_wave = (tile + kSortThreads - 1) / kSortThreads * 64;
   const int64_t w_lo = lo + wave * per_wave, w_hi = w_lo + per_wave < hi ? w_lo + per_wave : hi;
-  for (int64_t q0 = w_lo; q0 < w_hi; q0 += 64) {
-    bool in;
-    const int e = expert_of(a.ids, q0 + lane, w_hi, a.experts, &in);
-    if (in) atomicAdd(&next[wave][e], 1);
+  int held[kHeld];
+  load_experts(a, w_lo, w_hi, held);
+  for (int64_t q0 = w_lo; q0 < w_hi; q0 += kHeld * 64) {
+    int x[kHeld];
+#pragma unroll
+    for (int u = 0; u < kHeld; ++u) x[u] = held[u];
+    if (q0 != w_lo) load_experts(a, q0, w_hi, x);
+#pragma unroll
+    for (int u = 0; u < kHeld; ++u)
+      if (x[u] >= 0) atomicAdd(&next[wave][x[u]], 1);
   }
   __syncthreads();
   // thread e: its expert's slots in all tiles, in the tiles before this one, and the segment's start
@@ -145,25 +158,37 @@ __global__ __launch_bounds__(kSortThreads) void sort_kernel(SortArgs a, int64_t 
       gptr<int32_t>(a.counts)[e] = total;
       if (e == 0) gptr<int32_t>(a.offsets)[a.experts] = rows;
     }
-    // rows of this segment that no slot takes
-    if (e % gridDim.x == blockIdx.x)
-      for (int p = first + total; p < first + padded; ++p) gptr<int32_t>(a.src)[p] = -1;
+    part[0][e] = first + total;
+    part[1][e] = first + padded;
   }
   for (int64_t p = rows + static_cast<int64_t>(blockIdx.x) * kSortThreads + threadIdx.x; p < a.rows;
        p += static_cast<int64_t>(gridDim.x) * kSortThreads)
     gptr<int32_t>(a.src)[p] = -1;
   __syncthreads();
-  for (int64_t q0 = w_lo; q0 < w_hi; q0 += 64) {
-    const int64_t q = q0 + lane;
-    bool in;
-    const int x = expert_of(a.ids, q, w_hi, a.experts, &in);
-    const uint64_t same = same_expert(x, in, bits);
-    const int rank = __popcll(same & ((uint64_t(1) << lane) - 1));
-    int p = 0;
-    if (in && rank == 0) p = atomicAdd(&next[wave][x], __popcll(same));  // the lowest lane takes rows for all of them
-    p = __shfl(p, in ? __ffsll(static_cast<unsigned long long>(same)) - 1 : lane, 64) + rank;
-    if (q < w_hi) gptr<int32_t>(a.pos)[q] = in ? p : -1;
-    if (in) gptr<int32_t>(a.src)[p] = static_cast<int32_t>(q);
+  if (a.align > 1) {  // rows of the segments that no slot takes, 16 lanes to a segment
+    constexpr int kAtOnce = kSortThreads / 16;
+    for (int x = static_cast<int>(blockIdx.x) * kAtOnce + static_cast<int>(threadIdx.x) / 16; x < a.experts;
+         x += static_cast<int>(gridDim.x) * kAtOnce)
+      for (int p = part[0][x] + (lane & 15); p < part[1][x]; p += 16) gptr<int32_t>(a.src)[p] = -1;
+  }
+  for (int64_t q0 = w_lo; q0 < w_hi; q0 += kHeld * 64) {
+    int x[kHeld];
+#pragma unroll
+    for (int u = 0; u < kHeld; ++u) x[u] = held[u];
+    if (q0 != w_lo) load_experts(a, q0, w_hi, x);
+#pragma unroll
+    for (int u = 0; u < kHeld; ++u) {
+      const int64_t q = q0 + u * 64 + lane;
+      if (q - lane >= w_hi) break;
+      const bool in = x[u] >= 0;
+      const uint64_t same = same_expert(x[u], in, bits);
+      const int rank = __popcll(same & ((uint64_t(1) << lane) - 1));
+      int p = 0;
+      if (in && rank == 0) p = atomicAdd(&next[wave][x[u]], __popcll(same));  // the lowest lane takes rows for all of them
+      p = __shfl(p, in ? __ffsll(static_cast<unsigned long long>(same)) - 1 : lane, 64) + rank;
+      if (q < w_hi) gptr<int32_t>(a.pos)[q] = in ? p : -1;
+      if (in) gptr<int32_t>(a.src)[p] = static_cast<int32_t>(q);
+    }
   }
 }
 
@@ -219,6 +244,7 @@ __device__ __forceinline__ void zero_pads(const MoveArgs& a, int group, int part
 // end), the others copy their tokens' rows. U 16-byte vectors a lane at a time. The last vector of a row is moved up to
 // end with it (its first bytes are then written twice, with the same values); rows below 16 bytes go byte by byte.
 constexpr int kCopyLanes = 128, kCopyUnroll = 4;
+template <int MODE>
 __global__ __launch_bounds__(kCopyLanes) void dispatch_kernel(MoveArgs a, int row_bytes, int scale_bytes, int pad_groups,
                                                               int pad_parts) {
   constexpr int LANES = kCopyLanes, U = kCopyUnroll;
@@ -239,7 +265,7 @@ __global__ __launch_bounds__(kCopyLanes) void dispatch_kernel(MoveArgs a, int ro
 #pragma unroll
           for (int u = 0; u < U; ++u) {
             at[u] = clamped<16>(b0 + u * LANES * 16, row_bytes);
-            v[u] = ld_row(from, at[u]);
+            v[u] = ld_row<kCached>(from, at[u]);
           }
 #pragma unroll
           for (int j = 0; j < kChoices; ++j) {
@@ -247,7 +273,7 @@ __global__ __launch_bounds__(kCopyLanes) void dispatch_kernel(MoveArgs a, int ro
             char* to = static_cast<char*>(a.y) + p[j] * static_cast<int64_t>(row_bytes);
 #pragma unroll
             for (int u = 0; u < U; ++u)
-              if (b0 + u * LANES * 16 < row_bytes) st_row(to, at[u], v[u]);
+              if (b0 + u * LANES * 16 < row_bytes) st_row<MODE>(to, at[u], v[u]);
           }
         }
       } else if (lane < row_bytes) {
@@ -276,7 +302,7 @@ template <int DT> __device__ __forceinline__ int lane_elem() { return static_cas
 
 // The sum runs in fp32 over the choices in order, the addend last, and is rounded once. A slot without a row adds
 // nothing: its row is not read. The rows of up to eight choices, U vectors of each, are on their way together.
-template <int DT, int LANES, int U, bool EXACT>
+template <int DT, int LANES, int U, int MODE>
 __global__ __launch_bounds__(LANES) void combine_kernel(MoveArgs a) {
   constexpr int V = Traits<DT>::kVec;
   const int64_t row = static_cast<int64_t>(a.hidden) * Traits<DT>::kSize;
@@ -293,7 +319,7 @@ __global__ __launch_bounds__(LANES) void combine_kernel(MoveArgs a) {
 #pragma unroll
         for (int i = 0; i < V; ++i) acc[u][i] = 0.0f;
         if (a.extra && b0 + u * LANES * V < a.hidden)
-          add[u] = load_vec<DT, EXACT>(static_cast<const char*>(a.extra) + t * row, b0 + u * LANES * V + lane_elem<DT>(),
+          add[u] = load_vec<DT, MODE>(static_cast<const char*>(a.extra) + t * row, b0 + u * LANES * V + lane_elem<DT>(),
                                        a.hidden);
       }
       for (int j0 = 0; j0 < a.k; j0 += kChoices) {
@@ -308,7 +334,7 @@ __global__ __launch_bounds__(LANES) void combine_kernel(MoveArgs a) {
 #pragma unroll
           for (int u = 0; u < U; ++u)
             if (b0 + u * LANES * V < a.hidden)
-              x[j][u] = load_vec<DT, EXACT>(static_cast<const char*>(a.x) + p[j] * row,
+              x[j][u] = load_vec<DT, MODE>(static_cast<const char*>(a.x) + p[j] * row,
                                             b0 + u * LANES * V + lane_elem<DT>(), a.hidden);
         }
 #pragma unroll
@@ -334,15 +360,15 @@ __global__ __launch_bounds__(LANES) void combine_kernel(MoveArgs a) {
 #pragma unroll
           for (int i = 0; i < V; ++i) acc[u][i] += v[i];
         }
-        settle_vec<DT, EXACT>(acc[u], e, a.hidden);
-        store_vec<DT>(static_cast<char*>(a.y) + t * row, e, a.hidden, Slot<DT>::pack(acc[u]));
+        settle_vec<DT, MODE>(acc[u], e, a.hidden);
+        store_vec<DT, MODE>(static_cast<char*>(a.y) + t * row, e, a.hidden, Slot<DT>::pack(acc[u]));
       }
     }
   }
 }
 
 // The waves' dot products are joined in LDS. The first pad_groups workgroups zero the pad rows.
-template <int DT, int LANES, int U, bool EXACT>
+template <int DT, int LANES, int U, int MODE>
 __global__ __launch_bounds__(LANES) void combine_bwd_kernel(MoveArgs a, int pad_groups, int pad_parts) {
   constexpr int V = Traits<DT>::kVec;
   constexpr int kWaves = LANES / 64;
@@ -366,7 +392,7 @@ __global__ __launch_bounds__(LANES) void combine_bwd_kernel(MoveArgs a, int pad_
 #pragma unroll
         for (int u = 0; u < U; ++u)
           if (b0 + u * LANES * V < a.hidden)
-            d[u] = load_vec<DT, EXACT>(static_cast<const char*>(a.extra) + t * row, b0 + u * LANES * V + lane_elem<DT>(),
+            d[u] = load_vec<DT, MODE>(static_cast<const char*>(a.extra) + t * row, b0 + u * LANES * V + lane_elem<DT>(),
                                        a.hidden);
 #pragma unroll
         for (int j = 0; j < kChoices; ++j) {
@@ -374,7 +400,7 @@ __global__ __launch_bounds__(LANES) void combine_bwd_kernel(MoveArgs a, int pad_
 #pragma unroll
           for (int u = 0; u < U; ++u)
             if (b0 + u * LANES * V < a.hidden)
-              x[j][u] = load_vec<DT, EXACT>(static_cast<const char*>(a.x) + p[j] * row,
+              x[j][u] = load_vec<DT, MODE>(static_cast<const char*>(a.x) + p[j] * row,
                                             b0 + u * LANES * V + lane_elem<DT>(), a.hidden);
         }
 #pragma unroll
@@ -383,19 +409,19 @@ __global__ __launch_bounds__(LANES) void combine_bwd_kernel(MoveArgs a, int pad_
           const int e = b0 + u * LANES * V + lane_elem<DT>();
           float dv[V];
           Slot<DT>::unpack(d[u], dv);
-          settle_vec<DT, EXACT>(dv, e, a.hidden);
+          settle_vec<DT, MODE>(dv, e, a.hidden);
 #pragma unroll
           for (int j = 0; j < kChoices; ++j) {
             if (p[j] < 0) continue;
             float v[V], y[V];
             Slot<DT>::unpack(x[j][u], v);
-            settle_vec<DT, EXACT>(v, e, a.hidden);
+            settle_vec<DT, MODE>(v, e, a.hidden);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
               dot[j] = fmaf(dv[i], v[i], dot[j]);
               y[i] = w[j] * dv[i];
             }
-            store_vec<DT>(static_cast<char*>(a.y) + p[j] * row, e, a.hidden, Slot<DT>::pack(y));
+            store_vec<DT, MODE>(static_cast<char*>(a.y) + p[j] * row, e, a.hidden, Slot<DT>::pack(y));
           }
         }
       }
@@ -423,11 +449,11 @@ __global__ __launch_bounds__(LANES) void combine_bwd_kernel(MoveArgs a, int pad_
   }
 }
 
-// Slots per workgroup of the tiled sort: 2048, more where that would make over 512 tiles (every workgroup reads all
+// Slots per workgroup of the tiled sort: 1024, more where that would make over 512 tiles (every workgroup reads all
 // tiles' histograms).
 int64_t sort_tile(int64_t slots) {
   const int64_t even = (slots + 511) / 512;
-  return even <= 2048 ? 2048 : (even + kSortThreads - 1) / kSortThreads * kSortThreads;
+  return (even + kSortThreads - 1) / kSortThreads * kSortThreads;
 }
 
 constexpr int kUnroll = 2;  // vectors of a row a lane takes at a time
@@ -446,45 +472,45 @@ int pad_parts(const MoveArgs& a, int64_t row_bytes) {
   return spare < 1 ? 1 : spare > 16 ? 16 : static_cast<int>(spare);
 }
 
-template <int DT, int LANES, int U, bool EXACT> hipError_t combine_run(const MoveArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL((combine_kernel<DT, LANES, U, EXACT>), dim3(static_cast<unsigned>(groups_for(a.tokens))),
+template <int DT, int LANES, int U, int MODE> hipError_t combine_run(const MoveArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL((combine_kernel<DT, LANES, U, MODE>), dim3(static_cast<unsigned>(groups_for(a.tokens))),
                      dim3(LANES), 0, s, a);
   return hipGetLastError();
 }
+template <int DT, int MODE> hipError_t combine_lanes(const MoveArgs& a, int lanes, hipStream_t s) {
+  if (lanes == 256) return combine_run<DT, 256, kUnroll, MODE>(a, s);
+  if (lanes == 128) return combine_run<DT, 128, kUnroll, MODE>(a, s);
+  return combine_run<DT, 64, kUnroll, MODE>(a, s);
+}
 template <int DT> hipError_t combine_dt(const MoveArgs& a, hipStream_t s) {
   constexpr int V = Traits<DT>::kVec;
-  if (a.hidden < V || (a.extra == a.y && a.hidden % V != 0)) return combine_run<DT, 64, 1, true>(a, s);
-  switch (lanes_for((a.hidden + V - 1) / V, a.tokens)) {
-    case 256: return combine_run<DT, 256, kUnroll, false>(a, s);
-    case 128: return combine_run<DT, 128, kUnroll, false>(a, s);
-    default:
-#ifdef EXP_S1
-    if (a.hidden <= 64 * V) return combine_run<DT, 64, 1, false>(a, s);
-#endif
-    return combine_run<DT, 64, kUnroll, false>(a, s);
-  }
+  if (a.hidden < V || (a.extra == a.y && a.hidden % V != 0)) return combine_run<DT, 64, 1, kExact>(a, s);
+  const int64_t row = static_cast<int64_t>(a.hidden) * Traits<DT>::kSize;
+  const int lanes = lanes_for((a.hidden + V - 1) / V, a.tokens);
+  return streams(a.tokens * row * (a.k + 2), row) ? combine_lanes<DT, kStream>(a, lanes, s)
+                                                  : combine_lanes<DT, kCached>(a, lanes, s);
 }
 
-template <int DT, int LANES, int U, bool EXACT> hipError_t combine_bwd_run(const MoveArgs& a, hipStream_t s) {
+template <int DT, int LANES, int U, int MODE> hipError_t combine_bwd_run(const MoveArgs& a, hipStream_t s) {
   const int parts = pad_parts(a, static_cast<int64_t>(a.hidden) * Traits<DT>::kSize);
   const int pads = a.offsets ? a.experts * parts : 0;
-  hipLaunchKernelGGL((combine_bwd_kernel<DT, LANES, U, EXACT>),
+  hipLaunchKernelGGL((combine_bwd_kernel<DT, LANES, U, MODE>),
                      dim3(static_cast<unsigned>(groups_for(a.tokens) + pads)), dim3(LANES), 0, s, a, pads, parts);
   return hipGetLastError();
 }
+template <int DT, int U, int MODE> hipError_t combine_bwd_lanes(const MoveArgs& a, int lanes, hipStream_t s) {
+  if (lanes == 256) return combine_bwd_run<DT, 256, U, MODE>(a, s);
+  if (lanes == 128) return combine_bwd_run<DT, 128, U, MODE>(a, s);
+  return combine_bwd_run<DT, 64, U, MODE>(a, s);
+}
 template <int DT> hipError_t combine_bwd_dt(const MoveArgs& a, hipStream_t s) {
   constexpr int V = Traits<DT>::kVec;
+  const int64_t row = static_cast<int64_t>(a.hidden) * Traits<DT>::kSize;
   const int lanes = lanes_for((a.hidden + V - 1) / V, a.tokens);
-  if (a.hidden < V || (a.x == a.y && a.hidden % V != 0)) {  // the same lanes, so that dweights has the same bits
-    if (lanes == 256) return combine_bwd_run<DT, 256, 1, true>(a, s);
-    if (lanes == 128) return combine_bwd_run<DT, 128, 1, true>(a, s);
-    return combine_bwd_run<DT, 64, 1, true>(a, s);
-  }
-  switch (lanes) {
-    case 256: return combine_bwd_run<DT, 256, kUnroll, false>(a, s);
-    case 128: return combine_bwd_run<DT, 128, kUnroll, false>(a, s);
-    default: return combine_bwd_run<DT, 64, kUnroll, false>(a, s);
-  }
+  // in place with the same lanes, so that dweights has the same bits
+  if (a.hidden < V || (a.x == a.y && a.hidden % V != 0)) return combine_bwd_lanes<DT, 1, kExact>(a, lanes, s);
+  return streams(a.tokens * row * (2 * a.k + 1), row) ? combine_bwd_lanes<DT, kUnroll, kStream>(a, lanes, s)
+                                                      : combine_bwd_lanes<DT, kUnroll, kCached>(a, lanes, s);
 }
 
 }  // namespace
@@ -516,8 +542,11 @@ hipError_t launch_expert_dispatch(const MoveArgs& a, int esize, hipStream_t s) {
   const int row = a.hidden * esize, scale = a.x_scales ? (a.hidden + AR_FP8_BLOCK - 1) / AR_FP8_BLOCK * 4 : 0;
   const int parts = pad_parts(a, row);
   const int pads = a.offsets ? a.experts * parts : 0;
-  hipLaunchKernelGGL(dispatch_kernel, dim3(static_cast<unsigned>(groups_for(a.tokens) + pads)), dim3(kCopyLanes), 0, s,
-                     a, row, scale, pads, parts);
+  const dim3 grid(static_cast<unsigned>(groups_for(a.tokens) + pads)), block(kCopyLanes);
+  if (streams(a.tokens * row * static_cast<int64_t>(a.k + 1), row))
+    hipLaunchKernelGGL(dispatch_kernel<kStream>, grid, block, 0, s, a, row, scale, pads, parts);
+  else
+    hipLaunchKernelGGL(dispatch_kernel<kCached>, grid, block, 0, s, a, row, scale, pads, parts);
   return hipGetLastError();
 }
 

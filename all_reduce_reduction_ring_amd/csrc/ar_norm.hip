@@ -31,10 +31,10 @@ template <int DT> struct Raw {
 };
 
 // A slot of a row as stored, from the clamped places.
-template <int DT, bool EXACT> __device__ __forceinline__ Raw<DT> load_raw(const void* row, int e0, int hidden) {
+template <int DT, int MODE> __device__ __forceinline__ Raw<DT> load_raw(const void* row, int e0, int hidden) {
   Raw<DT> r;
 #pragma unroll
-  for (int v = 0; v < kVecs<DT>; ++v) r.w[v] = load_vec<DT, EXACT>(row, vec_at(e0, v), hidden);
+  for (int v = 0; v < kVecs<DT>; ++v) r.w[v] = load_vec<DT, MODE>(row, vec_at(e0, v), hidden);
   return r;
 }
 template <int DT> __device__ __forceinline__ void unpack_raw(const Raw<DT>& r, float (&v)[kPerLane]) {
@@ -46,9 +46,9 @@ template <int DT> __device__ __forceinline__ void unpack_raw(const Raw<DT>& r, f
   }
 }
 // Values read from clamped places, moved where they belong.
-template <int DT, bool EXACT> __device__ __forceinline__ void settle(float (&v)[kPerLane], int e0, int hidden) {
+template <int DT, int MODE> __device__ __forceinline__ void settle(float (&v)[kPerLane], int e0, int hidden) {
 #pragma unroll
-  for (int i = 0; i < kVecs<DT>; ++i) settle_vec<DT, EXACT>(v + i * Traits<DT>::kVec, vec_at(e0, i), hidden);
+  for (int i = 0; i < kVecs<DT>; ++i) settle_vec<DT, MODE>(v + i * Traits<DT>::kVec, vec_at(e0, i), hidden);
 }
 
 template <int NR, typename F> __device__ __forceinline__ void each_rank(int n, F f) {
@@ -61,7 +61,7 @@ template <int NR, typename F> __device__ __forceinline__ void each_rank(int n, F
 }
 
 // A slot rounded into the type and stored to the row `to(r)` of every rank.
-template <int DT, int NR, typename F>
+template <int DT, int NR, int MODE, typename F>
 __device__ __forceinline__ void store_slot(const float (&v)[kPerLane], int e0, int hidden, int n, F to) {
   constexpr int V = Traits<DT>::kVec, kSize = Traits<DT>::kSize;
 #pragma unroll
@@ -72,7 +72,7 @@ __device__ __forceinline__ void store_slot(const float (&v)[kPerLane], int e0, i
     const u32x4 w = Slot<DT>::pack(x);
     const int e = vec_at(e0, i);
     const uint32_t at = static_cast<uint32_t>(e) * kSize;
-    if (e + V <= hidden) each_rank<NR>(n, [&](int r) { st_row(to(r), at, w); });
+    if (e + V <= hidden) each_rank<NR>(n, [&](int r) { st_row<MODE>(to(r), at, w); });
     else if (e < hidden) {
 #pragma unroll 1
       for (int r = 0; r < n; ++r) st_row_part<kSize>(to(r), at, w, (hidden - e) * kSize);
@@ -81,7 +81,7 @@ __device__ __forceinline__ void store_slot(const float (&v)[kPerLane], int e0, i
 }
 
 // A slot's 8 codes, as two words (elements 0-3 and 4-7), to the row `to(r)` of every rank.
-template <int DT, int NR, typename F>
+template <int DT, int NR, int MODE, typename F>
 __device__ __forceinline__ void store_codes(const uint32_t (&w)[2], int e0, int hidden, int n, F to) {
   constexpr int V = Traits<DT>::kVec;
 #pragma unroll
@@ -90,8 +90,10 @@ __device__ __forceinline__ void store_codes(const uint32_t (&w)[2], int e0, int 
     if (e + V <= hidden) {
       each_rank<NR>(n, [&](int r) {
         uint8_t* p = to(r) + opaque(e);
-        if constexpr (V == 8) __builtin_nontemporal_store(u32x2{w[0], w[1]}, gptr<u32x2_a1>(p));
-        else __builtin_nontemporal_store(w[i], gptr<u32_a1>(p));
+        if constexpr (V == 8 && MODE == kStream) __builtin_nontemporal_store(u32x2{w[0], w[1]}, gptr<u32x2_a1>(p));
+        else if constexpr (V == 8) *gptr<u32x2_a1>(p) = u32x2{w[0], w[1]};
+        else if constexpr (MODE == kStream) __builtin_nontemporal_store(w[i], gptr<u32_a1>(p));
+        else *gptr<u32_a1>(p) = w[i];
       });
     } else if (e < hidden) {
 #pragma unroll 1
@@ -104,11 +106,11 @@ struct RawCodes {
   uint32_t w[2];
   float scale;
 };
-template <int DT, bool EXACT>
+template <int DT, int MODE>
 __device__ __forceinline__ RawCodes load_codes(const uint8_t* row, const float* scales, int e0, int hidden) {
   constexpr int V = Traits<DT>::kVec;
   RawCodes r{{0, 0}, 0.0f};
-  if constexpr (EXACT) {
+  if constexpr (MODE == kExact) {
     for (int k = 0; k < V; ++k)
       if (e0 + k < hidden) r.w[k >> 2] |= static_cast<uint32_t>(gptr<uint8_t>(row)[e0 + k]) << (8 * (k & 3));
   } else if constexpr (V == 8) {
@@ -138,25 +140,25 @@ __device__ __forceinline__ void unpack_codes(const RawCodes& r, float (&v)[kPerL
 struct RawGamma {
   u32x4 w[2];
 };
-template <int DT, bool EXACT> __device__ __forceinline__ RawGamma load_gamma(const NormArgs& a, int e0) {
+template <int DT, int MODE> __device__ __forceinline__ RawGamma load_gamma(const NormArgs& a, int e0) {
   RawGamma r;
   if (Traits<DT>::kSize == 2 && a.gamma_f32) {
     const uint32_t at = clamped<kPerLane>(e0, a.hidden) * 4;
-    if constexpr (EXACT) {
+    if constexpr (MODE == kExact) {
 #pragma unroll
       for (int k = 0; k < kPerLane; ++k) r.w[k >> 2][k & 3] = e0 + k < a.hidden ? gptr<uint32_t>(a.gamma)[e0 + k] : 0;
     } else {
-      r.w[0] = ld_row(a.gamma, at);
-      r.w[1] = ld_row(a.gamma, at + 16);
+      r.w[0] = ld_row<kCached>(a.gamma, at);
+      r.w[1] = ld_row<kCached>(a.gamma, at + 16);
     }
   } else {
-    const Raw<DT> x = load_raw<DT, EXACT>(a.gamma, e0, a.hidden);
+    const Raw<DT> x = load_raw<DT, MODE == kExact ? kExact : kCached>(a.gamma, e0, a.hidden);
 #pragma unroll
     for (int v = 0; v < kVecs<DT>; ++v) r.w[v] = x.w[v];
   }
   return r;
 }
-template <int DT, bool EXACT>
+template <int DT, int MODE>
 __device__ __forceinline__ void unpack_gamma(const NormArgs& a, const RawGamma& r, int e0, float (&v)[kPerLane]) {
   if (Traits<DT>::kSize == 2 && !a.gamma_f32) {
     Slot<Traits<DT>::kSize == 2 ? DT : AR_BF16>::unpack(r.w[0], v);
@@ -164,7 +166,7 @@ __device__ __forceinline__ void unpack_gamma(const NormArgs& a, const RawGamma& 
 #pragma unroll
     for (int k = 0; k < kPerLane; ++k) v[k] = __uint_as_float(r.w[k / 4][k % 4]);
   }
-  settle<DT, EXACT>(v, e0, a.hidden);
+  settle<DT, MODE>(v, e0, a.hidden);
 }
 
 // Sum over the workgroup, in every thread; `lds` holds one float per wave and is free again two barriers later, so
@@ -187,14 +189,14 @@ constexpr int kMaxTeams = 8;
 
 // The ranks' slots of a row (NR: their number if known; otherwise `batch` of them from rank r0 on), and their sum in
 // rank order onto h.
-template <int DT, int NR, bool EXACT> struct RankSlots {
+template <int DT, int NR, int MODE> struct RankSlots {
   static constexpr int kBatch = NR > 0 ? NR : kRankBatch;
   Raw<DT> raw[kBatch];
   __device__ __forceinline__ void load(const NormArgs& a, int64_t off, int e0, int r0) {
 #pragma unroll
     for (int r = 0; r < kBatch; ++r)
       if (NR > 0 || r0 + r < a.n)
-        raw[r] = load_raw<DT, EXACT>(static_cast<const char*>(a.in[r0 + r]) + off, e0, a.hidden);
+        raw[r] = load_raw<DT, MODE>(static_cast<const char*>(a.in[r0 + r]) + off, e0, a.hidden);
   }
   __device__ __forceinline__ void add(const NormArgs& a, int r0, float (&h)[kPerLane]) const {
 #pragma unroll
@@ -210,13 +212,13 @@ template <int DT, int NR, bool EXACT> struct RankSlots {
 };
 
 // h = the sum of the ranks' slots, the first ones already on their way.
-template <int DT, int NR, bool EXACT>
-__device__ __forceinline__ void sum_ranks(const NormArgs& a, const RankSlots<DT, NR, EXACT>& first, int64_t off, int e0,
+template <int DT, int NR, int MODE>
+__device__ __forceinline__ void sum_ranks(const NormArgs& a, const RankSlots<DT, NR, MODE>& first, int64_t off, int e0,
                                           float (&h)[kPerLane]) {
   first.add(a, 0, h);
   if constexpr (NR == 0) {
     for (int r0 = kRankBatch; r0 < a.n; r0 += kRankBatch) {
-      RankSlots<DT, NR, EXACT> more;
+      RankSlots<DT, NR, MODE> more;
       more.load(a, off, e0, r0);
       more.add(a, r0, h);
     }
@@ -237,7 +239,7 @@ __device__ __forceinline__ void quant8(const float (&v)[kPerLane], float* scale,
 }
 
 // One workgroup, one row.
-template <int DT, int S, int NR, bool EXACT>
+template <int DT, int S, int NR, int MODE>
 __global__ __launch_bounds__(kMaxThreads) void rmsnorm_kernel(NormArgs a, int64_t row0) {
   __shared__ float lds[kMaxThreads / 64];
   constexpr int kSize = Traits<DT>::kSize;
@@ -248,22 +250,22 @@ __global__ __launch_bounds__(kMaxThreads) void rmsnorm_kernel(NormArgs a, int64_
   RawGamma gam[S];
   float ss = 0.0f;
 #pragma unroll
-  for (int s = 0; s < S; ++s) gam[s] = load_gamma<DT, EXACT>(a, first_of<DT>(s * threads + static_cast<int>(threadIdx.x)));
+  for (int s = 0; s < S; ++s) gam[s] = load_gamma<DT, MODE>(a, first_of<DT>(s * threads + static_cast<int>(threadIdx.x)));
 #pragma unroll
   for (int s = 0; s < S; ++s) {
     const int e0 = first_of<DT>(s * threads + static_cast<int>(threadIdx.x));
-    RankSlots<DT, NR, EXACT> first;
+    RankSlots<DT, NR, MODE> first;
     Raw<DT> res;
     first.load(a, at * kSize, e0, 0);
-    if (a.residual) res = load_raw<DT, EXACT>(static_cast<const char*>(a.residual) + at * kSize, e0, a.hidden);
-    sum_ranks<DT, NR, EXACT>(a, first, at * kSize, e0, h[s]);
+    if (a.residual) res = load_raw<DT, MODE>(static_cast<const char*>(a.residual) + at * kSize, e0, a.hidden);
+    sum_ranks<DT, NR, MODE>(a, first, at * kSize, e0, h[s]);
     if (a.residual) {
       float v[kPerLane];
       unpack_raw<DT>(res, v);
 #pragma unroll
       for (int k = 0; k < kPerLane; ++k) h[s][k] += v[k];
     }
-    settle<DT, EXACT>(h[s], e0, a.hidden);
+    settle<DT, MODE>(h[s], e0, a.hidden);
 #pragma unroll
     for (int k = 0; k < kPerLane; ++k) ss += h[s][k] * h[s][k];
   }
@@ -276,33 +278,33 @@ __global__ __launch_bounds__(kMaxThreads) void rmsnorm_kernel(NormArgs a, int64_
     const int e0 = first_of<DT>(i);
     const bool block_lane = (i & 15) == 0 && e0 < a.hidden;
     if (a.residual_out)
-      store_slot<DT, 1>(h[s], e0, a.hidden, 1, [&](int) { return static_cast<char*>(a.residual_out) + at * kSize; });
+      store_slot<DT, 1, MODE>(h[s], e0, a.hidden, 1, [&](int) { return static_cast<char*>(a.residual_out) + at * kSize; });
     if (a.codes) {
       float sc;
       uint32_t w[2];
       quant8(h[s], &sc, w);
-      store_codes<DT, 1>(w, e0, a.hidden, 1, [&](int) { return a.codes + at; });
+      store_codes<DT, 1, MODE>(w, e0, a.hidden, 1, [&](int) { return a.codes + at; });
       if (block_lane) gptr<float>(a.scales + row * nb)[i >> 4] = sc;
     }
     float y[kPerLane];
-    unpack_gamma<DT, EXACT>(a, gam[s], e0, y);
+    unpack_gamma<DT, MODE>(a, gam[s], e0, y);
 #pragma unroll
     for (int k = 0; k < kPerLane; ++k) y[k] = h[s][k] * rstd * y[k];
     if (a.out8) {
       float sc;
       uint32_t w[2];
       quant8(y, &sc, w);
-      store_codes<DT, NR>(w, e0, a.hidden, a.n, [&](int r) { return static_cast<uint8_t*>(a.out[r]) + at; });
+      store_codes<DT, NR, MODE>(w, e0, a.hidden, a.n, [&](int r) { return static_cast<uint8_t*>(a.out[r]) + at; });
       if (block_lane) each_rank<NR>(a.n, [&](int r) { *gptr<float>(a.out_scales[r] + row * nb + opaque(i >> 4)) = sc; });
     } else {
-      store_slot<DT, NR>(y, e0, a.hidden, a.n, [&](int r) { return static_cast<char*>(a.out[r]) + at * kSize; });
+      store_slot<DT, NR, MODE>(y, e0, a.hidden, a.n, [&](int r) { return static_cast<char*>(a.out[r]) + at * kSize; });
     }
   }
 }
 
 // What a lane reads of one slot of a row in the backward pass.
-template <int DT, int NR, bool EXACT> struct BwdSlot {
-  RankSlots<DT, NR, EXACT> first;
+template <int DT, int NR, int MODE> struct BwdSlot {
+  RankSlots<DT, NR, MODE> first;
   Raw<DT> saved, res;
   RawCodes codes;
   __device__ __forceinline__ void load(const NormArgs& a, int64_t row, int e0) {
@@ -310,11 +312,11 @@ template <int DT, int NR, bool EXACT> struct BwdSlot {
     const int64_t at = row * a.hidden;
     first.load(a, at * kSize, e0, 0);
     if (a.saved_scales)
-      codes = load_codes<DT, EXACT>(static_cast<const uint8_t*>(a.saved) + at,
+      codes = load_codes<DT, MODE>(static_cast<const uint8_t*>(a.saved) + at,
                                     a.saved_scales + row * ((a.hidden + kBlock - 1) / kBlock), e0, a.hidden);
     else
-      saved = load_raw<DT, EXACT>(static_cast<const char*>(a.saved) + at * kSize, e0, a.hidden);
-    if (a.residual) res = load_raw<DT, EXACT>(static_cast<const char*>(a.residual) + at * kSize, e0, a.hidden);
+      saved = load_raw<DT, MODE>(static_cast<const char*>(a.saved) + at * kSize, e0, a.hidden);
+    if (a.residual) res = load_raw<DT, MODE>(static_cast<const char*>(a.residual) + at * kSize, e0, a.hidden);
   }
 };
 
@@ -323,7 +325,7 @@ template <int DT, int NR, bool EXACT> struct BwdSlot {
 // the teams' sums are joined in LDS and leave as one row of partial sums per workgroup, which dgamma_kernel adds up in
 // order. One slot a lane (S = 1): the next row is read while this one's dot product is joined and its results are
 // stored. Wider rows (S > 1) have one team and read their row when its turn comes.
-template <int DT, int S, int NR, bool EXACT>
+template <int DT, int S, int NR, int MODE>
 __global__ __launch_bounds__(kMaxThreads) void rmsnorm_bwd_kernel(NormArgs a, int team_threads) {
   constexpr bool kAhead = S == 1 && (Traits<DT>::kSize == 2 || NR < 8);
   __shared__ float lds[2][kMaxThreads / 64];
@@ -337,12 +339,12 @@ __global__ __launch_bounds__(kMaxThreads) void rmsnorm_bwd_kernel(NormArgs a, in
   RawGamma gam[S];
 #pragma unroll
   for (int s = 0; s < S; ++s) {
-    if (S < 4) gam[s] = load_gamma<DT, EXACT>(a, first_of<DT>(s * team_threads + tid));
+    if (S < 4) gam[s] = load_gamma<DT, MODE>(a, first_of<DT>(s * team_threads + tid));
 #pragma unroll
     for (int k = 0; k < kPerLane; ++k) dg[s][k] = 0.0f;
   }
   int flip = 0;
-  BwdSlot<DT, NR, EXACT> next;
+  BwdSlot<DT, NR, MODE> next;
   float rstd_next = 0.0f;
   int64_t base = static_cast<int64_t>(blockIdx.x) * teams;
   if (kAhead && base + team < a.rows) {
@@ -360,17 +362,17 @@ __global__ __launch_bounds__(kMaxThreads) void rmsnorm_bwd_kernel(NormArgs a, in
 #pragma unroll
       for (int s = 0; s < S; ++s) {
         const int e0 = first_of<DT>(s * team_threads + tid);
-        BwdSlot<DT, NR, EXACT> x;
+        BwdSlot<DT, NR, MODE> x;
         if (kAhead) x = next;
         else x.load(a, row, e0);
-        sum_ranks<DT, NR, EXACT>(a, x.first, at * kSize, e0, g[s]);
-        settle<DT, EXACT>(g[s], e0, a.hidden);
+        sum_ranks<DT, NR, MODE>(a, x.first, at * kSize, e0, g[s]);
+        settle<DT, MODE>(g[s], e0, a.hidden);
         if (a.saved_scales) unpack_codes(x.codes, xh[s]);
         else unpack_raw<DT>(x.saved, xh[s]);
-        settle<DT, EXACT>(xh[s], e0, a.hidden);
+        settle<DT, MODE>(xh[s], e0, a.hidden);
         res[s] = x.res;
         float y[kPerLane];
-        unpack_gamma<DT, EXACT>(a, S < 4 ? gam[s] : load_gamma<DT, EXACT>(a, e0), e0, y);
+        unpack_gamma<DT, MODE>(a, S < 4 ? gam[s] : load_gamma<DT, MODE>(a, e0), e0, y);
 #pragma unroll
         for (int k = 0; k < kPerLane; ++k) {
           xh[s][k] *= rstd;
@@ -410,11 +412,11 @@ __global__ __launch_bounds__(kMaxThreads) void rmsnorm_bwd_kernel(NormArgs a, in
       if (a.residual) {
         float v[kPerLane];
         unpack_raw<DT>(res[s], v);
-        settle<DT, EXACT>(v, e0, a.hidden);
+        settle<DT, MODE>(v, e0, a.hidden);
 #pragma unroll
         for (int k = 0; k < kPerLane; ++k) g[s][k] += v[k];
       }
-      store_slot<DT, NR>(g[s], e0, a.hidden, a.n, [&](int r) { return static_cast<char*>(a.out[r]) + at * kSize; });
+      store_slot<DT, NR, MODE>(g[s], e0, a.hidden, a.n, [&](int r) { return static_cast<char*>(a.out[r]) + at * kSize; });
     }
   }
   if (teams > 1) {
@@ -503,40 +505,42 @@ int64_t groups_of(int64_t rows, const Shape& sh, int n) {
 
 constexpr int64_t kMaxGrid = 1 << 21;  // a launch has fewer than 2^32 threads
 
-template <int DT, int S, int NR, bool EXACT>
+template <int DT, int S, int NR, int MODE>
 hipError_t run(const NormArgs& a, bool bwd, const Shape& sh, hipStream_t s) {
   const int threads = sh.threads;
   if (bwd) {
-    hipLaunchKernelGGL((rmsnorm_bwd_kernel<DT, S, NR, EXACT>), dim3(static_cast<unsigned>(groups_of(a.rows, sh, a.n))),
+    hipLaunchKernelGGL((rmsnorm_bwd_kernel<DT, S, NR, MODE>), dim3(static_cast<unsigned>(groups_of(a.rows, sh, a.n))),
                        dim3(threads * teams_of(a.rows, sh)), 0, s, a, threads);
     return hipGetLastError();
   }
   for (int64_t row = 0; row < a.rows; row += kMaxGrid) {
     const int64_t rows = a.rows - row < kMaxGrid ? a.rows - row : kMaxGrid;
-    hipLaunchKernelGGL((rmsnorm_kernel<DT, S, NR, EXACT>), dim3(static_cast<unsigned>(rows)), dim3(threads), 0, s, a, row);
+    hipLaunchKernelGGL((rmsnorm_kernel<DT, S, NR, MODE>), dim3(static_cast<unsigned>(rows)), dim3(threads), 0, s, a, row);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
 }
-template <int DT, int S>
-hipError_t run_n(const NormArgs& a, bool bwd, const Shape& sh, hipStream_t s) {
+template <int DT, int S, int MODE> hipError_t run_n(const NormArgs& a, bool bwd, const Shape& sh, hipStream_t s) {
   switch (a.n) {
-    case 1: return run<DT, S, 1, false>(a, bwd, sh, s);
-    case 2: return run<DT, S, 2, false>(a, bwd, sh, s);
-    case 3: return run<DT, S, 3, false>(a, bwd, sh, s);
-    case 4: return run<DT, S, 4, false>(a, bwd, sh, s);
-    case 8: return run<DT, S, 8, false>(a, bwd, sh, s);
-    default: return run<DT, S, 0, false>(a, bwd, sh, s);
+    case 1: return run<DT, S, 1, MODE>(a, bwd, sh, s);
+    case 2: return run<DT, S, 2, MODE>(a, bwd, sh, s);
+    case 3: return run<DT, S, 3, MODE>(a, bwd, sh, s);
+    case 4: return run<DT, S, 4, MODE>(a, bwd, sh, s);
+    case 8: return run<DT, S, 8, MODE>(a, bwd, sh, s);
+    default: return run<DT, S, 0, MODE>(a, bwd, sh, s);
   }
 }
 
 template <int DT> hipError_t launch(const NormArgs& a, bool bwd, hipStream_t s) {
   const Shape sh = shape_of(a.hidden);
-  if (a.hidden < Traits<DT>::kVec) return run<DT, 1, 0, true>(a, bwd, sh, s);
-  if (sh.slots == 1) return run_n<DT, 1>(a, bwd, sh, s);
-  if (sh.slots == 2) return run_n<DT, 2>(a, bwd, sh, s);
-  return run_n<DT, 4>(a, bwd, sh, s);
+  const int64_t row = static_cast<int64_t>(a.hidden) * Traits<DT>::kSize;
+  if (a.hidden < Traits<DT>::kVec) return run<DT, 1, 0, kExact>(a, bwd, sh, s);
+  if (sh.slots == 1)
+    return streams(a.rows * row * (2 * a.n + 2), row) ? run_n<DT, 1, kStream>(a, bwd, sh, s)
+                                                      : run_n<DT, 1, kCached>(a, bwd, sh, s);
+  if (sh.slots == 2) return run_n<DT, 2, kCached>(a, bwd, sh, s);
+  return run_n<DT, 4, kCached>(a, bwd, sh, s);
 }
 
 }  // namespace

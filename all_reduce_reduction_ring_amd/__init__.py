@@ -433,6 +433,38 @@ def ar_version() -> int:
 
 
 # ------------------------------------------------------------------------------------------ block boundary
+_native = None  # the compiled argument checks; False where they cannot be loaded
+
+
+def _load_native():
+    """Load and bind the compiled argument checks (_marshal.so). They do what the checks below do, for arguments that
+    plainly fit, in a tenth of the time; without them every call goes through the ones below."""
+    global _native
+    L = lib()
+    try:
+        import torch
+        from . import _marshal
+        entries = (L.ar_allreduce_rmsnorm, L.ar_allreduce_rmsnorm_bwd, L.ar_expert_sort, L.ar_expert_dispatch,
+                   L.ar_expert_combine, L.ar_expert_combine_bwd)
+        _marshal.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in entries), torch._C._cuda_getDevice,
+                      torch._C._cuda_getCurrentRawStream)
+        _native = _marshal
+    except (ImportError, AttributeError) as e:
+        import warnings
+        warnings.warn(f"_marshal.so is missing or does not fit this torch ({e}): checking arguments in Python, slower")
+        _native = False
+    return _native
+
+
+def _done(rc, entry):
+    """Whether a compiled call went through (None: its arguments did not plainly fit); raises for an error status."""
+    if rc is None:
+        return False
+    if rc != AR_OK:
+        raise ArError(rc, entry)
+    return True
+
+
 def _addr(t, what, dtypes, shape, dev):
     """The address of a tensor that must be contiguous, of one of `dtypes`, of `shape`, on GPU `dev` (an index)."""
     if t.dtype not in dtypes:
@@ -494,6 +526,10 @@ def ar_allreduce_rmsnorm(ins, gamma, outs, residual=None, residual_out=None, rst
     [rows, hidden] tensors of the same dtype (outs[r] may be ins[r]), or, with out_scales (a list of float32
     [rows, ceil(hidden/128)]), of uint8 / float8_e4m3fn codes. residual_out receives the new residual (it may be
     `residual`), rstd float32 [rows], saved and saved_scales the new residual in 8 bits."""
+    native = _native if _native is not None else _load_native()
+    if native and _done(native.rmsnorm(ins, gamma, outs, residual, residual_out, rstd, out_scales, saved, saved_scales, eps,
+                                      stream), "ar_allreduce_rmsnorm"):
+        return
     kinds = _kinds()
     shape, dt, dev = _matrix(ins[0], "ins") if len(ins) else (None, None, -1)
     if shape is None:
@@ -527,6 +563,10 @@ def ar_allreduce_rmsnorm_bwd(ins, saved, gamma, rstd, outs, dgamma, saved_scales
     residual_out (or its 8-bit `saved`, with saved_scales), rstd the forward's. outs[r] receives the gradient of
     every rank's partial product and of the residual, dgamma (float32 [hidden]) the weight's. workspace: a GPU tensor
     of ar_allreduce_rmsnorm_bwd_workspace_size(rows, hidden) bytes."""
+    native = _native if _native is not None else _load_native()
+    if native and _done(native.rmsnorm_bwd(ins, saved, gamma, rstd, outs, dgamma, saved_scales, residual_grad, workspace,
+                                          stream), "ar_allreduce_rmsnorm_bwd"):
+        return
     kinds = _kinds()
     shape, dt, dev = _matrix(ins[0], "ins") if len(ins) else (None, None, -1)
     if shape is None:
@@ -565,6 +605,9 @@ def ar_expert_sort(ids, offsets, counts, pos, src, align=1, workspace=None, stre
     """Sort the slots ids[tokens, k] (int32; an id outside [0, experts) takes no row) by expert: offsets
     [experts + 1], counts [experts], pos [tokens, k] (a slot's row or -1) and src [rows] (a row's slot or -1), all
     int32. Segments start on multiples of `align`; rows >= ar_expert_rows(tokens, k, experts, align)."""
+    native = _native if _native is not None else _load_native()
+    if native and _done(native.expert_sort(ids, offsets, counts, pos, src, align, workspace, stream), "ar_expert_sort"):
+        return
     i32 = _kinds()[3]
     if ids.dim() != 2:
         raise ValueError("ids must be a matrix [tokens, k]")
@@ -594,6 +637,9 @@ def ar_expert_dispatch(x, pos, offsets, counts, xs, x_scales=None, xs_scales=Non
     """xs[pos[t, j]] = x[t] for the rows of x [tokens, hidden] (float32, bfloat16, float16, or uint8 /
     float8_e4m3fn with x_scales, whose rows go to xs_scales). The pad rows that offsets and counts describe are
     zeroed (both None: there are none)."""
+    native = _native if _native is not None else _load_native()
+    if native and _done(native.expert_dispatch(x, pos, offsets, counts, xs, x_scales, xs_scales, stream), "ar_expert_dispatch"):
+        return
     kinds = _kinds()
     if x.dim() != 2 or xs.dim() != 2 or pos.dim() != 2:
         raise ValueError("x, xs and pos must be matrices")
@@ -617,6 +663,9 @@ def ar_expert_dispatch(x, pos, offsets, counts, xs, x_scales=None, xs_scales=Non
 def ar_expert_combine(ys, pos, out, weights=None, addend=None, stream=None):
     """out[t] = sum_j weights[t, j] ys[pos[t, j]] + addend[t]; weights float32 [tokens, k] (None: 1, the gradient of
     ar_expert_dispatch), addend [tokens, hidden] (may be `out`)."""
+    native = _native if _native is not None else _load_native()
+    if native and _done(native.expert_combine(ys, pos, out, weights, addend, stream), "ar_expert_combine"):
+        return
     kinds = _kinds()
     shape, dt, dev = _matrix(out, "out")
     if ys.dim() != 2 or pos.dim() != 2:
@@ -634,6 +683,9 @@ def ar_expert_combine(ys, pos, out, weights=None, addend=None, stream=None):
 def ar_expert_combine_bwd(dout, ys, pos, weights, offsets, counts, dys, dweights, stream=None):
     """The gradient of ar_expert_combine: dys[pos[t, j]] = weights[t, j] dout[t] (pad rows zeroed as in
     ar_expert_dispatch; dys may be ys) and dweights[t, j] = <dout[t], ys[pos[t, j]]> (float32 [tokens, k])."""
+    native = _native if _native is not None else _load_native()
+    if native and _done(native.expert_combine_bwd(dout, ys, pos, weights, offsets, counts, dys, dweights, stream), "ar_expert_combine_bwd"):
+        return
     kinds = _kinds()
     shape, dt, dev = _matrix(dout, "dout")
     if ys.dim() != 2 or pos.dim() != 2:

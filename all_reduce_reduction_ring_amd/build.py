@@ -1,4 +1,4 @@
-"""Build libar.so (HIP, gfx950) in-tree with hipcc.
+"""Build libar.so (HIP, gfx950) in-tree with hipcc, and the binding's compiled argument checks with g++.
 
 Every source under csrc/ is compiled for gfx950 only, with IEEE fp32 semantics kept intact
 (-ffp-contract=off: no a*b+c contraction anywhere, so sums and the fp8 quantize/dequantize round trips are
@@ -22,6 +22,9 @@ LIB = os.path.join(HERE, "libar.so")
 # library of their own, so that nothing in libar exists only to be measured
 CEILING_SRC = "ar_ceiling.hip"
 CEILING_LIB = os.path.join(HERE, "libar_ceiling.so")
+# the argument checks of the block-boundary entry points for torch tensors (host code, a CPython module)
+MARSHAL_SRC = "ar_marshal.cpp"
+MARSHAL_LIB = os.path.join(HERE, "_marshal.so")
 ARCH = "gfx950"
 
 SOURCES = ["ar_api.hip", "ar_collapsed.hip", "ar_stepwise.hip", "ar_bucket.hip", "ar_fp8.hip", "ar_tensors.hip",
@@ -71,9 +74,28 @@ def _link(objs, out):
     os.replace(tmp, out)
 
 
+def _build_marshal() -> None:
+    import sysconfig
+
+    import torch
+
+    home = os.path.dirname(torch.__file__)
+    tmp = MARSHAL_LIB + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", "-I", os.path.join(ROOT, "include"),
+           "-isystem", os.path.join(home, "include"), "-isystem", sysconfig.get_paths()["include"],
+           os.path.join(CSRC, MARSHAL_SRC), "-o", tmp, "-L", os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cpu",
+           "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {MARSHAL_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, MARSHAL_LIB)
+
+
 def build(jobs: int | None = None) -> str:
-    """Compile every source and link libar.so (and libar_ceiling.so); returns libar's path."""
+    """Compile every source and link libar.so (and libar_ceiling.so and _marshal.so); returns libar's path."""
     os.makedirs(BUILD, exist_ok=True)
+    _build_marshal()
     units = UNITS + [(CEILING_SRC, [])]
     jobs = jobs or min(len(units), max(1, (os.cpu_count() or 4)))
     # the slowest units first, so they are not left running alone at the end

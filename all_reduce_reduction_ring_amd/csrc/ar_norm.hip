@@ -307,7 +307,7 @@ template <int DT, int NR, int MODE> struct BwdSlot {
   RankSlots<DT, NR, MODE> first;
   Raw<DT> saved, res;
   RawCodes codes;
-  __device__ __forceinline__ void load(const NormArgs& a, int64_t row, int e0) {
+  __device__ __forceinline__ void load(const NormArgs& a, int64_t row, int e0, bool residual) {
     constexpr int kSize = Traits<DT>::kSize;
     const int64_t at = row * a.hidden;
     first.load(a, at * kSize, e0, 0);
@@ -316,25 +316,70 @@ template <int DT, int NR, int MODE> struct BwdSlot {
                                     a.saved_scales + row * ((a.hidden + kBlock - 1) / kBlock), e0, a.hidden);
     else
       saved = load_raw<DT, MODE>(static_cast<const char*>(a.saved) + at * kSize, e0, a.hidden);
-    if (a.residual) res = load_raw<DT, MODE>(static_cast<const char*>(a.residual) + at * kSize, e0, a.hidden);
+    if (residual) res = load_raw<DT, MODE>(static_cast<const char*>(a.residual) + at * kSize, e0, a.hidden);
   }
 };
+
+// dgamma of one 128-element block of columns by a whole workgroup: 16 lanes to a row, every row once.
+template <int DT, int NR, int MODE>
+__device__ __forceinline__ void columns_dgamma(const NormArgs& a, int block, float* lds, float* dgamma) {
+  constexpr int V = Traits<DT>::kVec;
+  const int lane = threadIdx.x & 15, at_once = static_cast<int>(blockDim.x) >> 4;
+  const int e0 = first_of<DT>(block * 16 + lane);
+  float dg[kPerLane];
+#pragma unroll
+  for (int k = 0; k < kPerLane; ++k) dg[k] = 0.0f;
+  for (int64_t row = threadIdx.x >> 4; row < a.rows; row += at_once) {
+    BwdSlot<DT, NR, MODE> x;
+    x.load(a, row, e0, false);
+    const float rstd = gptr<float>(a.rstd_in)[row];
+    float g[kPerLane], xh[kPerLane];
+    sum_ranks<DT, NR, MODE>(a, x.first, row * a.hidden * Traits<DT>::kSize, e0, g);
+    if (a.saved_scales) unpack_codes(x.codes, xh);
+    else unpack_raw<DT>(x.saved, xh);
+#pragma unroll
+    for (int k = 0; k < kPerLane; ++k) dg[k] += g[k] * (xh[k] * rstd);
+  }
+  settle<DT, MODE>(dg, e0, a.hidden);
+#pragma unroll
+  for (int k = 0; k < kPerLane; ++k) {
+    dg[k] += __shfl_xor(dg[k], 16, 64);
+    dg[k] += __shfl_xor(dg[k], 32, 64);
+    if ((threadIdx.x & 63) < 16) lds[(threadIdx.x >> 6) * kBlock + lane * kPerLane + k] = dg[k];
+  }
+  __syncthreads();
+  if (threadIdx.x < kBlock) {
+    float sum = 0.0f;
+    for (int w = 0; w < static_cast<int>(blockDim.x) >> 6; ++w) sum += lds[w * kBlock + threadIdx.x];
+    const int k = threadIdx.x % kPerLane;
+    const int e = vec_at(first_of<DT>(block * 16 + static_cast<int>(threadIdx.x) / kPerLane), k / V) + k % V;
+    if (e < a.hidden) gptr<float>(dgamma)[e] = sum;
+  }
+}
 
 // A workgroup holds R teams of threads, each of which takes a row at a time: team i of workgroup b the rows
 // b R + i, + groups R, + 2 groups R, ... Every thread keeps its columns' sums of dy xhat in registers over all its rows;
 // the teams' sums are joined in LDS and leave as one row of partial sums per workgroup, which dgamma_kernel adds up in
 // order. One slot a lane (S = 1): the next row is read while this one's dot product is joined and its results are
 // stored. Wider rows (S > 1) have one team and read their row when its turn comes.
-template <int DT, int S, int NR, int MODE>
-__global__ __launch_bounds__(kMaxThreads) void rmsnorm_bwd_kernel(NormArgs a, int team_threads) {
+// SMALL: no second launch; the workgroups from `groups` on each sum a block of columns instead, reading those again.
+template <int DT, int S, int NR, int MODE, bool SMALL>
+__global__ __launch_bounds__(kMaxThreads) void rmsnorm_bwd_kernel(NormArgs a, int team_threads, int groups,
+                                                                  float* dgamma) {
   constexpr bool kAhead = S == 1 && (Traits<DT>::kSize == 2 || NR < 8);
   __shared__ float lds[2][kMaxThreads / 64];
   __shared__ float join[S == 1 ? kTeamThreads * kPerLane : 1];
   constexpr int kSize = Traits<DT>::kSize;
+  if constexpr (SMALL) {
+    if (static_cast<int>(blockIdx.x) >= groups) {
+      columns_dgamma<DT, NR, MODE>(a, static_cast<int>(blockIdx.x) - groups, join, dgamma);
+      return;
+    }
+  }
   const int teams = S == 1 ? static_cast<int>(blockDim.x) / team_threads : 1;
   const int team = S == 1 ? __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / team_threads) : 0;
   const int tid = static_cast<int>(threadIdx.x) - team * team_threads;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * teams;
+  const int64_t step = static_cast<int64_t>(groups) * teams;
   float dg[S][kPerLane];
   RawGamma gam[S];
 #pragma unroll
@@ -348,7 +393,7 @@ __global__ __launch_bounds__(kMaxThreads) void rmsnorm_bwd_kernel(NormArgs a, in
   float rstd_next = 0.0f;
   int64_t base = static_cast<int64_t>(blockIdx.x) * teams;
   if (kAhead && base + team < a.rows) {
-    next.load(a, base + team, first_of<DT>(tid));
+    next.load(a, base + team, first_of<DT>(tid), a.residual);
     rstd_next = gptr<float>(a.rstd_in)[base + team];
   }
   for (; base < a.rows; base += step, flip ^= 1) {  // all teams stay in the loop for the barriers in it
@@ -364,7 +409,7 @@ __global__ __launch_bounds__(kMaxThreads) void rmsnorm_bwd_kernel(NormArgs a, in
         const int e0 = first_of<DT>(s * team_threads + tid);
         BwdSlot<DT, NR, MODE> x;
         if (kAhead) x = next;
-        else x.load(a, row, e0);
+        else x.load(a, row, e0, a.residual);
         sum_ranks<DT, NR, MODE>(a, x.first, at * kSize, e0, g[s]);
         settle<DT, MODE>(g[s], e0, a.hidden);
         if (a.saved_scales) unpack_codes(x.codes, xh[s]);
@@ -390,7 +435,7 @@ __global__ __launch_bounds__(kMaxThreads) void rmsnorm_bwd_kernel(NormArgs a, in
           for (int v = 0; v < kVecs<DT>; ++v) arrived(res[s].w[v]);
       }
       if (kAhead && row + step < a.rows) {
-        next.load(a, row + step, first_of<DT>(tid));
+        next.load(a, row + step, first_of<DT>(tid), a.residual);
         rstd_next = gptr<float>(a.rstd_in)[row + step];
       }
     }
@@ -419,6 +464,7 @@ __global__ __launch_bounds__(kMaxThreads) void rmsnorm_bwd_kernel(NormArgs a, in
       store_slot<DT, NR, MODE>(g[s], e0, a.hidden, a.n, [&](int r) { return static_cast<char*>(a.out[r]) + at * kSize; });
     }
   }
+  if constexpr (SMALL) return;
   if (teams > 1) {
     const int others = team_threads * (teams - 1);
     if (team > 0) {
@@ -505,42 +551,90 @@ int64_t groups_of(int64_t rows, const Shape& sh, int n) {
 
 constexpr int64_t kMaxGrid = 1 << 21;  // a launch has fewer than 2^32 threads
 
+// Backward without partial sums, in one launch: dgamma's columns read the ranks' rows and the saved ones a second time.
+// Up to 256 rows and 24 MiB read twice (two launches against one: 1 row of 4096, 8 ranks 8.2 / 4.0 us, 128 of 1000, 2
+// ranks 6.7 / 4.6, 256 of 4096, 8 ranks 15.7 / 14.7; beyond: 512 of 1000, 2 ranks 7.8 / 9.4, 512 of 4096, 8 ranks
+// 20.6 / 29.4).
+bool reads_twice(const NormArgs& a, const Shape& sh, int size) {
+  return sh.slots == 1 && a.rows <= 256 && a.rows * a.hidden * size * (a.n + 1) <= (24 << 20);
+}
+bool over_inputs(const NormArgs& a) {
+  for (int r = 0; r < a.n; ++r)
+    for (int i = 0; i < a.n; ++i)
+      if (a.out[r] == a.in[i]) return true;
+  return false;
+}
+
 template <int DT, int S, int NR, int MODE>
-hipError_t run(const NormArgs& a, bool bwd, const Shape& sh, hipStream_t s) {
-  const int threads = sh.threads;
-  if (bwd) {
-    hipLaunchKernelGGL((rmsnorm_bwd_kernel<DT, S, NR, MODE>), dim3(static_cast<unsigned>(groups_of(a.rows, sh, a.n))),
-                       dim3(threads * teams_of(a.rows, sh)), 0, s, a, threads);
-    return hipGetLastError();
+hipError_t run_bwd(const NormArgs& a, const Shape& sh, float* dgamma, hipStream_t s) {
+  if constexpr (S == 1 && MODE != kStream) {
+    if (reads_twice(a, sh, Traits<DT>::kSize)) {
+      const int teams = kMaxThreads / sh.threads, blocks = (a.hidden + kBlock - 1) / kBlock;
+      const int groups = static_cast<int>((a.rows + teams - 1) / teams);
+      const dim3 block(teams * sh.threads);
+      if (groups > 0 && over_inputs(a)) {  // all columns first, then the rows that overwrite what those read
+        hipLaunchKernelGGL((rmsnorm_bwd_kernel<DT, S, NR, MODE, true>), dim3(blocks), block, 0, s, a, sh.threads, 0,
+                           dgamma);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        hipLaunchKernelGGL((rmsnorm_bwd_kernel<DT, S, NR, MODE, true>), dim3(groups), block, 0, s, a, sh.threads, groups,
+                           dgamma);
+        return hipGetLastError();
+      }
+      hipLaunchKernelGGL((rmsnorm_bwd_kernel<DT, S, NR, MODE, true>), dim3(groups + blocks), block, 0, s, a, sh.threads,
+                         groups, dgamma);
+      return hipGetLastError();
+    }
   }
+  const int teams = teams_of(a.rows, sh), groups = static_cast<int>(groups_of(a.rows, sh, a.n));
+  if (groups > 0) {
+    hipLaunchKernelGGL((rmsnorm_bwd_kernel<DT, S, NR, MODE, false>), dim3(groups), dim3(teams * sh.threads), 0, s, a,
+                       sh.threads, groups, nullptr);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL(dgamma_kernel, dim3((a.hidden + kSumColumns - 1) / kSumColumns), dim3(1024), 0, s, a.partial,
+                     static_cast<int64_t>(groups), a.hidden, dgamma);
+  return hipGetLastError();
+}
+
+template <int DT, int S, int NR, int MODE>
+hipError_t run_fwd(const NormArgs& a, const Shape& sh, hipStream_t s) {
   for (int64_t row = 0; row < a.rows; row += kMaxGrid) {
     const int64_t rows = a.rows - row < kMaxGrid ? a.rows - row : kMaxGrid;
-    hipLaunchKernelGGL((rmsnorm_kernel<DT, S, NR, MODE>), dim3(static_cast<unsigned>(rows)), dim3(threads), 0, s, a, row);
+    hipLaunchKernelGGL((rmsnorm_kernel<DT, S, NR, MODE>), dim3(static_cast<unsigned>(rows)), dim3(sh.threads), 0, s, a,
+                       row);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
 }
-template <int DT, int S, int MODE> hipError_t run_n(const NormArgs& a, bool bwd, const Shape& sh, hipStream_t s) {
+
+// dgamma: of the backward pass; null for the forward
+template <int DT, int S, int NR, int MODE>
+hipError_t run(const NormArgs& a, float* dgamma, const Shape& sh, hipStream_t s) {
+  return dgamma ? run_bwd<DT, S, NR, MODE>(a, sh, dgamma, s) : run_fwd<DT, S, NR, MODE>(a, sh, s);
+}
+template <int DT, int S, int MODE> hipError_t run_n(const NormArgs& a, float* dgamma, const Shape& sh, hipStream_t s) {
   switch (a.n) {
-    case 1: return run<DT, S, 1, MODE>(a, bwd, sh, s);
-    case 2: return run<DT, S, 2, MODE>(a, bwd, sh, s);
-    case 3: return run<DT, S, 3, MODE>(a, bwd, sh, s);
-    case 4: return run<DT, S, 4, MODE>(a, bwd, sh, s);
-    case 8: return run<DT, S, 8, MODE>(a, bwd, sh, s);
-    default: return run<DT, S, 0, MODE>(a, bwd, sh, s);
+    case 1: return run<DT, S, 1, MODE>(a, dgamma, sh, s);
+    case 2: return run<DT, S, 2, MODE>(a, dgamma, sh, s);
+    case 3: return run<DT, S, 3, MODE>(a, dgamma, sh, s);
+    case 4: return run<DT, S, 4, MODE>(a, dgamma, sh, s);
+    case 8: return run<DT, S, 8, MODE>(a, dgamma, sh, s);
+    default: return run<DT, S, 0, MODE>(a, dgamma, sh, s);
   }
 }
 
-template <int DT> hipError_t launch(const NormArgs& a, bool bwd, hipStream_t s) {
+template <int DT> hipError_t launch(const NormArgs& a, float* dgamma, hipStream_t s) {
   const Shape sh = shape_of(a.hidden);
   const int64_t row = static_cast<int64_t>(a.hidden) * Traits<DT>::kSize;
-  if (a.hidden < Traits<DT>::kVec) return run<DT, 1, 0, kExact>(a, bwd, sh, s);
+  if (a.hidden < Traits<DT>::kVec) return run<DT, 1, 0, kExact>(a, dgamma, sh, s);
   if (sh.slots == 1)
-    return streams(a.rows * row * (2 * a.n + 2), row) ? run_n<DT, 1, kStream>(a, bwd, sh, s)
-                                                      : run_n<DT, 1, kCached>(a, bwd, sh, s);
-  if (sh.slots == 2) return run_n<DT, 2, kCached>(a, bwd, sh, s);
-  return run_n<DT, 4, kCached>(a, bwd, sh, s);
+    return streams(a.rows * row * (2 * a.n + 2), row) ? run_n<DT, 1, kStream>(a, dgamma, sh, s)
+                                                      : run_n<DT, 1, kCached>(a, dgamma, sh, s);
+  if (sh.slots == 2) return run_n<DT, 2, kCached>(a, dgamma, sh, s);
+  return run_n<DT, 4, kCached>(a, dgamma, sh, s);
 }
 
 }  // namespace
@@ -550,28 +644,16 @@ int64_t rmsnorm_bwd_groups(int64_t rows, int64_t hidden, int n) {
 }
 
 hipError_t launch_rmsnorm(const NormArgs& a, int dtype, hipStream_t s) {
-  switch (dtype) {
-    case AR_F32: return launch<AR_F32>(a, false, s);
-    case AR_BF16: return launch<AR_BF16>(a, false, s);
-    case AR_F16: return launch<AR_F16>(a, false, s);
-    default: return hipErrorInvalidValue;
-  }
+  return launch_rmsnorm_bwd(a, dtype, nullptr, s);
 }
 
 hipError_t launch_rmsnorm_bwd(const NormArgs& a, int dtype, float* dgamma, hipStream_t s) {
-  const int64_t groups = rmsnorm_bwd_groups(a.rows, a.hidden, a.n);
-  hipError_t e = hipSuccess;
-  if (groups > 0) {
-    switch (dtype) {
-      case AR_F32: e = launch<AR_F32>(a, true, s); break;
-      case AR_BF16: e = launch<AR_BF16>(a, true, s); break;
-      case AR_F16: e = launch<AR_F16>(a, true, s); break;
-      default: return hipErrorInvalidValue;
-    }
+  switch (dtype) {
+    case AR_F32: return launch<AR_F32>(a, dgamma, s);
+    case AR_BF16: return launch<AR_BF16>(a, dgamma, s);
+    case AR_F16: return launch<AR_F16>(a, dgamma, s);
+    default: return hipErrorInvalidValue;
   }
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(dgamma_kernel, dim3((a.hidden + kSumColumns - 1) / kSumColumns), dim3(1024), 0, s, a.partial, groups, a.hidden, dgamma);
-  return hipGetLastError();
 }
 
 }  // namespace ar

@@ -338,7 +338,7 @@ int ar_allreduce_rmsnorm(const void* const* in_bufs, int nranks, size_t rows, si
 /* The gradient of ar_allreduce_rmsnorm. With dy = dy_0 + ... + dy_{N-1} (the ranks' partial gradients of y, fp32, in
  * rank order), h as saved and xhat = h * rstd:
  *   g = dy * gamma,   dx = rstd * (g - xhat * mean over the row of g * xhat) + residual_grad
- *   dgamma = sum over the rows of dy * xhat   (fp32; the order is fixed by rows and hidden alone)
+ *   dgamma = sum over the rows of dy * xhat   (fp32, in an order fixed by nranks, rows, hidden and dtype)
  * dx is the gradient of every x_r and of the residual; it goes to every rank.
  *   in_bufs: host array of nranks device pointers to [rows][hidden], the dy_r.
  *   saved: saved_scales NULL: h as [rows][hidden] of dtype (the forward's residual_out). Otherwise its 8-bit form.

@@ -140,7 +140,7 @@ __device__ __forceinline__ void unpack_codes(const RawCodes& r, float (&v)[kPerL
 struct RawGamma {
   u32x4 w[2];
 };
-template <int DT, int MODE> __device__ __forceinline__ RawGamma load_gamma(const NormArgs& a, int e0) {
+template <int DT, int MODE> __device__ __forceinline__ RawGamma load_gamma(const NormCommon& a, int e0) {
   RawGamma r;
   if (Traits<DT>::kSize == 2 && a.gamma_f32) {
     const uint32_t at = clamped<kPerLane>(e0, a.hidden) * 4;
@@ -159,7 +159,7 @@ template <int DT, int MODE> __device__ __forceinline__ RawGamma load_gamma(const
   return r;
 }
 template <int DT, int MODE>
-__device__ __forceinline__ void unpack_gamma(const NormArgs& a, const RawGamma& r, int e0, float (&v)[kPerLane]) {
+__device__ __forceinline__ void unpack_gamma(const NormCommon& a, const RawGamma& r, int e0, float (&v)[kPerLane]) {
   if (Traits<DT>::kSize == 2 && !a.gamma_f32) {
     Slot<Traits<DT>::kSize == 2 ? DT : AR_BF16>::unpack(r.w[0], v);
   } else {
@@ -183,6 +183,19 @@ __device__ __forceinline__ float group_sum(float v, float* lds) {
 }
 
 constexpr int kMaxThreads = 1024;
+constexpr int kFewRanks = 8;
+// The arguments that the kernels for NR ranks take (NR 0: any number).
+template <int NR> using ArgsFor = NormArgsOf<NR == 0 ? AR_MAX_RANKS : kFewRanks>;
+template <int NR> ArgsFor<NR> args_for(const NormArgs& a) {
+  ArgsFor<NR> b;
+  static_cast<NormCommon&>(b) = a;
+  for (int r = 0; r < (NR == 0 ? AR_MAX_RANKS : NR); ++r) {
+    b.in[r] = a.in[r];
+    b.out[r] = a.out[r];
+    b.out_scales[r] = a.out_scales[r];
+  }
+  return b;
+}
 constexpr int kRankBatch = 4;
 constexpr int kTeamThreads = 512;  // a backward workgroup of several teams
 constexpr int kMaxTeams = 8;
@@ -192,13 +205,13 @@ constexpr int kMaxTeams = 8;
 template <int DT, int NR, int MODE> struct RankSlots {
   static constexpr int kBatch = NR > 0 ? NR : kRankBatch;
   Raw<DT> raw[kBatch];
-  __device__ __forceinline__ void load(const NormArgs& a, int64_t off, int e0, int r0) {
+  __device__ __forceinline__ void load(const ArgsFor<NR>& a, int64_t off, int e0, int r0) {
 #pragma unroll
     for (int r = 0; r < kBatch; ++r)
       if (NR > 0 || r0 + r < a.n)
         raw[r] = load_raw<DT, MODE>(static_cast<const char*>(a.in[r0 + r]) + off, e0, a.hidden);
   }
-  __device__ __forceinline__ void add(const NormArgs& a, int r0, float (&h)[kPerLane]) const {
+  __device__ __forceinline__ void add(const ArgsFor<NR>& a, int r0, float (&h)[kPerLane]) const {
 #pragma unroll
     for (int r = 0; r < kBatch; ++r) {
       if (NR > 0 || r0 + r < a.n) {
@@ -213,7 +226,7 @@ template <int DT, int NR, int MODE> struct RankSlots {
 
 // h = the sum of the ranks' slots, the first ones already on their way.
 template <int DT, int NR, int MODE>
-__device__ __forceinline__ void sum_ranks(const NormArgs& a, const RankSlots<DT, NR, MODE>& first, int64_t off, int e0,
+__device__ __forceinline__ void sum_ranks(const ArgsFor<NR>& a, const RankSlots<DT, NR, MODE>& first, int64_t off, int e0,
                                           float (&h)[kPerLane]) {
   first.add(a, 0, h);
   if constexpr (NR == 0) {
@@ -240,7 +253,7 @@ __device__ __forceinline__ void quant8(const float (&v)[kPerLane], float* scale,
 
 // One workgroup, one row.
 template <int DT, int S, int NR, int MODE>
-__global__ __launch_bounds__(kMaxThreads) void rmsnorm_kernel(NormArgs a, int64_t row0) {
+__global__ __launch_bounds__(kMaxThreads) void rmsnorm_kernel(ArgsFor<NR> a, int64_t row0) {
   __shared__ float lds[kMaxThreads / 64];
   constexpr int kSize = Traits<DT>::kSize;
   const int nb = (a.hidden + kBlock - 1) / kBlock, threads = static_cast<int>(blockDim.x);
@@ -307,7 +320,7 @@ template <int DT, int NR, int MODE> struct BwdSlot {
   RankSlots<DT, NR, MODE> first;
   Raw<DT> saved, res;
   RawCodes codes;
-  __device__ __forceinline__ void load(const NormArgs& a, int64_t row, int e0, bool residual) {
+  __device__ __forceinline__ void load(const ArgsFor<NR>& a, int64_t row, int e0, bool residual) {
     constexpr int kSize = Traits<DT>::kSize;
     const int64_t at = row * a.hidden;
     first.load(a, at * kSize, e0, 0);
@@ -322,7 +335,7 @@ template <int DT, int NR, int MODE> struct BwdSlot {
 
 // dgamma of one 128-element block of columns by a whole workgroup: 16 lanes to a row, every row once.
 template <int DT, int NR, int MODE>
-__device__ __forceinline__ void columns_dgamma(const NormArgs& a, int block, float* lds, float* dgamma) {
+__device__ __forceinline__ void columns_dgamma(const ArgsFor<NR>& a, int block, float* lds, float* dgamma) {
   constexpr int V = Traits<DT>::kVec;
   const int lane = threadIdx.x & 15, at_once = static_cast<int>(blockDim.x) >> 4;
   const int e0 = first_of<DT>(block * 16 + lane);
@@ -364,7 +377,7 @@ __device__ __forceinline__ void columns_dgamma(const NormArgs& a, int block, flo
 // stored. Wider rows (S > 1) have one team and read their row when its turn comes.
 // SMALL: no second launch; the workgroups from `groups` on each sum a block of columns instead, reading those again.
 template <int DT, int S, int NR, int MODE, bool SMALL>
-__global__ __launch_bounds__(kMaxThreads) void rmsnorm_bwd_kernel(NormArgs a, int team_threads, int groups,
+__global__ __launch_bounds__(kMaxThreads) void rmsnorm_bwd_kernel(ArgsFor<NR> a, int team_threads, int groups,
                                                                   float* dgamma) {
   constexpr bool kAhead = S == 1 && (Traits<DT>::kSize == 2 || NR < 8);
   __shared__ float lds[2][kMaxThreads / 64];
@@ -573,22 +586,22 @@ hipError_t run_bwd(const NormArgs& a, const Shape& sh, float* dgamma, hipStream_
       const int groups = static_cast<int>((a.rows + teams - 1) / teams);
       const dim3 block(teams * sh.threads);
       if (groups > 0 && over_inputs(a)) {  // all columns first, then the rows that overwrite what those read
-        hipLaunchKernelGGL((rmsnorm_bwd_kernel<DT, S, NR, MODE, true>), dim3(blocks), block, 0, s, a, sh.threads, 0,
+        hipLaunchKernelGGL((rmsnorm_bwd_kernel<DT, S, NR, MODE, true>), dim3(blocks), block, 0, s, args_for<NR>(a), sh.threads, 0,
                            dgamma);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
-        hipLaunchKernelGGL((rmsnorm_bwd_kernel<DT, S, NR, MODE, true>), dim3(groups), block, 0, s, a, sh.threads, groups,
+        hipLaunchKernelGGL((rmsnorm_bwd_kernel<DT, S, NR, MODE, true>), dim3(groups), block, 0, s, args_for<NR>(a), sh.threads, groups,
                            dgamma);
         return hipGetLastError();
       }
-      hipLaunchKernelGGL((rmsnorm_bwd_kernel<DT, S, NR, MODE, true>), dim3(groups + blocks), block, 0, s, a, sh.threads,
+      hipLaunchKernelGGL((rmsnorm_bwd_kernel<DT, S, NR, MODE, true>), dim3(groups + blocks), block, 0, s, args_for<NR>(a), sh.threads,
                          groups, dgamma);
       return hipGetLastError();
     }
   }
   const int teams = teams_of(a.rows, sh), groups = static_cast<int>(groups_of(a.rows, sh, a.n));
   if (groups > 0) {
-    hipLaunchKernelGGL((rmsnorm_bwd_kernel<DT, S, NR, MODE, false>), dim3(groups), dim3(teams * sh.threads), 0, s, a,
+    hipLaunchKernelGGL((rmsnorm_bwd_kernel<DT, S, NR, MODE, false>), dim3(groups), dim3(teams * sh.threads), 0, s, args_for<NR>(a),
                        sh.threads, groups, nullptr);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -602,7 +615,7 @@ template <int DT, int S, int NR, int MODE>
 hipError_t run_fwd(const NormArgs& a, const Shape& sh, hipStream_t s) {
   for (int64_t row = 0; row < a.rows; row += kMaxGrid) {
     const int64_t rows = a.rows - row < kMaxGrid ? a.rows - row : kMaxGrid;
-    hipLaunchKernelGGL((rmsnorm_kernel<DT, S, NR, MODE>), dim3(static_cast<unsigned>(rows)), dim3(sh.threads), 0, s, a,
+    hipLaunchKernelGGL((rmsnorm_kernel<DT, S, NR, MODE>), dim3(static_cast<unsigned>(rows)), dim3(sh.threads), 0, s, args_for<NR>(a),
                        row);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;

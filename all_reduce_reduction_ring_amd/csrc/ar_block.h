@@ -195,4 +195,16 @@ __device__ __forceinline__ float wave_sum(float v) {
   return (row(0) + row(16)) + (row(32) + row(48));
 }
 
+// Sum over the LANES lanes (8, 16 or 32) that share a row, in each of them; they are active or not together.
+template <int LANES> __device__ __forceinline__ float lanes_sum(float v) {
+  auto step = [](float x, int y) { return x + __int_as_float(y); };
+  v = step(v, __builtin_amdgcn_update_dpp(0, __float_as_int(v), 0xB1, 0xF, 0xF, false));   // quad_perm [1,0,3,2]
+  v = step(v, __builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x4E, 0xF, 0xF, false));   // quad_perm [2,3,0,1]
+  v = step(v, __builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x141, 0xF, 0xF, false));  // row_half_mirror
+  if constexpr (LANES >= 16)
+    v = step(v, __builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x140, 0xF, 0xF, false));  // row_mirror
+  if constexpr (LANES >= 32) v += __shfl_xor(v, 16, 64);
+  return v;
+}
+
 }  // namespace ar

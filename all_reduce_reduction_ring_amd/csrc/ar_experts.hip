@@ -456,6 +456,145 @@ int64_t sort_tile(int64_t slots) {
   return (even + kSortThreads - 1) / kSortThreads * kSortThreads;
 }
 
+// ------------------------------------------------------------------------------------------ short rows
+// Rows of up to 32 vectors: LANES lanes (8, 16 or 32) take a token, one vector a lane, several tokens a wave. A wave per
+// token leaves most lanes idle there, and the kernels wait for one chain of loads after another: positions, rows. 16,384
+// tokens of 4 choices, bf16, against a wave per token: 64 wide, combine 13.3 -> 3.7 us, its gradient 25.5 -> 6.1, sort
+// and dispatch 19.3 -> 11.7; 256 wide, 14.1 -> 9.4, 26.1 -> 15.1, 21.2 -> 17.1.
+constexpr int kShortThreads = 256;
+
+// The rows of choices j0 .. j0 + 7 of token t (-1: none), one register each.
+__device__ __forceinline__ void load_rows_each(const MoveArgs& a, int64_t t, int j0, int (&p)[kChoices]) {
+#pragma unroll
+  for (int j = 0; j < kChoices; ++j) p[j] = j0 + j < a.k ? gptr<int32_t>(a.pos + t * a.k)[j0 + j] : -1;
+#pragma unroll
+  for (int j = 0; j < kChoices; ++j) p[j] = p[j] >= 0 && p[j] < a.rows ? p[j] : -1;
+}
+
+template <int LANES>
+__global__ __launch_bounds__(kShortThreads) void dispatch_short_kernel(MoveArgs a, int row_bytes, int scale_bytes,
+                                                                       int pad_groups, int pad_parts) {
+  if (static_cast<int>(blockIdx.x) < pad_groups) {
+    zero_pads(a, static_cast<int>(blockIdx.x), pad_parts, row_bytes, scale_bytes);
+    return;
+  }
+  constexpr int kTokens = kShortThreads / LANES;
+  const int lane = threadIdx.x % LANES;
+  for (int64_t t = static_cast<int64_t>(blockIdx.x - pad_groups) * kTokens + threadIdx.x / LANES; t < a.tokens;
+       t += static_cast<int64_t>(gridDim.x - pad_groups) * kTokens) {
+    const int64_t at = clamped<16>(lane * 16, row_bytes);
+    const u32x4 v = ldu16(static_cast<const char*>(a.x) + t * row_bytes + at);
+    uint32_t sc = 0;
+    if (lane * 4 < scale_bytes) sc = *gptr<uint32_t>(static_cast<const char*>(a.x_scales) + t * scale_bytes + lane * 4);
+    for (int j0 = 0; j0 < a.k; j0 += kChoices) {
+      int p[kChoices];
+      load_rows_each(a, t, j0, p);
+#pragma unroll
+      for (int j = 0; j < kChoices; ++j) {
+        if (p[j] < 0) continue;
+        if (lane * 16 < row_bytes) stu16(static_cast<char*>(a.y) + p[j] * static_cast<int64_t>(row_bytes) + at, v);
+        if (lane * 4 < scale_bytes)
+          *gptr<uint32_t>(static_cast<char*>(a.y_scales) + p[j] * static_cast<int64_t>(scale_bytes) + lane * 4) = sc;
+      }
+    }
+  }
+}
+
+template <int DT, int LANES, int MODE>
+__global__ __launch_bounds__(kShortThreads) void combine_short_kernel(MoveArgs a) {
+  constexpr int V = Traits<DT>::kVec, kTokens = kShortThreads / LANES;
+  const int64_t row = static_cast<int64_t>(a.hidden) * Traits<DT>::kSize;
+  const int e = static_cast<int>(threadIdx.x) % LANES * V;
+  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kTokens + threadIdx.x / LANES; t < a.tokens;
+       t += static_cast<int64_t>(gridDim.x) * kTokens) {
+    float acc[V];
+    u32x4 add = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] = 0.0f;
+    if (a.extra) add = load_vec<DT, MODE>(static_cast<const char*>(a.extra) + t * row, e, a.hidden);
+    for (int j0 = 0; j0 < a.k; j0 += kChoices) {
+      int p[kChoices];
+      float w[kChoices];
+      load_rows_each(a, t, j0, p);
+#pragma unroll
+      for (int j = 0; j < kChoices; ++j) w[j] = a.weights && j0 + j < a.k ? gptr<float>(a.weights + t * a.k)[j0 + j] : 1.0f;
+      u32x4 x[kChoices];
+#pragma unroll
+      for (int j = 0; j < kChoices; ++j)
+        if (p[j] >= 0) x[j] = load_vec<DT, MODE>(static_cast<const char*>(a.x) + p[j] * row, e, a.hidden);
+#pragma unroll
+      for (int j = 0; j < kChoices; ++j) {
+        if (p[j] < 0) continue;
+        float v[V];
+        Slot<DT>::unpack(x[j], v);
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] = fmaf(w[j], v[i], acc[i]);
+      }
+    }
+    if (a.extra) {
+      float v[V];
+      Slot<DT>::unpack(add, v);
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc[i] += v[i];
+    }
+    settle_vec<DT, MODE>(acc, e, a.hidden);
+    store_vec<DT, MODE>(static_cast<char*>(a.y) + t * row, e, a.hidden, Slot<DT>::pack(acc));
+  }
+}
+
+template <int DT, int LANES, int MODE>
+__global__ __launch_bounds__(kShortThreads) void combine_bwd_short_kernel(MoveArgs a, int pad_groups, int pad_parts) {
+  constexpr int V = Traits<DT>::kVec, kTokens = kShortThreads / LANES;
+  const int64_t row = static_cast<int64_t>(a.hidden) * Traits<DT>::kSize;
+  if (static_cast<int>(blockIdx.x) < pad_groups) {
+    zero_pads(a, static_cast<int>(blockIdx.x), pad_parts, row, 0);
+    return;
+  }
+  const int e = static_cast<int>(threadIdx.x) % LANES * V;
+  for (int64_t t = static_cast<int64_t>(blockIdx.x - pad_groups) * kTokens + threadIdx.x / LANES; t < a.tokens;
+       t += static_cast<int64_t>(gridDim.x - pad_groups) * kTokens) {
+    const u32x4 d = load_vec<DT, MODE>(static_cast<const char*>(a.extra) + t * row, e, a.hidden);
+    for (int j0 = 0; j0 < a.k; j0 += kChoices) {
+      int p[kChoices];
+      float w[kChoices];
+      load_rows_each(a, t, j0, p);
+#pragma unroll
+      for (int j = 0; j < kChoices; ++j) w[j] = j0 + j < a.k ? gptr<float>(a.weights + t * a.k)[j0 + j] : 0.0f;
+      u32x4 x[kChoices];
+#pragma unroll
+      for (int j = 0; j < kChoices; ++j) {
+        x[j] = u32x4{0, 0, 0, 0};
+        if (p[j] >= 0) x[j] = load_vec<DT, MODE>(static_cast<const char*>(a.x) + p[j] * row, e, a.hidden);
+      }
+      float dv[V];
+      Slot<DT>::unpack(d, dv);
+      settle_vec<DT, MODE>(dv, e, a.hidden);
+      float dot[kChoices];
+#pragma unroll
+      for (int j = 0; j < kChoices; ++j) {
+        dot[j] = 0.0f;
+        if (j0 + j >= a.k) continue;
+        float v[V], y[V];
+        Slot<DT>::unpack(x[j], v);
+        settle_vec<DT, MODE>(v, e, a.hidden);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          dot[j] = fmaf(dv[i], v[i], dot[j]);
+          y[i] = w[j] * dv[i];
+        }
+        dot[j] = lanes_sum<LANES>(dot[j]);
+        if (p[j] < 0) dot[j] = 0.0f;  // rather than the gradient's infinities and NaN times zero
+        else store_vec<DT, MODE>(static_cast<char*>(a.y) + p[j] * row, e, a.hidden, Slot<DT>::pack(y));
+      }
+      if (e == 0) {
+#pragma unroll
+        for (int j = 0; j < kChoices; ++j)
+          if (j0 + j < a.k) gptr<float>(a.dweights + t * a.k)[j0 + j] = dot[j];
+      }
+    }
+  }
+}
+
 constexpr int kUnroll = 2;  // vectors of a row a lane takes at a time
 
 // Lanes per token: as many as have two vectors each, up to 256; with few tokens, twice as many.
@@ -465,6 +604,13 @@ int lanes_for(int64_t vectors, int64_t tokens) {
 }
 // A launch has fewer than 2^32 threads.
 int64_t groups_for(int64_t tokens) { return tokens < (1 << 23) ? tokens : (1 << 23); }
+
+// Lanes per token of the kernels for short rows (0: the row is not short).
+int short_lanes(int64_t vectors) { return vectors > 32 ? 0 : vectors > 16 ? 32 : vectors > 8 ? 16 : 8; }
+unsigned short_groups(int64_t tokens, int lanes) {
+  const int64_t per = kShortThreads / lanes;
+  return static_cast<unsigned>(groups_for((tokens + per - 1) / per));
+}
 
 // Workgroups per expert that zero its pad rows: one for every 64 KiB that an expert's pads can have on average.
 int pad_parts(const MoveArgs& a, int64_t row_bytes) {
@@ -482,9 +628,21 @@ template <int DT, int MODE> hipError_t combine_lanes(const MoveArgs& a, int lane
   if (lanes == 128) return combine_run<DT, 128, kUnroll, MODE>(a, s);
   return combine_run<DT, 64, kUnroll, MODE>(a, s);
 }
+template <int DT, int LANES> hipError_t combine_short(const MoveArgs& a, bool exact, hipStream_t s) {
+  const dim3 grid(short_groups(a.tokens, LANES)), block(kShortThreads);
+  if (exact) hipLaunchKernelGGL((combine_short_kernel<DT, LANES, kExact>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((combine_short_kernel<DT, LANES, kCached>), grid, block, 0, s, a);
+  return hipGetLastError();
+}
 template <int DT> hipError_t combine_dt(const MoveArgs& a, hipStream_t s) {
   constexpr int V = Traits<DT>::kVec;
-  if (a.hidden < V || (a.extra == a.y && a.hidden % V != 0)) return combine_run<DT, 64, 1, kExact>(a, s);
+  const bool exact = a.hidden < V || (a.extra == a.y && a.hidden % V != 0);
+  switch (short_lanes((a.hidden + V - 1) / V)) {
+    case 8: return combine_short<DT, 8>(a, exact, s);
+    case 16: return combine_short<DT, 16>(a, exact, s);
+    case 32: return combine_short<DT, 32>(a, exact, s);
+  }
+  if (exact) return combine_run<DT, 64, 1, kExact>(a, s);
   const int64_t row = static_cast<int64_t>(a.hidden) * Traits<DT>::kSize;
   const int lanes = lanes_for((a.hidden + V - 1) / V, a.tokens);
   return streams(a.tokens * row * (a.k + 2), row) ? combine_lanes<DT, kStream>(a, lanes, s)
@@ -503,12 +661,26 @@ template <int DT, int U, int MODE> hipError_t combine_bwd_lanes(const MoveArgs& 
   if (lanes == 128) return combine_bwd_run<DT, 128, U, MODE>(a, s);
   return combine_bwd_run<DT, 64, U, MODE>(a, s);
 }
+template <int DT, int LANES> hipError_t combine_bwd_short(const MoveArgs& a, bool exact, hipStream_t s) {
+  const int parts = pad_parts(a, static_cast<int64_t>(a.hidden) * Traits<DT>::kSize);
+  const int pads = a.offsets ? a.experts * parts : 0;
+  const dim3 grid(short_groups(a.tokens, LANES) + pads), block(kShortThreads);
+  if (exact) hipLaunchKernelGGL((combine_bwd_short_kernel<DT, LANES, kExact>), grid, block, 0, s, a, pads, parts);
+  else hipLaunchKernelGGL((combine_bwd_short_kernel<DT, LANES, kCached>), grid, block, 0, s, a, pads, parts);
+  return hipGetLastError();
+}
 template <int DT> hipError_t combine_bwd_dt(const MoveArgs& a, hipStream_t s) {
   constexpr int V = Traits<DT>::kVec;
+  const bool exact = a.hidden < V || (a.x == a.y && a.hidden % V != 0);
+  switch (short_lanes((a.hidden + V - 1) / V)) {
+    case 8: return combine_bwd_short<DT, 8>(a, exact, s);
+    case 16: return combine_bwd_short<DT, 16>(a, exact, s);
+    case 32: return combine_bwd_short<DT, 32>(a, exact, s);
+  }
   const int64_t row = static_cast<int64_t>(a.hidden) * Traits<DT>::kSize;
   const int lanes = lanes_for((a.hidden + V - 1) / V, a.tokens);
   // in place with the same lanes, so that dweights has the same bits
-  if (a.hidden < V || (a.x == a.y && a.hidden % V != 0)) return combine_bwd_lanes<DT, 1, kExact>(a, lanes, s);
+  if (exact) return combine_bwd_lanes<DT, 1, kExact>(a, lanes, s);
   return streams(a.tokens * row * (2 * a.k + 1), row) ? combine_bwd_lanes<DT, kUnroll, kStream>(a, lanes, s)
                                                       : combine_bwd_lanes<DT, kUnroll, kCached>(a, lanes, s);
 }
@@ -540,8 +712,17 @@ hipError_t launch_expert_sort(const SortArgs& a, hipStream_t s) {
 
 hipError_t launch_expert_dispatch(const MoveArgs& a, int esize, hipStream_t s) {
   const int row = a.hidden * esize, scale = a.x_scales ? (a.hidden + AR_FP8_BLOCK - 1) / AR_FP8_BLOCK * 4 : 0;
+  if (a.tokens == 0) return hipSuccess;
   const int parts = pad_parts(a, row);
   const int pads = a.offsets ? a.experts * parts : 0;
+  const int lanes = row < 16 ? 0 : short_lanes((row + 15) / 16);
+  if (lanes) {
+    const dim3 grid(short_groups(a.tokens, lanes) + pads), block(kShortThreads);
+    if (lanes == 8) hipLaunchKernelGGL(dispatch_short_kernel<8>, grid, block, 0, s, a, row, scale, pads, parts);
+    else if (lanes == 16) hipLaunchKernelGGL(dispatch_short_kernel<16>, grid, block, 0, s, a, row, scale, pads, parts);
+    else hipLaunchKernelGGL(dispatch_short_kernel<32>, grid, block, 0, s, a, row, scale, pads, parts);
+    return hipGetLastError();
+  }
   const dim3 grid(static_cast<unsigned>(groups_for(a.tokens) + pads)), block(kCopyLanes);
   if (streams(a.tokens * row * static_cast<int64_t>(a.k + 1), row))
     hipLaunchKernelGGL(dispatch_kernel<kStream>, grid, block, 0, s, a, row, scale, pads, parts);

@@ -183,6 +183,7 @@ __device__ __forceinline__ float group_sum(float v, float* lds) {
 }
 
 constexpr int kMaxThreads = 1024;
+constexpr int kShortThreads = 256;  // a forward workgroup of several rows
 constexpr int kFewRanks = 8;
 // The arguments that the kernels for NR ranks take (NR 0: any number).
 template <int NR> using ArgsFor = NormArgsOf<NR == 0 ? AR_MAX_RANKS : kFewRanks>;
@@ -198,7 +199,6 @@ template <int NR> ArgsFor<NR> args_for(const NormArgs& a) {
 }
 constexpr int kRankBatch = 4;
 constexpr int kTeamThreads = 512;  // a backward workgroup of several teams
-constexpr int kMaxTeams = 8;
 
 // The ranks' slots of a row (NR: their number if known; otherwise `batch` of them from rank r0 on), and their sum in
 // rank order onto h.
@@ -251,22 +251,27 @@ __device__ __forceinline__ void quant8(const float (&v)[kPerLane], float* scale,
   *scale = s.scale;
 }
 
-// One workgroup, one row.
-template <int DT, int S, int NR, int MODE>
+// One workgroup, one row; LANES > 0: LANES lanes to a row (rows of at most LANES slots).
+template <int DT, int S, int NR, int MODE, int LANES>
 __global__ __launch_bounds__(kMaxThreads) void rmsnorm_kernel(ArgsFor<NR> a, int64_t row0) {
   __shared__ float lds[kMaxThreads / 64];
   constexpr int kSize = Traits<DT>::kSize;
   const int nb = (a.hidden + kBlock - 1) / kBlock, threads = static_cast<int>(blockDim.x);
-  const int64_t row = row0 + blockIdx.x;
+  const int tid = static_cast<int>(LANES > 0 ? threadIdx.x % LANES : threadIdx.x);
+  int64_t row = row0 + blockIdx.x;
+  if constexpr (LANES > 0) {
+    row = row0 + static_cast<int64_t>(blockIdx.x) * (kShortThreads / LANES) + threadIdx.x / LANES;
+    if (row >= a.rows) return;
+  }
   const int64_t at = row * a.hidden;
   float h[S][kPerLane];
   RawGamma gam[S];
   float ss = 0.0f;
 #pragma unroll
-  for (int s = 0; s < S; ++s) gam[s] = load_gamma<DT, MODE>(a, first_of<DT>(s * threads + static_cast<int>(threadIdx.x)));
+  for (int s = 0; s < S; ++s) gam[s] = load_gamma<DT, MODE>(a, first_of<DT>(s * threads + tid));
 #pragma unroll
   for (int s = 0; s < S; ++s) {
-    const int e0 = first_of<DT>(s * threads + static_cast<int>(threadIdx.x));
+    const int e0 = first_of<DT>(s * threads + tid);
     RankSlots<DT, NR, MODE> first;
     Raw<DT> res;
     first.load(a, at * kSize, e0, 0);
@@ -282,12 +287,14 @@ __global__ __launch_bounds__(kMaxThreads) void rmsnorm_kernel(ArgsFor<NR> a, int
 #pragma unroll
     for (int k = 0; k < kPerLane; ++k) ss += h[s][k] * h[s][k];
   }
-  const float mean = group_sum(ss, lds) / static_cast<float>(a.hidden);
+  if constexpr (LANES > 0) ss = lanes_sum<LANES>(ss);
+  else ss = group_sum(ss, lds);
+  const float mean = ss / static_cast<float>(a.hidden);
   const float rstd = 1.0f / sqrtf(mean + a.eps);
-  if (a.rstd && threadIdx.x == 0) gptr<float>(a.rstd)[row] = rstd;
+  if (a.rstd && tid == 0) gptr<float>(a.rstd)[row] = rstd;
 #pragma unroll
   for (int s = 0; s < S; ++s) {
-    const int i = s * threads + static_cast<int>(threadIdx.x);
+    const int i = s * threads + tid;
     const int e0 = first_of<DT>(i);
     const bool block_lane = (i & 15) == 0 && e0 < a.hidden;
     if (a.residual_out)
@@ -375,8 +382,8 @@ __device__ __forceinline__ void columns_dgamma(const ArgsFor<NR>& a, int block, 
 // the teams' sums are joined in LDS and leave as one row of partial sums per workgroup, which dgamma_kernel adds up in
 // order. One slot a lane (S = 1): the next row is read while this one's dot product is joined and its results are
 // stored. Wider rows (S > 1) have one team and read their row when its turn comes.
-// SMALL: no second launch; the workgroups from `groups` on each sum a block of columns instead, reading those again.
-template <int DT, int S, int NR, int MODE, bool SMALL>
+// LANES > 0: a team is LANES lanes of a wave (rows of at most LANES slots). SMALL: no second launch; the workgroups from `groups` on each sum a block of columns instead, reading those again.
+template <int DT, int S, int NR, int MODE, bool SMALL, int LANES>
 __global__ __launch_bounds__(kMaxThreads) void rmsnorm_bwd_kernel(ArgsFor<NR> a, int team_threads, int groups,
                                                                   float* dgamma) {
   constexpr bool kAhead = S == 1 && (Traits<DT>::kSize == 2 || NR < 8);
@@ -390,7 +397,9 @@ __global__ __launch_bounds__(kMaxThreads) void rmsnorm_bwd_kernel(ArgsFor<NR> a,
     }
   }
   const int teams = S == 1 ? static_cast<int>(blockDim.x) / team_threads : 1;
-  const int team = S == 1 ? __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / team_threads) : 0;
+  const int team = LANES > 0 ? static_cast<int>(threadIdx.x) / LANES
+                   : S == 1  ? __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / team_threads)
+                             : 0;
   const int tid = static_cast<int>(threadIdx.x) - team * team_threads;
   const int64_t step = static_cast<int64_t>(groups) * teams;
   float dg[S][kPerLane];
@@ -452,8 +461,9 @@ __global__ __launch_bounds__(kMaxThreads) void rmsnorm_bwd_kernel(ArgsFor<NR> a,
         rstd_next = gptr<float>(a.rstd_in)[row + step];
       }
     }
-    dot = wave_sum(dot);
-    if (team_threads > 64) {
+    if constexpr (LANES > 0) dot = lanes_sum<LANES>(dot);
+    else dot = wave_sum(dot);
+    if (LANES == 0 && team_threads > 64) {
       if ((threadIdx.x & 63) == 0) lds[flip][threadIdx.x >> 6] = dot;
       __syncthreads();
       dot = 0.0f;
@@ -478,19 +488,33 @@ __global__ __launch_bounds__(kMaxThreads) void rmsnorm_bwd_kernel(ArgsFor<NR> a,
     }
   }
   if constexpr (SMALL) return;
-  if (teams > 1) {
-    const int others = team_threads * (teams - 1);
-    if (team > 0) {
+  // The teams' sums: those inside a wave first, then, in order, one part of `width` threads after another.
+  int parts = teams, part = team, width = team_threads;
+  bool holds = true;
+  if constexpr (LANES > 0) {
 #pragma unroll
-      for (int k = 0; k < kPerLane; ++k) join[k * others + (team - 1) * team_threads + tid] = dg[0][k];
+    for (int d = LANES; d < 64; d *= 2)
+#pragma unroll
+      for (int k = 0; k < kPerLane; ++k) dg[0][k] += __shfl_xor(dg[0][k], d, 64);
+    parts = static_cast<int>(blockDim.x) >> 6;
+    part = static_cast<int>(threadIdx.x) >> 6;
+    width = LANES;
+    holds = (threadIdx.x & 63) < LANES;
+  }
+  if (parts > 1) {
+    const int others = width * (parts - 1);
+    if (part > 0 && holds) {
+#pragma unroll
+      for (int k = 0; k < kPerLane; ++k) join[k * others + (part - 1) * width + tid] = dg[0][k];
     }
     __syncthreads();
-    if (team > 0) return;
-    for (int t = 0; t < teams - 1; ++t) {
+    if (part > 0) return;
+    for (int t = 0; t < parts - 1; ++t) {
 #pragma unroll
-      for (int k = 0; k < kPerLane; ++k) dg[0][k] += join[k * others + t * team_threads + tid];
+      for (int k = 0; k < kPerLane; ++k) dg[0][k] += join[k * others + t * width + tid];
     }
   }
+  if (!holds) return;
   float* to = a.partial + static_cast<int64_t>(blockIdx.x) * a.hidden;
 #pragma unroll
   for (int s = 0; s < S; ++s) {
@@ -533,22 +557,29 @@ __global__ __launch_bounds__(1024) void dgamma_kernel(const float* partial, int6
 }
 
 // Threads and slots per thread for a row of `hidden` elements: one slot of 8 a lane, two or four only where 1024
-// threads do not cover the row.
+// threads do not cover the row. Whole waves, but for rows of up to 128 or 256 elements, which 16 or 32 lanes take
+// (against a wave per row, bf16: 16,384 rows of 64, 2 ranks, forward 11.3 -> 5.0 us, backward 15.9 -> 9.2; of 256, 12.6 ->
+// 9.5 and 18.7 -> 15.1; 131,072 rows of 128, one rank, 54 -> 21 and 71 -> 28).
 struct Shape {
   int threads, slots;
 };
-Shape shape_of(int hidden) {
+Shape wave_shape(int hidden) {
   const int slots = (hidden + kBlock - 1) / kBlock * 16;  // whole blocks: 16 lanes each
   const int per = slots <= kMaxThreads ? 1 : slots <= 2 * kMaxThreads ? 2 : 4;
   return Shape{((slots + per - 1) / per + 63) / 64 * 64, per};
 }
+Shape shape_of(int hidden) {
+  if (hidden <= 2 * kBlock) return Shape{hidden <= kBlock ? 16 : 32, 1};
+  return wave_shape(hidden);
+}
 
-// Backward: teams per workgroup, as many as make 512 threads while there are rows for 256 workgroups (129 rows of 1003
-// fp16, 2 ranks: 6.4 us with one team, 7.9 us with four; 16,384 rows of 256 bf16: 28.5 us with one, 17.9 us with eight).
+// Backward: teams per workgroup, as many as make 512 threads while there are rows for 256 workgroups (16,384 rows of 256
+// bf16 with a wave each: 28.5 us with one team, 17.9 us with eight); whole waves.
 int teams_of(int64_t rows, const Shape& sh) {
+  const int unit = sh.threads < 64 ? 64 / sh.threads : 1;
   int64_t teams = kTeamThreads / sh.threads;
-  if (teams > rows / 256) teams = rows / 256;
-  return sh.slots > 1 || teams < 1 ? 1 : teams > kMaxTeams ? kMaxTeams : static_cast<int>(teams);
+  if (teams > rows / 256) teams = rows / 256 / unit * unit;
+  return sh.slots > 1 || teams < unit ? unit : static_cast<int>(teams);
 }
 // Workgroups: for 16 waves on each of the 256 compute units, or for 8 where a wave's own loads are many (6 ranks and
 // more: 8 x 8192 x 4096 bf16 232 us, against 244 us with 16 waves; one rank, 16,384 x 2048: 83 us against 59 us); one
@@ -568,8 +599,8 @@ constexpr int64_t kMaxGrid = 1 << 21;  // a launch has fewer than 2^32 threads
 // Up to 256 rows and 24 MiB read twice (two launches against one: 1 row of 4096, 8 ranks 8.2 / 4.0 us, 128 of 1000, 2
 // ranks 6.7 / 4.6, 256 of 4096, 8 ranks 15.7 / 14.7; beyond: 512 of 1000, 2 ranks 7.8 / 9.4, 512 of 4096, 8 ranks
 // 20.6 / 29.4).
-bool reads_twice(const NormArgs& a, const Shape& sh, int size) {
-  return sh.slots == 1 && a.rows <= 256 && a.rows * a.hidden * size * (a.n + 1) <= (24 << 20);
+bool reads_twice(const NormArgs& a, int size) {
+  return a.hidden <= kMaxThreads * kPerLane && a.rows <= 256 && a.rows * a.hidden * size * (a.n + 1) <= (24 << 20);
 }
 bool over_inputs(const NormArgs& a) {
   for (int r = 0; r < a.n; ++r)
@@ -578,31 +609,31 @@ bool over_inputs(const NormArgs& a) {
   return false;
 }
 
-template <int DT, int S, int NR, int MODE>
-hipError_t run_bwd(const NormArgs& a, const Shape& sh, float* dgamma, hipStream_t s) {
-  if constexpr (S == 1 && MODE != kStream) {
-    if (reads_twice(a, sh, Traits<DT>::kSize)) {
-      const int teams = kMaxThreads / sh.threads, blocks = (a.hidden + kBlock - 1) / kBlock;
-      const int groups = static_cast<int>((a.rows + teams - 1) / teams);
-      const dim3 block(teams * sh.threads);
-      if (groups > 0 && over_inputs(a)) {  // all columns first, then the rows that overwrite what those read
-        hipLaunchKernelGGL((rmsnorm_bwd_kernel<DT, S, NR, MODE, true>), dim3(blocks), block, 0, s, args_for<NR>(a), sh.threads, 0,
-                           dgamma);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
-        hipLaunchKernelGGL((rmsnorm_bwd_kernel<DT, S, NR, MODE, true>), dim3(groups), block, 0, s, args_for<NR>(a), sh.threads, groups,
-                           dgamma);
-        return hipGetLastError();
-      }
-      hipLaunchKernelGGL((rmsnorm_bwd_kernel<DT, S, NR, MODE, true>), dim3(groups + blocks), block, 0, s, args_for<NR>(a), sh.threads,
-                         groups, dgamma);
-      return hipGetLastError();
-    }
+template <int DT, int NR, int MODE> hipError_t run_bwd_once(const NormArgs& a, float* dgamma, hipStream_t s) {
+  const Shape sh = wave_shape(a.hidden);
+  const int teams = kMaxThreads / sh.threads, blocks = (a.hidden + kBlock - 1) / kBlock;
+  const int groups = static_cast<int>((a.rows + teams - 1) / teams);
+  const dim3 block(teams * sh.threads);
+  const auto b = args_for<NR>(a);
+  if (groups > 0 && over_inputs(a)) {  // all columns first, then the rows that overwrite what those read
+    hipLaunchKernelGGL((rmsnorm_bwd_kernel<DT, 1, NR, MODE, true, 0>), dim3(blocks), block, 0, s, b, sh.threads, 0, dgamma);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((rmsnorm_bwd_kernel<DT, 1, NR, MODE, true, 0>), dim3(groups), block, 0, s, b, sh.threads, groups,
+                       dgamma);
+    return hipGetLastError();
   }
+  hipLaunchKernelGGL((rmsnorm_bwd_kernel<DT, 1, NR, MODE, true, 0>), dim3(groups + blocks), block, 0, s, b, sh.threads,
+                     groups, dgamma);
+  return hipGetLastError();
+}
+
+template <int DT, int S, int NR, int MODE, int LANES>
+hipError_t run_bwd(const NormArgs& a, const Shape& sh, float* dgamma, hipStream_t s) {
   const int teams = teams_of(a.rows, sh), groups = static_cast<int>(groups_of(a.rows, sh, a.n));
   if (groups > 0) {
-    hipLaunchKernelGGL((rmsnorm_bwd_kernel<DT, S, NR, MODE, false>), dim3(groups), dim3(teams * sh.threads), 0, s, args_for<NR>(a),
-                       sh.threads, groups, nullptr);
+    hipLaunchKernelGGL((rmsnorm_bwd_kernel<DT, S, NR, MODE, false, LANES>), dim3(groups), dim3(teams * sh.threads), 0, s,
+                       args_for<NR>(a), sh.threads, groups, nullptr);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -611,12 +642,14 @@ hipError_t run_bwd(const NormArgs& a, const Shape& sh, float* dgamma, hipStream_
   return hipGetLastError();
 }
 
-template <int DT, int S, int NR, int MODE>
+template <int DT, int S, int NR, int MODE, int LANES>
 hipError_t run_fwd(const NormArgs& a, const Shape& sh, hipStream_t s) {
-  for (int64_t row = 0; row < a.rows; row += kMaxGrid) {
-    const int64_t rows = a.rows - row < kMaxGrid ? a.rows - row : kMaxGrid;
-    hipLaunchKernelGGL((rmsnorm_kernel<DT, S, NR, MODE>), dim3(static_cast<unsigned>(rows)), dim3(sh.threads), 0, s, args_for<NR>(a),
-                       row);
+  constexpr int kRows = LANES > 0 ? kShortThreads / LANES : 1;  // of a workgroup
+  const int threads = LANES > 0 ? kShortThreads : sh.threads;
+  for (int64_t row = 0; row < a.rows; row += kMaxGrid * kRows) {
+    const int64_t left = (a.rows - row + kRows - 1) / kRows, groups = left < kMaxGrid ? left : kMaxGrid;
+    hipLaunchKernelGGL((rmsnorm_kernel<DT, S, NR, MODE, LANES>), dim3(static_cast<unsigned>(groups)), dim3(threads), 0, s,
+                       args_for<NR>(a), row);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -624,30 +657,37 @@ hipError_t run_fwd(const NormArgs& a, const Shape& sh, hipStream_t s) {
 }
 
 // dgamma: of the backward pass; null for the forward
-template <int DT, int S, int NR, int MODE>
+template <int DT, int S, int NR, int MODE, int LANES>
 hipError_t run(const NormArgs& a, float* dgamma, const Shape& sh, hipStream_t s) {
-  return dgamma ? run_bwd<DT, S, NR, MODE>(a, sh, dgamma, s) : run_fwd<DT, S, NR, MODE>(a, sh, s);
+  if (!dgamma) return run_fwd<DT, S, NR, MODE, LANES>(a, sh, s);
+  if constexpr (S == 1 && MODE != kStream) {
+    if (reads_twice(a, Traits<DT>::kSize)) return run_bwd_once<DT, NR, MODE>(a, dgamma, s);
+  }
+  return run_bwd<DT, S, NR, MODE, LANES>(a, sh, dgamma, s);
 }
-template <int DT, int S, int MODE> hipError_t run_n(const NormArgs& a, float* dgamma, const Shape& sh, hipStream_t s) {
+template <int DT, int S, int MODE, int LANES>
+hipError_t run_n(const NormArgs& a, float* dgamma, const Shape& sh, hipStream_t s) {
   switch (a.n) {
-    case 1: return run<DT, S, 1, MODE>(a, dgamma, sh, s);
-    case 2: return run<DT, S, 2, MODE>(a, dgamma, sh, s);
-    case 3: return run<DT, S, 3, MODE>(a, dgamma, sh, s);
-    case 4: return run<DT, S, 4, MODE>(a, dgamma, sh, s);
-    case 8: return run<DT, S, 8, MODE>(a, dgamma, sh, s);
-    default: return run<DT, S, 0, MODE>(a, dgamma, sh, s);
+    case 1: return run<DT, S, 1, MODE, LANES>(a, dgamma, sh, s);
+    case 2: return run<DT, S, 2, MODE, LANES>(a, dgamma, sh, s);
+    case 3: return run<DT, S, 3, MODE, LANES>(a, dgamma, sh, s);
+    case 4: return run<DT, S, 4, MODE, LANES>(a, dgamma, sh, s);
+    case 8: return run<DT, S, 8, MODE, LANES>(a, dgamma, sh, s);
+    default: return run<DT, S, 0, MODE, LANES>(a, dgamma, sh, s);
   }
 }
 
 template <int DT> hipError_t launch(const NormArgs& a, float* dgamma, hipStream_t s) {
   const Shape sh = shape_of(a.hidden);
   const int64_t row = static_cast<int64_t>(a.hidden) * Traits<DT>::kSize;
-  if (a.hidden < Traits<DT>::kVec) return run<DT, 1, 0, kExact>(a, dgamma, sh, s);
+  if (a.hidden < Traits<DT>::kVec) return run<DT, 1, 0, kExact, 16>(a, dgamma, sh, s);
+  if (sh.threads == 16) return run_n<DT, 1, kCached, 16>(a, dgamma, sh, s);
+  if (sh.threads == 32) return run_n<DT, 1, kCached, 32>(a, dgamma, sh, s);
   if (sh.slots == 1)
-    return streams(a.rows * row * (2 * a.n + 2), row) ? run_n<DT, 1, kStream>(a, dgamma, sh, s)
-                                                      : run_n<DT, 1, kCached>(a, dgamma, sh, s);
-  if (sh.slots == 2) return run_n<DT, 2, kCached>(a, dgamma, sh, s);
-  return run_n<DT, 4, kCached>(a, dgamma, sh, s);
+    return streams(a.rows * row * (2 * a.n + 2), row) ? run_n<DT, 1, kStream, 0>(a, dgamma, sh, s)
+                                                      : run_n<DT, 1, kCached, 0>(a, dgamma, sh, s);
+  if (sh.slots == 2) return run_n<DT, 2, kCached, 0>(a, dgamma, sh, s);
+  return run_n<DT, 4, kCached, 0>(a, dgamma, sh, s);
 }
 
 }  // namespace

@@ -16,7 +16,9 @@ namespace {
 
 // ------------------------------------------------------------------------------------------ sort
 constexpr int kSortThreads = 1024;
-constexpr int kSortWaves = kSortThreads / 64;
+// Few slots and experts go to a workgroup of a quarter of the size (192 slots, 128 experts: 4.1 -> 3.2 us; 1024 slots and
+// 256 experts would lose, 5.2 -> 7.0).
+constexpr int kFewThreads = 256, kFewSlots = 512, kFewExperts = 128;
 constexpr int kMaxExperts = AR_MAX_EXPERTS;
 constexpr int kTileBatch = 8;             // histograms read together
 constexpr int kHeld = 4;  // slots a thread reads at a time; a thread's first ones stay in registers between the passes
@@ -47,7 +49,7 @@ __device__ __forceinline__ void load_experts(const SortArgs& a, int64_t q0, int6
 }
 
 // Exclusive sum over the workgroup's threads; `lds` holds one value per wave. Returns the total in *total.
-__device__ __forceinline__ int group_exclusive(int v, int* lds, int* total) {
+template <int WAVES> __device__ __forceinline__ int group_exclusive(int v, int* lds, int* total) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   int x = v;
 #pragma unroll
@@ -58,7 +60,7 @@ __device__ __forceinline__ int group_exclusive(int v, int* lds, int* total) {
   if (lane == 63) lds[wave] = x;
   __syncthreads();
   int before = 0, all = 0;
-  for (int w = 0; w < kSortWaves; ++w) {
+  for (int w = 0; w < WAVES; ++w) {
     if (w < wave) before += lds[w];
     all += lds[w];
   }
@@ -83,19 +85,21 @@ __global__ __launch_bounds__(kSortThreads) void sort_hist_kernel(SortArgs a, int
 
 // One workgroup per tile of slots (one tile: no histogram launch before it). Every workgroup adds up the tiles'
 // histograms for itself, so the tiles need no order among each other.
-__global__ __launch_bounds__(kSortThreads) void sort_kernel(SortArgs a, int64_t tile) {
-  __shared__ int next[kSortWaves][kMaxExperts];  // first the waves' counts, then the next row of (wave, expert)
-  __shared__ int part[2][kSortThreads];
-  __shared__ int scan[kSortWaves];
+template <int T, int EXPERTS>
+__global__ __launch_bounds__(T) void sort_kernel(SortArgs a, int64_t tile) {
+  constexpr int kWaves = T / 64;
+  __shared__ int next[kWaves][EXPERTS];  // first the waves' counts, then the next row of (wave, expert)
+  __shared__ int part[2][T];
+  __shared__ int scan[kWaves];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   int bits = 0;
   while ((1 << bits) < a.experts) ++bits;
-  for (int e = threadIdx.x; e < a.experts; e += kSortThreads)
-    for (int w = 0; w < kSortWaves; ++w) next[w][e] = 0;
+  for (int e = threadIdx.x; e < a.experts; e += T)
+    for (int w = 0; w < kWaves; ++w) next[w][e] = 0;
   __syncthreads();
   const int64_t lo = static_cast<int64_t>(blockIdx.x) * tile;
   const int64_t hi = lo + tile < a.slots ? lo + tile : a.slots;
-  const int64_t per_wave = (tile + kSortThreads - 1) / kSortThreads * 64;
+  const int64_t per_wave = (tile + T - 1) / T * 64;
   const int64_t w_lo = lo + wave * per_wave, w_hi = w_lo + per_wave < hi ? w_lo + per_wave : hi;
   int held[kHeld];
   load_experts(a, w_lo, w_hi, held);
@@ -116,17 +120,17 @@ __global__ __launch_bounds__(kSortThreads) void sort_kernel(SortArgs a, int64_t 
     // the tiles' histograms, an equal part of the tiles for each of the 1024 >> bits threads of an expert
     const int x = threadIdx.x & ((1 << bits) - 1), tiles = static_cast<int>(gridDim.x);
     if (x < a.experts) {
-      for (int t0 = threadIdx.x >> bits; t0 < tiles; t0 += kTileBatch * (kSortThreads >> bits)) {
+      for (int t0 = threadIdx.x >> bits; t0 < tiles; t0 += kTileBatch * (T >> bits)) {
         int c[kTileBatch];
 #pragma unroll
         for (int u = 0; u < kTileBatch; ++u) {
-          const int t = t0 + u * (kSortThreads >> bits);
+          const int t = t0 + u * (T >> bits);
           c[u] = t < tiles ? gptr<int32_t>(a.hist)[static_cast<int64_t>(t) * a.experts + x] : 0;
         }
 #pragma unroll
         for (int u = 0; u < kTileBatch; ++u) {
           total += c[u];
-          if (t0 + u * (kSortThreads >> bits) < static_cast<int>(blockIdx.x)) before += c[u];
+          if (t0 + u * (T >> bits) < static_cast<int>(blockIdx.x)) before += c[u];
         }
       }
     }
@@ -135,20 +139,20 @@ __global__ __launch_bounds__(kSortThreads) void sort_kernel(SortArgs a, int64_t 
     __syncthreads();
     total = before = 0;
     if (e < a.experts) {
-      for (int i = e; i < kSortThreads; i += 1 << bits) {
+      for (int i = e; i < T; i += 1 << bits) {
         total += part[0][i];
         before += part[1][i];
       }
     }
   } else if (e < a.experts) {
-    for (int w = 0; w < kSortWaves; ++w) total += next[w][e];
+    for (int w = 0; w < kWaves; ++w) total += next[w][e];
   }
   const int padded = (total + a.align - 1) / a.align * a.align;
   int rows = 0;
-  const int first = group_exclusive(padded, scan, &rows);
+  const int first = group_exclusive<kWaves>(padded, scan, &rows);
   if (e < a.experts) {
     int at = first + before;
-    for (int w = 0; w < kSortWaves; ++w) {
+    for (int w = 0; w < kWaves; ++w) {
       const int c = next[w][e];
       next[w][e] = at;
       at += c;
@@ -161,12 +165,12 @@ __global__ __launch_bounds__(kSortThreads) void sort_kernel(SortArgs a, int64_t 
     part[0][e] = first + total;
     part[1][e] = first + padded;
   }
-  for (int64_t p = rows + static_cast<int64_t>(blockIdx.x) * kSortThreads + threadIdx.x; p < a.rows;
-       p += static_cast<int64_t>(gridDim.x) * kSortThreads)
+  for (int64_t p = rows + static_cast<int64_t>(blockIdx.x) * T + threadIdx.x; p < a.rows;
+       p += static_cast<int64_t>(gridDim.x) * T)
     gptr<int32_t>(a.src)[p] = -1;
   __syncthreads();
   if (a.align > 1) {  // rows of the segments that no slot takes, 16 lanes to a segment
-    constexpr int kAtOnce = kSortThreads / 16;
+    constexpr int kAtOnce = T / 16;
     for (int x = static_cast<int>(blockIdx.x) * kAtOnce + static_cast<int>(threadIdx.x) / 16; x < a.experts;
          x += static_cast<int>(gridDim.x) * kAtOnce)
       for (int p = part[0][x] + (lane & 15); p < part[1][x]; p += 16) gptr<int32_t>(a.src)[p] = -1;
@@ -255,28 +259,50 @@ __global__ __launch_bounds__(kCopyLanes) void dispatch_kernel(MoveArgs a, int ro
   const int lane = threadIdx.x;
   for (int64_t t = blockIdx.x - pad_groups; t < a.tokens; t += gridDim.x - pad_groups) {
     const char* from = static_cast<const char*>(a.x) + t * row_bytes;
-    for (int j0 = 0; j0 < a.k; j0 += kChoices) {
-      int p[kChoices];
-      load_rows(a, t, j0, p);
-      if (row_bytes >= 16) {
-        for (int b0 = lane * 16; b0 < row_bytes; b0 += LANES * U * 16) {
-          u32x4 v[U];
-          uint32_t at[U];
+    int p[kChoices];
+    // Small calls read the row while the positions are on their way (48 tokens of 4096 bytes with the sort: 7.0 -> 6.0 us).
+    // Large ones are faster the other way round (16,384 x 8 rows of 8 KiB with the sort: 234 against 252 us).
+    auto put = [&](const u32x4 (&v)[U], const uint32_t (&at)[U], int b0) {
 #pragma unroll
-          for (int u = 0; u < U; ++u) {
-            at[u] = clamped<16>(b0 + u * LANES * 16, row_bytes);
-            v[u] = ld_row<kCached>(from, at[u]);
-          }
+      for (int j = 0; j < kChoices; ++j) {
+        if (p[j] < 0) continue;
+        char* to = static_cast<char*>(a.y) + p[j] * static_cast<int64_t>(row_bytes);
 #pragma unroll
-          for (int j = 0; j < kChoices; ++j) {
-            if (p[j] < 0) continue;
-            char* to = static_cast<char*>(a.y) + p[j] * static_cast<int64_t>(row_bytes);
+        for (int u = 0; u < U; ++u)
+          if (b0 + u * LANES * 16 < row_bytes) st_row<MODE>(to, at[u], v[u]);
+      }
+    };
+    auto get = [&](u32x4 (&v)[U], uint32_t (&at)[U], int b0) {
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-              if (b0 + u * LANES * 16 < row_bytes) st_row<MODE>(to, at[u], v[u]);
+      for (int u = 0; u < U; ++u) {
+        at[u] = clamped<16>(b0 + u * LANES * 16, row_bytes);
+        v[u] = ld_row<kCached>(from, at[u]);
+      }
+    };
+    u32x4 v[U];
+    uint32_t at[U];
+    if (row_bytes >= 16) {
+      if constexpr (MODE == kStream) {
+        for (int j0 = 0; j0 < a.k; j0 += kChoices) {
+          load_rows(a, t, j0, p);
+          for (int b0 = lane * 16; b0 < row_bytes; b0 += LANES * U * 16) {
+            get(v, at, b0);
+            put(v, at, b0);
           }
         }
-      } else if (lane < row_bytes) {
+      } else {
+        for (int b0 = 0; b0 < row_bytes; b0 += LANES * U * 16) {
+          get(v, at, b0 + lane * 16);
+          for (int j0 = 0; j0 < a.k; j0 += kChoices) {
+            if (b0 == 0 || a.k > kChoices) load_rows(a, t, j0, p);
+            put(v, at, b0 + lane * 16);
+          }
+        }
+      }
+    }
+    for (int j0 = 0; j0 < a.k; j0 += kChoices) {
+      if (row_bytes < 16 || a.k > kChoices) load_rows(a, t, j0, p);
+      if (row_bytes < 16 && lane < row_bytes) {
         const uint8_t v = gptr<uint8_t>(from)[lane];
 #pragma unroll
         for (int j = 0; j < kChoices; ++j)
@@ -381,6 +407,15 @@ __global__ __launch_bounds__(LANES) void combine_bwd_kernel(MoveArgs a, int pad_
   int flip = 0;
   for (int64_t t = blockIdx.x - pad_groups; t < a.tokens; t += gridDim.x - pad_groups) {
     for (int j0 = 0; j0 < a.k; j0 += kChoices, flip ^= 1) {
+      u32x4 d[U];
+      auto load_grad = [&](int b0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (b0 + u * LANES * V < a.hidden)
+            d[u] = load_vec<DT, MODE>(static_cast<const char*>(a.extra) + t * row, b0 + u * LANES * V + lane_elem<DT>(),
+                                      a.hidden);
+      };
+      load_grad(wave_first<DT>());  // while the positions are on their way
       int p[kChoices];
       float w[kChoices], dot[kChoices];
       load_rows(a, t, j0, p);
@@ -388,12 +423,8 @@ __global__ __launch_bounds__(LANES) void combine_bwd_kernel(MoveArgs a, int pad_
 #pragma unroll
       for (int j = 0; j < kChoices; ++j) dot[j] = 0.0f;
       for (int b0 = wave_first<DT>(); b0 < a.hidden; b0 += LANES * V * U) {
-        u32x4 d[U], x[kChoices][U];
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-          if (b0 + u * LANES * V < a.hidden)
-            d[u] = load_vec<DT, MODE>(static_cast<const char*>(a.extra) + t * row, b0 + u * LANES * V + lane_elem<DT>(),
-                                       a.hidden);
+        u32x4 x[kChoices][U];
+        if (b0 != wave_first<DT>()) load_grad(b0);
 #pragma unroll
         for (int j = 0; j < kChoices; ++j) {
           if (p[j] < 0) continue;
@@ -698,7 +729,11 @@ hipError_t launch_expert_sort(const SortArgs& a, hipStream_t s) {
   if (a.slots <= kOneGroupSlots) {
     SortArgs b = a;
     b.hist = nullptr;
-    hipLaunchKernelGGL(sort_kernel, dim3(1), block, 0, s, b, a.slots > 0 ? a.slots : 1);
+    const int64_t tile = a.slots > 0 ? a.slots : 1;
+    if (a.slots <= kFewSlots && a.experts <= kFewExperts)
+      hipLaunchKernelGGL((sort_kernel<kFewThreads, kFewThreads>), dim3(1), dim3(kFewThreads), 0, s, b, tile);
+    else
+      hipLaunchKernelGGL((sort_kernel<kSortThreads, kMaxExperts>), dim3(1), block, 0, s, b, tile);
     return hipGetLastError();
   }
   const int64_t tile = sort_tile(a.slots);
@@ -706,7 +741,7 @@ hipError_t launch_expert_sort(const SortArgs& a, hipStream_t s) {
   hipLaunchKernelGGL(sort_hist_kernel, grid, block, 0, s, a, tile);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(sort_kernel, grid, block, 0, s, a, tile);
+  hipLaunchKernelGGL((sort_kernel<kSortThreads, kMaxExperts>), grid, block, 0, s, a, tile);
   return hipGetLastError();
 }
 

@@ -56,19 +56,25 @@ struct BlockScale {
   float inv, scale;
 };
 
-// Block scale. Elements past the end of the data are held as zeros, so they never raise the amax; a NaN
-// never compares greater, so it never counts. All 64 lanes of the wave must call it (DPP).
-__device__ __forceinline__ BlockScale block_scale(const float (&v)[kPerLane]) {
+// The largest magnitude of a lane's values. Elements past the end of the data are held as zeros, so they never raise it;
+// a NaN never compares greater, so it never counts.
+template <int N> __device__ __forceinline__ float lane_amax(const float* v) {
   float m = 0.0f;
 #pragma unroll
-  for (int k = 0; k < kPerLane; ++k) {
+  for (int k = 0; k < N; ++k) {
     const float a = fabsf(v[k]);
     m = a > m ? a : m;
   }
-  const float amax = row16_max(m);
+  return m;
+}
+__device__ __forceinline__ BlockScale scale_for(float amax) {
   const float inv = 448.0f / amax, scale = amax / 448.0f;  // amax == 0 gives inv = inf: replaced below
   const bool unit = !(amax > 0.0f) || __builtin_isinf(inv);
   return BlockScale{unit ? 1.0f : inv, unit ? 1.0f : scale};
+}
+// Block scale. All 64 lanes of the wave must call it (DPP).
+__device__ __forceinline__ BlockScale block_scale(const float (&v)[kPerLane]) {
+  return scale_for(row16_max(lane_amax<kPerLane>(v)));
 }
 
 }  // namespace ar

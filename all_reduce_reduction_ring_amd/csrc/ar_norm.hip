@@ -7,7 +7,7 @@
 //
 // Both are bound by HBM: a row is read once, held in registers while its sums are formed, and written once. A workgroup
 // takes a row (short rows: several to a wave; backward: several rows to a workgroup); a lane holds one slot of 8 elements,
-// laid out so that the 16 lanes of a DPP row hold one 128-element block, and a block's scale is a maximum over them. Sums,
+// laid out so that 16 or 32 neighbouring lanes hold one 128-element block, and a block's scale is a maximum over them. Sums,
 // statistics and the values that are quantised stay in fp32; h, y and dx are rounded once, when they are stored. The norm
 // is taken of the unrounded h. Times below are one MI355X's, a kernel or call among others.
 #include "ar_block.h"
@@ -17,15 +17,23 @@
 namespace ar {
 namespace {
 
-// A lane's slot of 8 elements is kVecs vectors: 2-byte types, elements [8 i, 8 i + 8) for slot index i; fp32, elements
-// [128 b + 4 l, + 4) and the same + 64 for i = 16 b + l, so that each access of a wave covers whole lines.
+// A lane's slot of 8 elements is kVecs vectors: 2-byte types, elements [8 i, 8 i + 8) for slot index i. fp32, whole waves:
+// elements [512 u + 4 l, + 4) and the same + 256 for i = 64 u + l, so that every access of a wave is 1 KiB in one piece
+// (rows that share cache lines, 6 x 4993 x 3545: 201 us; in pieces of 256 bytes 224); a 128-element block lies in 32 lanes'
+// vectors. fp32, rows of 16 or 32 lanes (MODE without kWide): [128 b + 4 l, + 4) and the same + 64 for i = 16 b + l.
+constexpr int kWide = 4;
+constexpr int policy(int mode) { return mode & 3; }
 template <int DT> constexpr int kVecs = Traits<DT>::kSize == 2 ? 1 : 2;
-template <int DT> __device__ __forceinline__ int first_of(int i) {
+template <int DT, int MODE> constexpr bool kTwoBlocks = kVecs<DT> == 2 && (MODE & kWide) != 0;
+template <int DT, int MODE> __device__ __forceinline__ int first_of(int i) {
   if constexpr (Traits<DT>::kSize == 2) return i * 8;
+  else if constexpr ((MODE & kWide) != 0) return (i >> 6) * 4 * kBlock + (i & 63) * 4;
   else return (i >> 4) * kBlock + (i & 15) * 4;
 }
 // The first element of vector v of the slot that starts at e0.
-__device__ __forceinline__ int vec_at(int e0, int v) { return e0 + v * (kBlock / 2); }
+template <int MODE> __device__ __forceinline__ int vec_at(int e0, int v) {
+  return e0 + v * ((MODE & kWide) != 0 ? 2 * kBlock : kBlock / 2);
+}
 
 template <int DT> struct Raw {
   u32x4 w[kVecs<DT>];
@@ -35,7 +43,7 @@ template <int DT> struct Raw {
 template <int DT, int MODE> __device__ __forceinline__ Raw<DT> load_raw(const void* row, int e0, int hidden) {
   Raw<DT> r;
 #pragma unroll
-  for (int v = 0; v < kVecs<DT>; ++v) r.w[v] = load_vec<DT, MODE>(row, vec_at(e0, v), hidden);
+  for (int v = 0; v < kVecs<DT>; ++v) r.w[v] = load_vec<DT, policy(MODE)>(row, vec_at<MODE>(e0, v), hidden);
   return r;
 }
 template <int DT> __device__ __forceinline__ void unpack_raw(const Raw<DT>& r, float (&v)[kPerLane]) {
@@ -49,7 +57,7 @@ template <int DT> __device__ __forceinline__ void unpack_raw(const Raw<DT>& r, f
 // Values read from clamped places, moved where they belong.
 template <int DT, int MODE> __device__ __forceinline__ void settle(float (&v)[kPerLane], int e0, int hidden) {
 #pragma unroll
-  for (int i = 0; i < kVecs<DT>; ++i) settle_vec<DT, MODE>(v + i * Traits<DT>::kVec, vec_at(e0, i), hidden);
+  for (int i = 0; i < kVecs<DT>; ++i) settle_vec<DT, policy(MODE)>(v + i * Traits<DT>::kVec, vec_at<MODE>(e0, i), hidden);
 }
 
 template <int NR, typename F> __device__ __forceinline__ void each_rank(int n, F f) {
@@ -71,9 +79,9 @@ __device__ __forceinline__ void store_slot(const float (&v)[kPerLane], int e0, i
 #pragma unroll
     for (int k = 0; k < V; ++k) x[k] = v[i * V + k];
     const u32x4 w = Slot<DT>::pack(x);
-    const int e = vec_at(e0, i);
+    const int e = vec_at<MODE>(e0, i);
     const uint32_t at = static_cast<uint32_t>(e) * kSize;
-    if (e + V <= hidden) each_rank<NR>(n, [&](int r) { st_row<MODE>(to(r), at, w); });
+    if (e + V <= hidden) each_rank<NR>(n, [&](int r) { st_row<policy(MODE)>(to(r), at, w); });
     else if (e < hidden) {
 #pragma unroll 1
       for (int r = 0; r < n; ++r) st_row_part<kSize>(to(r), at, w, (hidden - e) * kSize);
@@ -87,13 +95,13 @@ __device__ __forceinline__ void store_codes(const uint32_t (&w)[2], int e0, int 
   constexpr int V = Traits<DT>::kVec;
 #pragma unroll
   for (int i = 0; i < kVecs<DT>; ++i) {
-    const int e = vec_at(e0, i);
+    const int e = vec_at<MODE>(e0, i);
     if (e + V <= hidden) {
       each_rank<NR>(n, [&](int r) {
         uint8_t* p = to(r) + opaque(e);
-        if constexpr (V == 8 && MODE == kStream) __builtin_nontemporal_store(u32x2{w[0], w[1]}, gptr<u32x2_a1>(p));
+        if constexpr (V == 8 && policy(MODE) == kStream) __builtin_nontemporal_store(u32x2{w[0], w[1]}, gptr<u32x2_a1>(p));
         else if constexpr (V == 8) *gptr<u32x2_a1>(p) = u32x2{w[0], w[1]};
-        else if constexpr (MODE == kStream) __builtin_nontemporal_store(w[i], gptr<u32_a1>(p));
+        else if constexpr (policy(MODE) == kStream) __builtin_nontemporal_store(w[i], gptr<u32_a1>(p));
         else *gptr<u32_a1>(p) = w[i];
       });
     } else if (e < hidden) {
@@ -105,13 +113,13 @@ __device__ __forceinline__ void store_codes(const uint32_t (&w)[2], int e0, int 
 
 struct RawCodes {
   uint32_t w[2];
-  float scale;
+  float scale[2];  // of the two halves
 };
 template <int DT, int MODE>
 __device__ __forceinline__ RawCodes load_codes(const uint8_t* row, const float* scales, int e0, int hidden) {
   constexpr int V = Traits<DT>::kVec;
-  RawCodes r{{0, 0}, 0.0f};
-  if constexpr (MODE == kExact) {
+  RawCodes r{{0, 0}, {0.0f, 0.0f}};
+  if constexpr (policy(MODE) == kExact) {
     for (int k = 0; k < V; ++k)
       if (e0 + k < hidden) r.w[k >> 2] |= static_cast<uint32_t>(gptr<uint8_t>(row)[e0 + k]) << (8 * (k & 3));
   } else if constexpr (V == 8) {
@@ -119,10 +127,12 @@ __device__ __forceinline__ RawCodes load_codes(const uint8_t* row, const float* 
     r.w[0] = p[0];
     r.w[1] = p[1];
   } else {
-    r.w[0] = *gptr<u32_a1>(row + opaque(clamped<4>(vec_at(e0, 0), hidden)));
-    r.w[1] = *gptr<u32_a1>(row + opaque(clamped<4>(vec_at(e0, 1), hidden)));
+    r.w[0] = *gptr<u32_a1>(row + opaque(clamped<4>(vec_at<MODE>(e0, 0), hidden)));
+    r.w[1] = *gptr<u32_a1>(row + opaque(clamped<4>(vec_at<MODE>(e0, 1), hidden)));
   }
-  r.scale = *gptr<float>(scales + opaque((e0 < hidden ? e0 : hidden - 1) / kBlock));
+  auto scale_of = [&](int e) { return *gptr<float>(scales + opaque((e < hidden ? e : hidden - 1) / kBlock)); };
+  r.scale[0] = scale_of(e0);
+  r.scale[1] = kTwoBlocks<DT, MODE> ? scale_of(vec_at<MODE>(e0, 1)) : r.scale[0];
   return r;
 }
 __device__ __forceinline__ void unpack_codes(const RawCodes& r, float (&v)[kPerLane]) {
@@ -130,10 +140,10 @@ __device__ __forceinline__ void unpack_codes(const RawCodes& r, float (&v)[kPerL
   for (int i = 0; i < 2; ++i) {
     const f32x2 lo = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(r.w[i]), false);
     const f32x2 hi = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(r.w[i]), true);
-    v[4 * i] = lo[0] * r.scale;
-    v[4 * i + 1] = lo[1] * r.scale;
-    v[4 * i + 2] = hi[0] * r.scale;
-    v[4 * i + 3] = hi[1] * r.scale;
+    v[4 * i] = lo[0] * r.scale[i];
+    v[4 * i + 1] = lo[1] * r.scale[i];
+    v[4 * i + 2] = hi[0] * r.scale[i];
+    v[4 * i + 3] = hi[1] * r.scale[i];
   }
 }
 
@@ -145,7 +155,7 @@ template <int DT, int MODE> __device__ __forceinline__ RawGamma load_gamma(const
   RawGamma r;
   if (Traits<DT>::kSize == 2 && a.gamma_f32) {
     const uint32_t at = clamped<kPerLane>(e0, a.hidden) * 4;
-    if constexpr (MODE == kExact) {
+    if constexpr (policy(MODE) == kExact) {
 #pragma unroll
       for (int k = 0; k < kPerLane; ++k) r.w[k >> 2][k & 3] = e0 + k < a.hidden ? gptr<uint32_t>(a.gamma)[e0 + k] : 0;
     } else {
@@ -153,7 +163,7 @@ template <int DT, int MODE> __device__ __forceinline__ RawGamma load_gamma(const
       r.w[1] = ld_row<kCached>(a.gamma, at + 16);
     }
   } else {
-    const Raw<DT> x = load_raw<DT, MODE == kExact ? kExact : kCached>(a.gamma, e0, a.hidden);
+    const Raw<DT> x = load_raw<DT, (policy(MODE) == kExact ? kExact : kCached) | (MODE & kWide)>(a.gamma, e0, a.hidden);
 #pragma unroll
     for (int v = 0; v < kVecs<DT>; ++v) r.w[v] = x.w[v];
   }
@@ -239,17 +249,45 @@ __device__ __forceinline__ void sum_ranks(const ArgsFor<NR>& a, const RankSlots<
   }
 }
 
-// One row's slot as codes: the scale per block by the codec's rule. All 64 lanes take part.
-__device__ __forceinline__ void quant8(const float (&v)[kPerLane], float* scale, uint32_t (&w)[2]) {
-  const BlockScale s = block_scale(v);
+// One row's slot as codes: the scale per block by the codec's rule. All lanes of the row take part.
+template <int DT, int MODE>
+__device__ __forceinline__ void quant8(const float (&v)[kPerLane], float (&scale)[2], uint32_t (&w)[2]) {
+  float inv[2];
+  if constexpr (kTwoBlocks<DT, MODE>) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float m = row16_max(lane_amax<4>(v + 4 * i)), other = __shfl_xor(m, 16, 64);
+      const BlockScale s = scale_for(m > other ? m : other);
+      inv[i] = s.inv;
+      scale[i] = s.scale;
+    }
+  } else {
+    const BlockScale s = block_scale(v);
+    inv[0] = inv[1] = s.inv;
+    scale[0] = scale[1] = s.scale;
+  }
   float q[kPerLane], r[kPerLane];
 #pragma unroll
-  for (int k = 0; k < kPerLane; ++k) q[k] = v[k] * s.inv;
+  for (int k = 0; k < kPerLane; ++k) q[k] = v[k] * inv[k >> 2];
   e4m3_round4(q, r, &w[0]);
   e4m3_round4(q + 4, r + 4, &w[1]);
   w[0] = canonical_nan_codes(w[0]);
   w[1] = canonical_nan_codes(w[1]);
-  *scale = s.scale;
+}
+
+// The scales of slot i to the row of scales `to(r)` of every rank, by the first lane of each block.
+template <int DT, int NR, int MODE, typename F>
+__device__ __forceinline__ void store_scales(const float (&scale)[2], int i, int hidden, int n, F to) {
+  const int e0 = first_of<DT, MODE>(i);
+  if constexpr (kTwoBlocks<DT, MODE>) {
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+      const int e = vec_at<MODE>(e0, v);
+      if ((i & 31) == 0 && e < hidden) each_rank<NR>(n, [&](int r) { *gptr<float>(to(r) + opaque(e / kBlock)) = scale[v]; });
+    }
+  } else {
+    if ((i & 15) == 0 && e0 < hidden) each_rank<NR>(n, [&](int r) { *gptr<float>(to(r) + opaque(i >> 4)) = scale[0]; });
+  }
 }
 
 // One workgroup, one row; LANES > 0: LANES lanes to a row (rows of at most LANES slots). One slot a lane wherever 1024
@@ -272,10 +310,10 @@ __global__ __launch_bounds__(kMaxThreads) void rmsnorm_kernel(ArgsFor<NR> a, int
   RawGamma gam[S];
   float ss = 0.0f;
 #pragma unroll
-  for (int s = 0; s < S; ++s) gam[s] = load_gamma<DT, MODE>(a, first_of<DT>(s * threads + tid));
+  for (int s = 0; s < S; ++s) gam[s] = load_gamma<DT, MODE>(a, first_of<DT, MODE>(s * threads + tid));
 #pragma unroll
   for (int s = 0; s < S; ++s) {
-    const int e0 = first_of<DT>(s * threads + tid);
+    const int e0 = first_of<DT, MODE>(s * threads + tid);
     RankSlots<DT, NR, MODE> first;
     Raw<DT> res;
     first.load(a, at * kSize, e0, 0);
@@ -299,27 +337,26 @@ __global__ __launch_bounds__(kMaxThreads) void rmsnorm_kernel(ArgsFor<NR> a, int
 #pragma unroll
   for (int s = 0; s < S; ++s) {
     const int i = s * threads + tid;
-    const int e0 = first_of<DT>(i);
-    const bool block_lane = (i & 15) == 0 && e0 < a.hidden;
+    const int e0 = first_of<DT, MODE>(i);
     if (a.residual_out)
       store_slot<DT, 1, MODE>(h[s], e0, a.hidden, 1, [&](int) { return static_cast<char*>(a.residual_out) + at * kSize; });
     if (a.codes) {
-      float sc;
+      float sc[2];
       uint32_t w[2];
-      quant8(h[s], &sc, w);
+      quant8<DT, MODE>(h[s], sc, w);
       store_codes<DT, 1, MODE>(w, e0, a.hidden, 1, [&](int) { return a.codes + at; });
-      if (block_lane) gptr<float>(a.scales + row * nb)[i >> 4] = sc;
+      store_scales<DT, 1, MODE>(sc, i, a.hidden, 1, [&](int) { return a.scales + row * nb; });
     }
     float y[kPerLane];
     unpack_gamma<DT, MODE>(a, gam[s], e0, y);
 #pragma unroll
     for (int k = 0; k < kPerLane; ++k) y[k] = h[s][k] * rstd * y[k];
     if (a.out8) {
-      float sc;
+      float sc[2];
       uint32_t w[2];
-      quant8(y, &sc, w);
+      quant8<DT, MODE>(y, sc, w);
       store_codes<DT, NR, MODE>(w, e0, a.hidden, a.n, [&](int r) { return static_cast<uint8_t*>(a.out[r]) + at; });
-      if (block_lane) each_rank<NR>(a.n, [&](int r) { *gptr<float>(a.out_scales[r] + row * nb + opaque(i >> 4)) = sc; });
+      store_scales<DT, NR, MODE>(sc, i, a.hidden, a.n, [&](int r) { return a.out_scales[r] + row * nb; });
     } else {
       store_slot<DT, NR, MODE>(y, e0, a.hidden, a.n, [&](int r) { return static_cast<char*>(a.out[r]) + at * kSize; });
     }
@@ -345,11 +382,11 @@ template <int DT, int NR, int MODE> struct BwdSlot {
 };
 
 // dgamma of one 128-element block of columns by a whole workgroup: 16 lanes to a row, every row once.
-template <int DT, int NR, int MODE>
+template <int DT, int NR, int WIDE_MODE>
 __device__ __forceinline__ void columns_dgamma(const ArgsFor<NR>& a, int block, float* lds, float* dgamma) {
-  constexpr int V = Traits<DT>::kVec;
+  constexpr int V = Traits<DT>::kVec, MODE = policy(WIDE_MODE);
   const int lane = threadIdx.x & 15, at_once = static_cast<int>(blockDim.x) >> 4;
-  const int e0 = first_of<DT>(block * 16 + lane);
+  const int e0 = first_of<DT, MODE>(block * 16 + lane);
   float dg[kPerLane];
 #pragma unroll
   for (int k = 0; k < kPerLane; ++k) dg[k] = 0.0f;
@@ -376,7 +413,7 @@ __device__ __forceinline__ void columns_dgamma(const ArgsFor<NR>& a, int block, 
     float sum = 0.0f;
     for (int w = 0; w < static_cast<int>(blockDim.x) >> 6; ++w) sum += lds[w * kBlock + threadIdx.x];
     const int k = threadIdx.x % kPerLane;
-    const int e = vec_at(first_of<DT>(block * 16 + static_cast<int>(threadIdx.x) / kPerLane), k / V) + k % V;
+    const int e = vec_at<MODE>(first_of<DT, MODE>(block * 16 + static_cast<int>(threadIdx.x) / kPerLane), k / V) + k % V;
     if (e < a.hidden) gptr<float>(dgamma)[e] = sum;
   }
 }
@@ -411,7 +448,7 @@ __global__ __launch_bounds__(kMaxThreads) void rmsnorm_bwd_kernel(ArgsFor<NR> a,
   RawGamma gam[S];
 #pragma unroll
   for (int s = 0; s < S; ++s) {
-    if (S < 4) gam[s] = load_gamma<DT, MODE>(a, first_of<DT>(s * team_threads + tid));
+    if (S < 4) gam[s] = load_gamma<DT, MODE>(a, first_of<DT, MODE>(s * team_threads + tid));
 #pragma unroll
     for (int k = 0; k < kPerLane; ++k) dg[s][k] = 0.0f;
   }
@@ -420,7 +457,7 @@ __global__ __launch_bounds__(kMaxThreads) void rmsnorm_bwd_kernel(ArgsFor<NR> a,
   float rstd_next = 0.0f;
   int64_t base = static_cast<int64_t>(blockIdx.x) * teams;
   if (kAhead && base + team < a.rows) {
-    next.load(a, base + team, first_of<DT>(tid), a.residual);
+    next.load(a, base + team, first_of<DT, MODE>(tid), a.residual);
     rstd_next = gptr<float>(a.rstd_in)[base + team];
   }
   for (; base < a.rows; base += step, flip ^= 1) {  // all teams stay in the loop for the barriers in it
@@ -433,7 +470,7 @@ __global__ __launch_bounds__(kMaxThreads) void rmsnorm_bwd_kernel(ArgsFor<NR> a,
       rstd = kAhead ? rstd_next : gptr<float>(a.rstd_in)[row];
 #pragma unroll
       for (int s = 0; s < S; ++s) {
-        const int e0 = first_of<DT>(s * team_threads + tid);
+        const int e0 = first_of<DT, MODE>(s * team_threads + tid);
         BwdSlot<DT, NR, MODE> x;
         if (kAhead) x = next;
         else x.load(a, row, e0, a.residual);
@@ -462,7 +499,7 @@ __global__ __launch_bounds__(kMaxThreads) void rmsnorm_bwd_kernel(ArgsFor<NR> a,
           for (int v = 0; v < kVecs<DT>; ++v) arrived(res[s].w[v]);
       }
       if (kAhead && row + step < a.rows) {
-        next.load(a, row + step, first_of<DT>(tid), a.residual);
+        next.load(a, row + step, first_of<DT, MODE>(tid), a.residual);
         rstd_next = gptr<float>(a.rstd_in)[row + step];
       }
     }
@@ -479,7 +516,7 @@ __global__ __launch_bounds__(kMaxThreads) void rmsnorm_bwd_kernel(ArgsFor<NR> a,
     const float mean = dot / static_cast<float>(a.hidden);
 #pragma unroll
     for (int s = 0; s < S; ++s) {
-      const int e0 = first_of<DT>(s * team_threads + tid);
+      const int e0 = first_of<DT, MODE>(s * team_threads + tid);
 #pragma unroll
       for (int k = 0; k < kPerLane; ++k) g[s][k] = rstd * (g[s][k] - xh[s][k] * mean);
       if (a.residual) {
@@ -523,10 +560,10 @@ __global__ __launch_bounds__(kMaxThreads) void rmsnorm_bwd_kernel(ArgsFor<NR> a,
   float* to = a.partial + static_cast<int64_t>(blockIdx.x) * a.hidden;
 #pragma unroll
   for (int s = 0; s < S; ++s) {
-    const int e0 = first_of<DT>(s * team_threads + tid);
+    const int e0 = first_of<DT, MODE>(s * team_threads + tid);
 #pragma unroll
     for (int k = 0; k < kPerLane; ++k) {
-      const int e = vec_at(e0, k / Traits<DT>::kVec) + k % Traits<DT>::kVec;
+      const int e = vec_at<MODE>(e0, k / Traits<DT>::kVec) + k % Traits<DT>::kVec;
       if (e < a.hidden) gptr<float>(to)[e] = dg[s][k];
     }
   }
@@ -666,8 +703,8 @@ hipError_t run_fwd(const NormArgs& a, const Shape& sh, hipStream_t s) {
 template <int DT, int S, int NR, int MODE, int LANES>
 hipError_t run(const NormArgs& a, float* dgamma, const Shape& sh, hipStream_t s) {
   if (!dgamma) return run_fwd<DT, S, NR, MODE, LANES>(a, sh, s);
-  if constexpr (S == 1 && MODE != kStream) {
-    if (reads_twice(a, Traits<DT>::kSize)) return run_bwd_once<DT, NR, MODE>(a, dgamma, s);
+  if constexpr (S == 1 && policy(MODE) != kStream) {
+    if (reads_twice(a, Traits<DT>::kSize)) return run_bwd_once<DT, NR, MODE | kWide>(a, dgamma, s);
   }
   return run_bwd<DT, S, NR, MODE, LANES>(a, sh, dgamma, s);
 }
@@ -690,10 +727,10 @@ template <int DT> hipError_t launch(const NormArgs& a, float* dgamma, hipStream_
   if (sh.threads == 16) return run_n<DT, 1, kCached, 16>(a, dgamma, sh, s);
   if (sh.threads == 32) return run_n<DT, 1, kCached, 32>(a, dgamma, sh, s);
   if (sh.slots == 1)
-    return streams(a.rows * row * (2 * a.n + 2), row) ? run_n<DT, 1, kStream, 0>(a, dgamma, sh, s)
-                                                      : run_n<DT, 1, kCached, 0>(a, dgamma, sh, s);
-  if (sh.slots == 2) return run_n<DT, 2, kCached, 0>(a, dgamma, sh, s);
-  return run_n<DT, 4, kCached, 0>(a, dgamma, sh, s);
+    return streams(a.rows * row * (2 * a.n + 2), row) ? run_n<DT, 1, kStream | kWide, 0>(a, dgamma, sh, s)
+                                                      : run_n<DT, 1, kCached | kWide, 0>(a, dgamma, sh, s);
+  if (sh.slots == 2) return run_n<DT, 2, kCached | kWide, 0>(a, dgamma, sh, s);
+  return run_n<DT, 4, kCached | kWide, 0>(a, dgamma, sh, s);
 }
 
 }  // namespace

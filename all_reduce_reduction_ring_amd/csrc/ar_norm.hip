@@ -60,6 +60,8 @@ template <int DT, int MODE> __device__ __forceinline__ void settle(float (&v)[kP
   for (int i = 0; i < kVecs<DT>; ++i) settle_vec<DT, policy(MODE)>(v + i * Traits<DT>::kVec, vec_at<MODE>(e0, i), hidden);
 }
 
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
 template <int NR, typename F> __device__ __forceinline__ void each_rank(int n, F f) {
   if constexpr (NR > 0) {
 #pragma unroll
@@ -431,6 +433,8 @@ __global__ __launch_bounds__(kMaxThreads) void rmsnorm_bwd_kernel(ArgsFor<NR> a,
   constexpr bool kAhead = S == 1 && (Traits<DT>::kSize == 2 || NR < 8);
   __shared__ float lds[2][kMaxThreads / 64];
   __shared__ float join[S == 1 ? kTeamThreads * kPerLane : 1];
+  // Wide rows: dgamma's sums lie in LDS (each thread its own), so that the row's values keep the registers.
+  __shared__ f32x4 wide_dg[S == 1 ? 1 : 2 * S * kMaxThreads];
   constexpr int kSize = Traits<DT>::kSize;
   if constexpr (SMALL) {
     if (static_cast<int>(blockIdx.x) >= groups) {
@@ -444,13 +448,13 @@ __global__ __launch_bounds__(kMaxThreads) void rmsnorm_bwd_kernel(ArgsFor<NR> a,
                              : 0;
   const int tid = static_cast<int>(threadIdx.x) - team * team_threads;
   const int64_t step = static_cast<int64_t>(groups) * teams;
-  float dg[S][kPerLane];
-  RawGamma gam[S];
+  float dg[1][kPerLane];
+  RawGamma gam;
+  if constexpr (S == 1) gam = load_gamma<DT, MODE>(a, first_of<DT, MODE>(tid));
 #pragma unroll
-  for (int s = 0; s < S; ++s) {
-    if (S < 4) gam[s] = load_gamma<DT, MODE>(a, first_of<DT, MODE>(s * team_threads + tid));
-#pragma unroll
-    for (int k = 0; k < kPerLane; ++k) dg[s][k] = 0.0f;
+  for (int k = 0; k < kPerLane; ++k) dg[0][k] = 0.0f;
+  if constexpr (S > 1) {
+    for (int i = 0; i < 2 * S; ++i) wide_dg[i * kMaxThreads + tid] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   }
   int flip = 0;
   BwdSlot<DT, NR, MODE> next;
@@ -481,11 +485,21 @@ __global__ __launch_bounds__(kMaxThreads) void rmsnorm_bwd_kernel(ArgsFor<NR> a,
         settle<DT, MODE>(xh[s], e0, a.hidden);
         res[s] = x.res;
         float y[kPerLane];
-        unpack_gamma<DT, MODE>(a, S < 4 ? gam[s] : load_gamma<DT, MODE>(a, e0), e0, y);
+        unpack_gamma<DT, MODE>(a, S == 1 ? gam : load_gamma<DT, MODE>(a, e0), e0, y);
+#pragma unroll
+        for (int k = 0; k < kPerLane; ++k) xh[s][k] *= rstd;
+        if constexpr (S > 1) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            f32x4 sum = wide_dg[(2 * s + i) * kMaxThreads + tid];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) sum[k] += g[s][4 * i + k] * xh[s][4 * i + k];
+            wide_dg[(2 * s + i) * kMaxThreads + tid] = sum;
+          }
+        }
 #pragma unroll
         for (int k = 0; k < kPerLane; ++k) {
-          xh[s][k] *= rstd;
-          dg[s][k] += g[s][k] * xh[s][k];
+          if constexpr (S == 1) dg[0][k] += g[s][k] * xh[s][k];
           g[s][k] *= y[k];
           dot += g[s][k] * xh[s][k];
         }
@@ -564,7 +578,9 @@ __global__ __launch_bounds__(kMaxThreads) void rmsnorm_bwd_kernel(ArgsFor<NR> a,
 #pragma unroll
     for (int k = 0; k < kPerLane; ++k) {
       const int e = vec_at<MODE>(e0, k / Traits<DT>::kVec) + k % Traits<DT>::kVec;
-      if (e < a.hidden) gptr<float>(to)[e] = dg[s][k];
+      float sum = dg[0][k];
+      if constexpr (S > 1) sum = wide_dg[(2 * s + k / 4) * kMaxThreads + tid][k % 4];
+      if (e < a.hidden) gptr<float>(to)[e] = sum;
     }
   }
 }

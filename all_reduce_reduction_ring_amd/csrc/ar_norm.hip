@@ -731,6 +731,7 @@ hipError_t run_n(const NormArgs& a, float* dgamma, const Shape& sh, hipStream_t 
     case 2: return run<DT, S, 2, MODE, LANES>(a, dgamma, sh, s);
     case 3: return run<DT, S, 3, MODE, LANES>(a, dgamma, sh, s);
     case 4: return run<DT, S, 4, MODE, LANES>(a, dgamma, sh, s);
+    case 6: return run<DT, S, 6, MODE, LANES>(a, dgamma, sh, s);
     case 8: return run<DT, S, 8, MODE, LANES>(a, dgamma, sh, s);
     default: return run<DT, S, 0, MODE, LANES>(a, dgamma, sh, s);
   }

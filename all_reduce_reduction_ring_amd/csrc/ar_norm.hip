@@ -426,6 +426,8 @@ __device__ __forceinline__ void columns_dgamma(const ArgsFor<NR>& a, int block, 
 // order. One slot a lane (S = 1): the next row is read while this one's dot product is joined and its results are
 // stored. Wider rows (S > 1) have one team and read their row when its turn comes.
 // LANES > 0: a team is LANES lanes of a wave (rows of at most LANES slots).
+// 8 x 8192 x 4096 bf16 from 8 bits 213 us (5.5 TB/s), one rank, 16,384 x 2048 47 us (5.8 TB/s); a workgroup per row without
+// reading ahead ran 231 and 55 us.
 // SMALL: no second launch; the workgroups from `groups` on each sum a block of columns instead, reading those again.
 template <int DT, int S, int NR, int MODE, bool SMALL, int LANES>
 __global__ __launch_bounds__(kMaxThreads) void rmsnorm_bwd_kernel(ArgsFor<NR> a, int team_threads, int groups,

@@ -11,6 +11,7 @@
 // sorted rows, which are whole rows wherever they lie, once each. Rows out of [0, rows) are taken as absent.
 #include "ar_block.h"
 #include "ar_internal.h"
+#include "ar_steps.h"
 
 namespace ar {
 namespace {
@@ -253,20 +254,20 @@ __device__ __forceinline__ void zero_pads(const MoveArgs& a, int group, int part
 // lanes of 2 252 us, 128 of 2 243, 64 of 2, 4 or 8 249 to 251, a wave per choice 248. Rows of 512 bytes to 16 KiB agree.
 constexpr int kCopyLanes = 128, kCopyUnroll = 4;
 template <int MODE>
-__global__ __launch_bounds__(kCopyLanes) void dispatch_kernel(MoveArgs a, int row_bytes, int scale_bytes, int pad_groups,
-                                                              int pad_parts) {
+__global__ __launch_bounds__(kCopyLanes) void dispatch_kernel(MoveArgs a, row_bytes_t row_bytes, row_bytes_t scale_bytes,
+                                                              int pad_groups, int pad_parts) {
   constexpr int LANES = kCopyLanes, U = kCopyUnroll;
   if (static_cast<int>(blockIdx.x) < pad_groups) {
     zero_pads(a, static_cast<int>(blockIdx.x), pad_parts, row_bytes, scale_bytes);
     return;
   }
-  const int lane = threadIdx.x;
+  const row_bytes_t lane = threadIdx.x;
   for (int64_t t = blockIdx.x - pad_groups; t < a.tokens; t += gridDim.x - pad_groups) {
     const char* from = static_cast<const char*>(a.x) + t * row_bytes;
     int p[kChoices];
     // Small calls read the row while the positions are on their way (48 tokens of 4096 bytes with the sort: 7.0 -> 6.0 us).
     // Large ones are faster the other way round (16,384 x 8 rows of 8 KiB with the sort: 234 against 252 us).
-    auto put = [&](const u32x4 (&v)[U], const uint32_t (&at)[U], int b0) {
+    auto put = [&](const u32x4 (&v)[U], const uint32_t (&at)[U], row_bytes_t b0) {
 #pragma unroll
       for (int j = 0; j < kChoices; ++j) {
         if (p[j] < 0) continue;
@@ -276,26 +277,26 @@ __global__ __launch_bounds__(kCopyLanes) void dispatch_kernel(MoveArgs a, int ro
           if (b0 + u * LANES * 16 < row_bytes) st_row<MODE>(to, at[u], v[u]);
       }
     };
-    auto get = [&](u32x4 (&v)[U], uint32_t (&at)[U], int b0) {
+    auto get = [&](u32x4 (&v)[U], uint32_t (&at)[U], row_bytes_t b0) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        at[u] = clamped<16>(b0 + u * LANES * 16, row_bytes);
+        at[u] = vector_place(b0 + u * LANES * 16, row_bytes);
         v[u] = ld_row<kCached>(from, at[u]);
       }
     };
     u32x4 v[U];
     uint32_t at[U];
-    if (row_bytes >= 16) {
+    if (row_bytes >= kVectorBytes) {
       if constexpr (MODE == kStream) {
         for (int j0 = 0; j0 < a.k; j0 += kChoices) {
           load_rows(a, t, j0, p);
-          for (int b0 = lane * 16; b0 < row_bytes; b0 += LANES * U * 16) {
+          for (row_bytes_t b0 = lane * 16; b0 < row_bytes; b0 += LANES * U * 16) {
             get(v, at, b0);
             put(v, at, b0);
           }
         }
       } else {
-        for (int b0 = 0; b0 < row_bytes; b0 += LANES * U * 16) {
+        for (row_bytes_t b0 = 0; b0 < row_bytes; b0 += LANES * U * 16) {
           get(v, at, b0 + lane * 16);
           for (int j0 = 0; j0 < a.k; j0 += kChoices) {
             if (b0 == 0 || a.k > kChoices) load_rows(a, t, j0, p);
@@ -305,14 +306,14 @@ __global__ __launch_bounds__(kCopyLanes) void dispatch_kernel(MoveArgs a, int ro
       }
     }
     for (int j0 = 0; j0 < a.k; j0 += kChoices) {
-      if (row_bytes < 16 || a.k > kChoices) load_rows(a, t, j0, p);
-      if (row_bytes < 16 && lane < row_bytes) {
+      if (row_bytes < kVectorBytes || a.k > kChoices) load_rows(a, t, j0, p);
+      if (row_bytes < kVectorBytes && lane < row_bytes) {
         const uint8_t v = gptr<uint8_t>(from)[lane];
 #pragma unroll
         for (int j = 0; j < kChoices; ++j)
           if (p[j] >= 0) gptr<uint8_t>(static_cast<char*>(a.y) + p[j] * static_cast<int64_t>(row_bytes))[lane] = v;
       }
-      for (int b = lane * 4; b < scale_bytes; b += LANES * 4) {
+      for (row_bytes_t b = lane * 4; b < scale_bytes; b += LANES * 4) {
         const uint32_t v = *gptr<uint32_t>(static_cast<const char*>(a.x_scales) + t * scale_bytes + opaque(b));
 #pragma unroll
         for (int j = 0; j < kChoices; ++j)
@@ -509,17 +510,18 @@ __device__ __forceinline__ void load_rows_each(const MoveArgs& a, int64_t t, int
 }
 
 template <int LANES>
-__global__ __launch_bounds__(kShortThreads) void dispatch_short_kernel(MoveArgs a, int row_bytes, int scale_bytes,
-                                                                       int pad_groups, int pad_parts) {
+__global__ __launch_bounds__(kShortThreads) void dispatch_short_kernel(MoveArgs a, row_bytes_t row_bytes,
+                                                                       row_bytes_t scale_bytes, int pad_groups,
+                                                                       int pad_parts) {
   if (static_cast<int>(blockIdx.x) < pad_groups) {
     zero_pads(a, static_cast<int>(blockIdx.x), pad_parts, row_bytes, scale_bytes);
     return;
   }
   constexpr int kTokens = kShortThreads / LANES;
-  const int lane = threadIdx.x % LANES;
+  const row_bytes_t lane = threadIdx.x % LANES;
   for (int64_t t = static_cast<int64_t>(blockIdx.x - pad_groups) * kTokens + threadIdx.x / LANES; t < a.tokens;
        t += static_cast<int64_t>(gridDim.x - pad_groups) * kTokens) {
-    const int64_t at = clamped<16>(lane * 16, row_bytes);
+    const int64_t at = vector_place(lane * 16, row_bytes);
     const u32x4 v = ldu16(static_cast<const char*>(a.x) + t * row_bytes + at);
     uint32_t sc = 0;
     if (lane * 4 < scale_bytes) sc = *gptr<uint32_t>(static_cast<const char*>(a.x_scales) + t * scale_bytes + lane * 4);
@@ -754,11 +756,12 @@ hipError_t launch_expert_sort(const SortArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_expert_dispatch(const MoveArgs& a, int esize, hipStream_t s) {
-  const int row = a.hidden * esize, scale = a.x_scales ? (a.hidden + AR_FP8_BLOCK - 1) / AR_FP8_BLOCK * 4 : 0;
+  const row_bytes_t row = static_cast<row_bytes_t>(a.hidden) * static_cast<row_bytes_t>(esize);
+  const row_bytes_t scale = a.x_scales ? row_scale_bytes(static_cast<row_bytes_t>(a.hidden), AR_FP8_BLOCK) : 0;
   if (a.tokens == 0) return hipSuccess;
   const int parts = pad_parts(a, row);
   const int pads = a.offsets ? a.experts * parts : 0;
-  const int lanes = row < 16 ? 0 : short_lanes((row + 15) / 16);
+  const int lanes = row < kVectorBytes ? 0 : short_lanes(row_vectors(row));
   if (lanes) {
     const dim3 grid(short_groups(a.tokens, lanes) + pads), block(kShortThreads);
     if (lanes == 8) hipLaunchKernelGGL(dispatch_short_kernel<8>, grid, block, 0, s, a, row, scale, pads, parts);

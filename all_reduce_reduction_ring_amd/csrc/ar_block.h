@@ -3,6 +3,7 @@
 #pragma once
 
 #include "ar_device.h"
+#include "ar_steps.h"
 
 namespace ar {
 
@@ -70,7 +71,7 @@ struct MoveArgs {
   int64_t tokens;
   int64_t rows;
   int hidden;              // rows are below 2^31 bytes
-  int k;
+  choice_t k;
   int experts;
 };
 hipError_t launch_expert_dispatch(const MoveArgs& a, int esize, hipStream_t s);

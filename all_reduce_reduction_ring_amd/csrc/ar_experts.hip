@@ -11,7 +11,6 @@
 // sorted rows, which are whole rows wherever they lie, once each. Rows out of [0, rows) are taken as absent.
 #include "ar_block.h"
 #include "ar_internal.h"
-#include "ar_steps.h"
 
 namespace ar {
 namespace {
@@ -202,10 +201,8 @@ __global__ __launch_bounds__(T) void sort_kernel(SortArgs a, int64_t tile) {
 // ------------------------------------------------------------------------------------------ rows
 // A workgroup of LANES threads (64, 128 or 256) takes a token. What it knows about the token's rows is kept in scalar
 // registers: the rows' addresses and the tests whether they are there.
-constexpr int kChoices = 8;  // choices of a token handled together
-
 // The rows of choices j0 .. j0 + 7 of token t (-1: none); in scalar registers. One load for all of them.
-__device__ __forceinline__ void load_rows(const MoveArgs& a, int64_t t, int j0, int (&p)[kChoices]) {
+__device__ __forceinline__ void load_rows(const MoveArgs& a, int64_t t, choice_t j0, int (&p)[kChoices]) {
   const int lane = threadIdx.x & 63;
   int v = -1;
   if (lane < kChoices && j0 + lane < a.k) v = gptr<int32_t>(a.pos + t * a.k)[j0 + lane];
@@ -214,7 +211,7 @@ __device__ __forceinline__ void load_rows(const MoveArgs& a, int64_t t, int j0, 
   for (int j = 0; j < kChoices; ++j) p[j] = __builtin_amdgcn_readlane(v, j);
 }
 // Their weights, 0 where there is no row.
-__device__ __forceinline__ void load_weights(const MoveArgs& a, int64_t t, int j0, const int (&p)[kChoices],
+__device__ __forceinline__ void load_weights(const MoveArgs& a, int64_t t, choice_t j0, const int (&p)[kChoices],
                                              float (&w)[kChoices]) {
   const int lane = threadIdx.x & 63;
   float v = 1.0f;
@@ -288,7 +285,7 @@ __global__ __launch_bounds__(kCopyLanes) void dispatch_kernel(MoveArgs a, row_by
     uint32_t at[U];
     if (row_bytes >= kVectorBytes) {
       if constexpr (MODE == kStream) {
-        for (int j0 = 0; j0 < a.k; j0 += kChoices) {
+        for (choice_t j0 = 0; j0 < a.k; j0 += kChoices) {
           load_rows(a, t, j0, p);
           for (row_bytes_t b0 = lane * 16; b0 < row_bytes; b0 += LANES * U * 16) {
             get(v, at, b0);
@@ -298,14 +295,14 @@ __global__ __launch_bounds__(kCopyLanes) void dispatch_kernel(MoveArgs a, row_by
       } else {
         for (row_bytes_t b0 = 0; b0 < row_bytes; b0 += LANES * U * 16) {
           get(v, at, b0 + lane * 16);
-          for (int j0 = 0; j0 < a.k; j0 += kChoices) {
+          for (choice_t j0 = 0; j0 < a.k; j0 += kChoices) {
             if (b0 == 0 || a.k > kChoices) load_rows(a, t, j0, p);
             put(v, at, b0 + lane * 16);
           }
         }
       }
     }
-    for (int j0 = 0; j0 < a.k; j0 += kChoices) {
+    for (choice_t j0 = 0; j0 < a.k; j0 += kChoices) {
       if (row_bytes < kVectorBytes || a.k > kChoices) load_rows(a, t, j0, p);
       if (row_bytes < kVectorBytes && lane < row_bytes) {
         const uint8_t v = gptr<uint8_t>(from)[lane];
@@ -354,7 +351,7 @@ __global__ __launch_bounds__(LANES) void combine_kernel(MoveArgs a) {
           add[u] = load_vec<DT, MODE>(static_cast<const char*>(a.extra) + t * row, b0 + u * LANES * V + lane_elem<DT>(),
                                        a.hidden);
       }
-      for (int j0 = 0; j0 < a.k; j0 += kChoices) {
+      for (choice_t j0 = 0; j0 < a.k; j0 += kChoices) {
         if (a.k > kChoices) {
           load_rows(a, t, j0, p);
           load_weights(a, t, j0, p, w);
@@ -413,7 +410,7 @@ __global__ __launch_bounds__(LANES) void combine_bwd_kernel(MoveArgs a, int pad_
   }
   int flip = 0;
   for (int64_t t = blockIdx.x - pad_groups; t < a.tokens; t += gridDim.x - pad_groups) {
-    for (int j0 = 0; j0 < a.k; j0 += kChoices, flip ^= 1) {
+    for (choice_t j0 = 0; j0 < a.k; j0 += kChoices, flip ^= 1) {
       u32x4 d[U];
       auto load_grad = [&](int b0) {
 #pragma unroll
@@ -472,7 +469,7 @@ __global__ __launch_bounds__(LANES) void combine_bwd_kernel(MoveArgs a, int pad_
           for (int j = 0; j < kChoices; ++j) lds[flip][threadIdx.x >> 6][j] = dot[j];
         }
         __syncthreads();  // one buffer is read while the next step fills the other
-        if (threadIdx.x < kChoices && j0 + static_cast<int>(threadIdx.x) < a.k) {
+        if (threadIdx.x < kChoices && j0 + threadIdx.x < a.k) {
           float sum = 0.0f;
 #pragma unroll
           for (int u = 0; u < kWaves; ++u) sum += lds[flip][u][threadIdx.x];
@@ -502,7 +499,7 @@ int64_t sort_tile(int64_t slots) {
 constexpr int kShortThreads = 256;
 
 // The rows of choices j0 .. j0 + 7 of token t (-1: none), one register each.
-__device__ __forceinline__ void load_rows_each(const MoveArgs& a, int64_t t, int j0, int (&p)[kChoices]) {
+__device__ __forceinline__ void load_rows_each(const MoveArgs& a, int64_t t, choice_t j0, int (&p)[kChoices]) {
 #pragma unroll
   for (int j = 0; j < kChoices; ++j) p[j] = j0 + j < a.k ? gptr<int32_t>(a.pos + t * a.k)[j0 + j] : -1;
 #pragma unroll
@@ -525,7 +522,7 @@ __global__ __launch_bounds__(kShortThreads) void dispatch_short_kernel(MoveArgs 
     const u32x4 v = ldu16(static_cast<const char*>(a.x) + t * row_bytes + at);
     uint32_t sc = 0;
     if (lane * 4 < scale_bytes) sc = *gptr<uint32_t>(static_cast<const char*>(a.x_scales) + t * scale_bytes + lane * 4);
-    for (int j0 = 0; j0 < a.k; j0 += kChoices) {
+    for (choice_t j0 = 0; j0 < a.k; j0 += kChoices) {
       int p[kChoices];
       load_rows_each(a, t, j0, p);
 #pragma unroll
@@ -551,7 +548,7 @@ __global__ __launch_bounds__(kShortThreads) void combine_short_kernel(MoveArgs a
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[i] = 0.0f;
     if (a.extra) add = load_vec<DT, MODE>(static_cast<const char*>(a.extra) + t * row, e, a.hidden);
-    for (int j0 = 0; j0 < a.k; j0 += kChoices) {
+    for (choice_t j0 = 0; j0 < a.k; j0 += kChoices) {
       int p[kChoices];
       float w[kChoices];
       load_rows_each(a, t, j0, p);
@@ -593,7 +590,7 @@ __global__ __launch_bounds__(kShortThreads) void combine_bwd_short_kernel(MoveAr
   for (int64_t t = static_cast<int64_t>(blockIdx.x - pad_groups) * kTokens + threadIdx.x / LANES; t < a.tokens;
        t += static_cast<int64_t>(gridDim.x - pad_groups) * kTokens) {
     const u32x4 d = load_vec<DT, MODE>(static_cast<const char*>(a.extra) + t * row, e, a.hidden);
-    for (int j0 = 0; j0 < a.k; j0 += kChoices) {
+    for (choice_t j0 = 0; j0 < a.k; j0 += kChoices) {
       int p[kChoices];
       float w[kChoices];
       load_rows_each(a, t, j0, p);

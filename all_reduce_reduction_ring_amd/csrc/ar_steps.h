@@ -1,6 +1,6 @@
-// ar_steps.h -- sizes and byte offsets of the row copies, plain functions that the host layer, the kernels and the CPU
-// tests share. A row has less than 2^31 bytes; the loops over it step past its end by up to a step, which 32 bits hold
-// without a sign only.
+// ar_steps.h -- sizes and byte offsets of the row copies and the steps over a token's choices: plain functions and types
+// that the host layer, the kernels and the CPU tests share. A row has less than 2^31 bytes; the loops over it step past
+// its end by up to a step, which 32 bits hold without a sign only.
 #pragma once
 
 #include <cstdint>
@@ -19,5 +19,9 @@ constexpr row_bytes_t row_scale_bytes(row_bytes_t hidden, row_bytes_t block) { r
 constexpr row_bytes_t vector_place(row_bytes_t b, row_bytes_t row_bytes) {
   return b + kVectorBytes <= row_bytes ? b : row_bytes - kVectorBytes;
 }
+
+// A token has up to 2^31 - 1 choices; the loops over them step past the last by up to 8 as well.
+using choice_t = uint32_t;
+constexpr int kChoices = 8;  // choices of a token handled together
 
 }  // namespace ar

@@ -1,4 +1,4 @@
-"""The sizes and byte offsets of the row copies (csrc/ar_steps.h), walked on the host: no sum wraps for any row that the
+"""The sizes and byte offsets of the row copies and the steps over choices (csrc/ar_steps.h), walked on the host: no sum wraps for any row that the
 entry points take, and a type with a sign in their place does not hold them."""
 import os
 import re
@@ -12,11 +12,19 @@ ROWS = [2 ** 31 - d for d in (1, 2, 4, 15, 16, 17, 127, 2048, 8176, 8191, 8192, 
     16, 17, 511, 513, 2047, 2048, 2049, 8192, 8193, 1 << 20]
 
 
-def _build(tmp_path, include):
-    exe = str(tmp_path / "row_steps")
-    subprocess.run(["g++", "-std=c++17", "-O2", "-fwrapv", "-w", "-I", str(include), os.path.join(ROOT, "tests", "c", "row_steps.cpp"),
+def _build(tmp_path, include, name="row_steps"):
+    exe = str(tmp_path / name)
+    subprocess.run(["g++", "-std=c++17", "-O2", "-fwrapv", "-w", "-I", str(include), os.path.join(ROOT, "tests", "c", name + ".cpp"),
                     "-o", exe], check=True, capture_output=True, text=True)
     return exe
+
+
+def _signed(tmp_path, name):
+    header = open(os.path.join(CSRC, "ar_steps.h")).read()
+    signed, n = re.subn(rf"using {name} = uint32_t;", f"using {name} = int32_t;", header)
+    assert n == 1
+    (tmp_path / "ar_steps.h").write_text(signed)
+    return tmp_path
 
 
 def test_every_row_size(tmp_path):
@@ -27,9 +35,17 @@ def test_every_row_size(tmp_path):
 @pytest.mark.parametrize("row", [2 ** 31 - 1, 2 ** 31 - 8191])
 def test_a_sign_shows(tmp_path, row):
     """The walk itself: with signed offsets it does not end in the row."""
-    header = open(os.path.join(CSRC, "ar_steps.h")).read()
-    signed, n = re.subn(r"using row_bytes_t = uint32_t;", "using row_bytes_t = int32_t;", header)
-    assert n == 1
-    (tmp_path / "ar_steps.h").write_text(signed)
-    r = subprocess.run([_build(tmp_path, tmp_path), str(row)], capture_output=True, text=True, timeout=120)
+    r = subprocess.run([_build(tmp_path, _signed(tmp_path, "row_bytes_t")), str(row)], capture_output=True, text=True, timeout=120)
+    assert r.returncode != 0
+
+
+def test_every_number_of_choices(tmp_path):
+    counts = [1, 7, 8, 9, 64, 2 ** 31 - 16, *range(2 ** 31 - 9, 2 ** 31)]
+    r = subprocess.run([_build(tmp_path, CSRC, "choice_steps"), *map(str, counts)], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0, r.stdout
+
+
+def test_a_sign_shows_in_the_choices(tmp_path):
+    exe = _build(tmp_path, _signed(tmp_path, "choice_t"), "choice_steps")
+    r = subprocess.run([exe, str(2 ** 31 - 1)], capture_output=True, text=True, timeout=120)
     assert r.returncode != 0

@@ -172,10 +172,12 @@ __global__ __launch_bounds__(T) void sort_kernel(SortArgs a, int64_t tile) {
     gptr<int32_t>(a.src)[p] = -1;
   __syncthreads();
   if (a.align > 1) {  // rows of the segments that no slot takes, 16 lanes to a segment
-    constexpr int kAtOnce = T / 16;
-    for (int x = static_cast<int>(blockIdx.x) * kAtOnce + static_cast<int>(threadIdx.x) / 16; x < a.experts;
-         x += static_cast<int>(gridDim.x) * kAtOnce)
-      for (int p = part[0][x] + (lane & 15); p < part[1][x]; p += 16) gptr<int32_t>(a.src)[p] = -1;
+    constexpr int kAtOnce = T / kPadLanes;
+    for (int x = static_cast<int>(blockIdx.x) * kAtOnce + static_cast<int>(threadIdx.x) / kPadLanes; x < a.experts;
+         x += static_cast<int>(gridDim.x) * kAtOnce) {
+      const sorted_row_t end = part[1][x];
+      for (sorted_row_t p = part[0][x] + lane % kPadLanes; p < end; p += kPadLanes) gptr<int32_t>(a.src)[p] = -1;
+    }
   }
   for (int64_t q0 = w_lo; q0 < w_hi; q0 += kHeld * 64) {
     int x[kHeld];

@@ -24,4 +24,8 @@ constexpr row_bytes_t vector_place(row_bytes_t b, row_bytes_t row_bytes) {
 using choice_t = uint32_t;
 constexpr int kChoices = 8;  // choices of a token handled together
 
+// Row numbers of the sorted rows are below 2^31; a segment's pads are walked 16 rows at a time, past its end by up to 15.
+using sorted_row_t = uint32_t;
+constexpr int kPadLanes = 16;
+
 }  // namespace ar

@@ -1,4 +1,4 @@
-"""The sizes and byte offsets of the row copies and the steps over choices (csrc/ar_steps.h), walked on the host: no sum wraps for any row that the
+"""The sizes and byte offsets of the row copies and the steps over choices and pad rows (csrc/ar_steps.h), walked on the host: no sum wraps for any row that the
 entry points take, and a type with a sign in their place does not hold them."""
 import os
 import re
@@ -47,5 +47,19 @@ def test_every_number_of_choices(tmp_path):
 
 def test_a_sign_shows_in_the_choices(tmp_path):
     exe = _build(tmp_path, _signed(tmp_path, "choice_t"), "choice_steps")
+    r = subprocess.run([exe, str(2 ** 31 - 1)], capture_output=True, text=True, timeout=120)
+    assert r.returncode != 0
+
+
+ENDS = [16, 17, 2 ** 20, 2 ** 31 - 17, *range(2 ** 31 - 16, 2 ** 31)]
+
+
+def test_pads_up_to_every_end(tmp_path):
+    r = subprocess.run([_build(tmp_path, CSRC, "pad_steps"), *map(str, ENDS)], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0, r.stdout
+
+
+def test_a_sign_shows_in_the_pads(tmp_path):
+    exe = _build(tmp_path, _signed(tmp_path, "sorted_row_t"), "pad_steps")
     r = subprocess.run([exe, str(2 ** 31 - 1)], capture_output=True, text=True, timeout=120)
     assert r.returncode != 0

@@ -53,3 +53,19 @@ def test_combine_and_its_gradient(dt):
     ar.ar_expert_combine_bwd(y[None], y.clone()[None], pos, w, None, None, out.view(dt)[None], dw)
     torch.cuda.synchronize()
     assert _untouched(base, n) and torch.equal(out.view(dt), y * 0.5)
+
+
+def test_sort_up_to_the_last_row():
+    """One segment of 2^31 - 1 rows, all but one of them pads."""
+    align = 2 ** 31 - 1
+    rows = ar.ar_expert_rows(1, 1, 1, align)
+    assert rows == align
+    i32 = torch.int32
+    base = torch.full((rows + 2 * GUARD,), 77, dtype=i32, device=DEV)
+    src = base[GUARD:GUARD + rows]
+    off, cnt, pos = torch.empty(2, dtype=i32, device=DEV), torch.empty(1, dtype=i32, device=DEV), torch.empty(1, 1, dtype=i32, device=DEV)
+    ar.ar_expert_sort(torch.zeros(1, 1, dtype=i32, device=DEV), off, cnt, pos, src, align)
+    torch.cuda.synchronize()
+    assert off.tolist() == [0, rows] and cnt.tolist() == [1] and pos.tolist() == [[0]]
+    assert src[0].item() == 0 and bool((src[1:] == -1).all())
+    assert bool((base[:GUARD] == 77).all()) and bool((base[GUARD + rows:] == 77).all())

@@ -745,7 +745,9 @@ int ar_expert_dispatch(const void* x, const float* x_scales, const int32_t* pos,
   size_t most = 0, xe = 0, xb = 0, ye = 0, yb = 0;
   if (!rows_fit(tokens, k, nexperts, 1, &most) || hidden == 0 || rows > INT32_MAX) return done(AR_ERR_INVALID);
   if (elem_size != 1 && elem_size != 2 && elem_size != 4) return done(AR_ERR_INVALID);
-  if ((x_scales == nullptr) != (xs_scales == nullptr) || (x_scales && elem_size != 1)) return done(AR_ERR_INVALID);
+  // without tokens, or without rows, one of the two is empty and has no address
+  if (tokens > 0 && rows > 0 && (x_scales == nullptr) != (xs_scales == nullptr)) return done(AR_ERR_INVALID);
+  if ((x_scales || xs_scales) && elem_size != 1) return done(AR_ERR_INVALID);
   if ((offsets == nullptr) != (counts == nullptr)) return done(AR_ERR_INVALID);
   const size_t es = static_cast<size_t>(elem_size), nb = blocks_of(hidden) * 4;
   if (!mul(tokens, hidden, &xe) || !mul(xe, es, &xb) || !mul(rows, hidden, &ye) || !mul(ye, es, &yb))

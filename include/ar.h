@@ -373,7 +373,8 @@ int ar_expert_sort(const int32_t* ids, size_t tokens, int k, int nexperts, int a
 /* Rows into the experts' order: xs[pos[t][j]] = x[t]. The pad rows inside the segments are zeroed (offsets and counts
  * as ar_expert_sort wrote them; both NULL where there are none). Rows from offsets[nexperts] on are not written.
  *   x: [tokens][hidden] of elem_size bytes each (4, 2, or 1 for 8-bit rows).       xs: [rows][hidden].
- *   x_scales, xs_scales: the scales of 8-bit rows, moved along with them; both or neither NULL, elem_size 1 only.
+ *   x_scales, xs_scales: the scales of 8-bit rows, moved along with them; both or neither NULL (either may be while
+ *     tokens or rows is 0), elem_size 1 only.
  *   pos: int32[tokens][k]; an entry outside [0, rows) is a slot without a row. Two slots never share a row.
  * Errors: AR_ERR_INVALID (NULL, alignment, sizes), AR_ERR_UNSUPPORTED (a row of 2^31 bytes or more), AR_ERR_ALIAS (any
  * overlap), AR_ERR_HIP. tokens == 0 enqueues nothing. */

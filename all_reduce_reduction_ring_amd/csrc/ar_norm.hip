@@ -650,7 +650,7 @@ int64_t groups_of(int64_t rows, const Shape& sh, int n) {
   int64_t most = (n >= 6 ? 2048 : 4096) / (teams * sh.threads / 64) / 256 * 256;
   if (most < 256) most = 256;
   if (most > 1024) most = 1024;
-  const int64_t all = (rows + teams - 1) / teams;
+  const int64_t all = rows / teams + (rows % teams != 0);  // rows may be as many as the type holds
   return all < most ? all : most;
 }
 

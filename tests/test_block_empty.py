@@ -39,3 +39,13 @@ def test_tensors():
                           x_scales=new(3, 2, dt=f32), xs_scales=new(0, 2, dt=f32))
     torch.cuda.synchronize()
     assert bool((xs == 3).all()) and bool((xsc == 3).all())
+
+
+def test_workspace_of_the_most_rows():
+    """The gradient's workspace stops growing: no more for the most rows that a call can name than for many."""
+    for hidden in (1, 100, 256, 4096, 16384, 32768):
+        many = ar.ar_allreduce_rmsnorm_bwd_workspace_size(1 << 40, hidden)
+        for rows in (2 ** 63 - 1, 2 ** 63 - 2, 2 ** 63 - 40, 2 ** 62):
+            assert ar.ar_allreduce_rmsnorm_bwd_workspace_size(rows, hidden) == many
+        with pytest.raises(ar.ArError):
+            ar.ar_allreduce_rmsnorm_bwd_workspace_size(2 ** 63, hidden)

@@ -146,6 +146,8 @@ def _stream(stream, device=None):
             return ctypes.c_void_p(raw(device.index))
         return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
     if isinstance(stream, int):
+        if not 0 <= stream < 2 ** 64 - 1:  # ctypes would cut it to 64 bits: to another stream, or the null stream
+            raise ValueError("stream must be a torch stream or a raw handle")
         return ctypes.c_void_p(stream)
     return ctypes.c_void_p(stream.cuda_stream)
 

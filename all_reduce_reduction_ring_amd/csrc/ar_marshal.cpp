@@ -79,19 +79,23 @@ struct Call {
     PyObject* cur = PyObject_CallNoArgs(g_current_device);
     const long now = cur ? PyLong_AsLong(cur) : -1;
     Py_XDECREF(cur);
-    if (now != device) throw Misfit();
-    if (o != Py_None) {
-      if (!PyLong_Check(o)) throw Misfit();
-      return PyLong_AsVoidPtr(o);
-    }
+    if (now != device || PyErr_Occurred()) throw Misfit();
+    if (o != Py_None) return handle_of(o);
     PyObject* index = PyLong_FromLong(device);
     PyObject* handle = index ? PyObject_CallOneArg(g_current_stream, index) : nullptr;
     Py_XDECREF(index);
-    if (!handle) throw Misfit();
-    void* s = PyLong_AsVoidPtr(handle);
-    Py_DECREF(handle);
-    return s;
+    const uint64_t s = handle ? PyLong_AsUnsignedLongLong(handle) : kNoHandle;
+    Py_XDECREF(handle);
+    if (s == kNoHandle) throw Misfit();
+    return reinterpret_cast<void*>(s);
   }
+  // An int as a handle. What the conversion refuses (negative, past 64 bits) must not become the null stream.
+  static void* handle_of(PyObject* o) {
+    const uint64_t s = PyLong_Check(o) ? PyLong_AsUnsignedLongLong(o) : kNoHandle;
+    if (s == kNoHandle) throw Misfit();
+    return reinterpret_cast<void*>(s);
+  }
+  static constexpr uint64_t kNoHandle = UINT64_MAX;  // what the conversion returns with an error set
 };
 
 // A list or tuple of one tensor per rank.

@@ -512,6 +512,22 @@ def _matrix(t, what):
     return t.shape, t.dtype, t.get_device()
 
 
+def _sizes(**named):
+    """Sizes as C takes them; ctypes would cut a larger number to its low bits, and a negative one to a huge one."""
+    for what, v in named.items():
+        if not 0 <= v < 2 ** 64:
+            raise ValueError(f"{what} must be a size of 64 bits, not {v}")
+    return tuple(named.values())
+
+
+def _ints(**named):
+    """Numbers that C takes as int."""
+    for what, v in named.items():
+        if not -2 ** 31 <= v < 2 ** 31:
+            raise ValueError(f"{what} must be an int of 32 bits, not {v}")
+    return tuple(named.values())
+
+
 def _workspace_arg(ws, dev):
     if ws is None:
         return None, 0
@@ -554,7 +570,7 @@ def ar_allreduce_rmsnorm(ins, gamma, outs, residual=None, residual_out=None, rst
 
 def ar_allreduce_rmsnorm_bwd_workspace_size(rows, hidden) -> int:
     out = ctypes.c_size_t(0)
-    _check(lib().ar_allreduce_rmsnorm_bwd_workspace_size(rows, hidden, ctypes.byref(out)),
+    _check(lib().ar_allreduce_rmsnorm_bwd_workspace_size(*_sizes(rows=rows, hidden=hidden), ctypes.byref(out)),
            "ar_allreduce_rmsnorm_bwd_workspace_size")
     return out.value
 
@@ -592,13 +608,14 @@ def ar_allreduce_rmsnorm_bwd(ins, saved, gamma, rstd, outs, dgamma, saved_scales
 def ar_expert_rows(tokens, k, nexperts, align=1) -> int:
     """The most rows that tokens * k slots take when sorted (what src and the sorted rows must hold)."""
     out = ctypes.c_size_t(0)
-    _check(lib().ar_expert_rows(tokens, k, nexperts, align, ctypes.byref(out)), "ar_expert_rows")
+    _check(lib().ar_expert_rows(*_sizes(tokens=tokens), *_ints(k=k, nexperts=nexperts, align=align), ctypes.byref(out)),
+           "ar_expert_rows")
     return out.value
 
 
 def ar_expert_sort_workspace_size(tokens, k, nexperts) -> int:
     out = ctypes.c_size_t(0)
-    _check(lib().ar_expert_sort_workspace_size(tokens, k, nexperts, ctypes.byref(out)),
+    _check(lib().ar_expert_sort_workspace_size(*_sizes(tokens=tokens), *_ints(k=k, nexperts=nexperts), ctypes.byref(out)),
            "ar_expert_sort_workspace_size")
     return out.value
 
@@ -620,8 +637,9 @@ def ar_expert_sort(ids, offsets, counts, pos, src, align=1, workspace=None, stre
             _addr(pos, "pos", i32, ids.shape, dev), _addr(src, "src", i32, (rows,), dev))
     device = ids.device
     at = _addr(ids, "ids", i32, ids.shape, dev)
+    numbers = _ints(k=k, experts=experts, align=align)
     with _on(device):
-        _check(lib().ar_expert_sort(at, tokens, k, experts, align, *args, rows, *_workspace_arg(workspace, dev),
+        _check(lib().ar_expert_sort(at, tokens, *numbers, *args, rows, *_workspace_arg(workspace, dev),
                                     _stream(stream, device)), "ar_expert_sort")
 
 
@@ -656,9 +674,10 @@ def ar_expert_dispatch(x, pos, offsets, counts, xs, x_scales=None, xs_scales=Non
           _addr(pos, "pos", kinds[3], (tokens, k), dev))
     off, cnt, experts = _pads(offsets, counts, dev)
     to = (_addr(xs, "xs", (dt,), (rows, hidden), dev), _opt(xs_scales, "xs_scales", kinds[2], (rows, nb), dev))
+    numbers = _ints(k=k, experts=experts)
     device = x.device
     with _on(device):
-        _check(lib().ar_expert_dispatch(*at, off, cnt, tokens, k, experts, hidden, x.element_size(), *to, rows,
+        _check(lib().ar_expert_dispatch(*at, off, cnt, tokens, *numbers, hidden, x.element_size(), *to, rows,
                                         _stream(stream, device)), "ar_expert_dispatch")
 
 
@@ -678,7 +697,7 @@ def ar_expert_combine(ys, pos, out, weights=None, addend=None, stream=None):
     device = out.device
     to = _addr(out, "out", (dt,), shape, dev)
     with _on(device):
-        _check(lib().ar_expert_combine(*at, tokens, k, hidden, dtype_code(dt), rows, to, _stream(stream, device)),
+        _check(lib().ar_expert_combine(*at, tokens, *_ints(k=k), hidden, dtype_code(dt), rows, to, _stream(stream, device)),
                "ar_expert_combine")
 
 
@@ -699,7 +718,7 @@ def ar_expert_combine_bwd(dout, ys, pos, weights, offsets, counts, dys, dweights
     to = (_addr(dys, "dys", (dt,), (rows, hidden), dev), _addr(dweights, "dweights", kinds[2], (tokens, k), dev))
     device = dout.device
     with _on(device):
-        _check(lib().ar_expert_combine_bwd(*at, off, cnt, tokens, k, experts, hidden, dtype_code(dt), rows, *to,
+        _check(lib().ar_expert_combine_bwd(*at, off, cnt, tokens, *_ints(k=k, experts=experts), hidden, dtype_code(dt), rows, *to,
                                            _stream(stream, device)), "ar_expert_combine_bwd")
 
 

@@ -424,7 +424,9 @@ __device__ __forceinline__ void columns_dgamma(const ArgsFor<NR>& a, int block, 
 // b R + i, + groups R, + 2 groups R, ... Every thread keeps its columns' sums of dy xhat in registers over all its rows;
 // the teams' sums are joined in LDS and leave as one row of partial sums per workgroup, which dgamma_kernel adds up in
 // order. One slot a lane (S = 1): the next row is read while this one's dot product is joined and its results are
-// stored. Wider rows (S > 1) have one team and read their row when its turn comes.
+// stored; not so fp32 rows of 6 ranks and more, whose next row does not fit the registers beside this one (fp32, 6 ranks,
+// ahead against not: 5461 x 4096 252 / 235 us, 4096 x 4096 from 8 bits 182 / 166, 16,384 x 200 64 / 44, 600 x 2048
+// 24.5 / 19.4). Wider rows (S > 1) have one team and read their row when its turn comes.
 // LANES > 0: a team is LANES lanes of a wave (rows of at most LANES slots).
 // 8 x 8192 x 4096 bf16 from 8 bits 213 us (5.5 TB/s), one rank, 16,384 x 2048 47 us (5.8 TB/s); a workgroup per row without
 // reading ahead ran 231 and 55 us.
@@ -432,7 +434,7 @@ __device__ __forceinline__ void columns_dgamma(const ArgsFor<NR>& a, int block, 
 template <int DT, int S, int NR, int MODE, bool SMALL, int LANES>
 __global__ __launch_bounds__(kMaxThreads) void rmsnorm_bwd_kernel(ArgsFor<NR> a, int team_threads, int groups,
                                                                   float* dgamma) {
-  constexpr bool kAhead = S == 1 && (Traits<DT>::kSize == 2 || NR < 8);
+  constexpr bool kAhead = S == 1 && (Traits<DT>::kSize == 2 || NR < 6);
   __shared__ float lds[2][kMaxThreads / 64];
   __shared__ float join[S == 1 ? kTeamThreads * kPerLane : 1];
   // Wide rows: dgamma's sums lie in LDS (each thread its own), so that the row's values keep the registers.

@@ -1,0 +1,17 @@
+"""The norm's gradient at every rank count up to nine in fp32 and bf16, on rows of whole waves, of lanes, and wider than a
+wave's slots, with more rows than the resident workgroups take at once and fewer: the next row is read ahead at some counts
+and not at others."""
+import pytest
+
+from test_gpu_block import BF16, F32
+from test_gpu_block_paths import check_bwd
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("n", range(1, 10))
+@pytest.mark.parametrize("rows,hidden,dt,save8,in_place", [
+    (600, 2048, F32, False, False), (1500, 4096, F32, True, True), (4500, 200, F32, True, False), (2600, 120, F32, False, True),
+    (600, 2048, BF16, True, True), (300, 8200, F32, False, False)])
+def test_norm_bwd(n, rows, hidden, dt, save8, in_place):
+    check_bwd(n, rows, hidden, dt, True, save8, 0, in_place)

@@ -17,9 +17,10 @@ namespace {
 
 // ------------------------------------------------------------------------------------------ sort
 constexpr int kSortThreads = 1024;
-// Few slots and experts go to a workgroup of a quarter of the size (192 slots, 128 experts: 4.1 -> 3.2 us; 1024 slots and
-// 256 experts would lose, 5.2 -> 7.0).
-constexpr int kFewThreads = 256, kFewSlots = 512, kFewExperts = 128;
+// Few slots go to a workgroup of a quarter of the size, which has a thread for each of 256 experts. With a dispatch of short
+// rows behind it, large workgroup against small: 64 slots 5.3 / 4.5 us (8 experts), 5.6 / 4.8 (64), 6.0 / 4.9 (128), 6.0 /
+// 5.0 (256); 512 slots 6.0 / 5.3, 6.0 / 5.5, 6.3 / 5.7, 6.3 / 5.9; 1024 slots 6.1 / 5.9, 6.4 / 6.5, 6.5 / 6.7, 6.6 / 7.0.
+constexpr int kFewThreads = 256, kFewSlots = 512;
 constexpr int kMaxExperts = AR_MAX_EXPERTS;
 constexpr int kTileBatch = 8;             // histograms read together
 constexpr int kHeld = 4;  // slots a thread reads at a time; a thread's first ones stay in registers between the passes
@@ -739,7 +740,7 @@ hipError_t launch_expert_sort(const SortArgs& a, hipStream_t s) {
     SortArgs b = a;
     b.hist = nullptr;
     const int64_t tile = a.slots > 0 ? a.slots : 1;
-    if (a.slots <= kFewSlots && a.experts <= kFewExperts)
+    if (a.slots <= kFewSlots && a.experts <= kFewThreads)
       hipLaunchKernelGGL((sort_kernel<kFewThreads, kFewThreads>), dim3(1), dim3(kFewThreads), 0, s, b, tile);
     else
       hipLaunchKernelGGL((sort_kernel<kSortThreads, kMaxExperts>), dim3(1), block, 0, s, b, tile);

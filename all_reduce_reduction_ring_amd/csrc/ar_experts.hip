@@ -265,8 +265,10 @@ __global__ __launch_bounds__(kCopyLanes) void dispatch_kernel(MoveArgs a, row_by
   for (int64_t t = blockIdx.x - pad_groups; t < a.tokens; t += gridDim.x - pad_groups) {
     const char* from = static_cast<const char*>(a.x) + t * row_bytes;
     int p[kChoices];
-    // Small calls read the row while the positions are on their way (48 tokens of 4096 bytes with the sort: 7.0 -> 6.0 us).
-    // Large ones are faster the other way round (16,384 x 8 rows of 8 KiB with the sort: 234 against 252 us).
+    // Calls that stream read the positions before the row, all others the row first, while the positions are on their way.
+    // With the sort, row first against positions first: 48 tokens, 4 choices of 4 KiB 6.1 / 6.2 us; 1536 x 8 of 8 KiB 30.2 /
+    // 31.4; 16,384 x 8 of 8194 bytes 301 / 314; streaming, 16,384 x 8 of 8 KiB, 251 / 237. Few tokens of wide rows lose by
+    // it: 48 tokens, 4 choices of 8 KiB 7.0 / 6.6; 10 choices of 16 KiB, whose positions are read in every step, 13.1 / 11.2.
     auto put = [&](const u32x4 (&v)[U], const uint32_t (&at)[U], row_bytes_t b0) {
 #pragma unroll
       for (int j = 0; j < kChoices; ++j) {

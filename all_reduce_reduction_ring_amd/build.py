@@ -12,6 +12,7 @@ import os
 import shutil
 import subprocess
 import sys
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -25,6 +26,7 @@ CEILING_LIB = os.path.join(HERE, "libar_ceiling.so")
 # the argument checks of the block-boundary entry points for torch tensors (host code, a CPython module)
 MARSHAL_SRC = "ar_marshal.cpp"
 MARSHAL_LIB = os.path.join(HERE, "_marshal.so")
+CXX = "g++"
 ARCH = "gfx950"
 
 SOURCES = ["ar_api.hip", "ar_collapsed.hip", "ar_stepwise.hip", "ar_bucket.hip", "ar_fp8.hip", "ar_tensors.hip",
@@ -81,21 +83,22 @@ def _build_marshal() -> None:
 
     home = os.path.dirname(torch.__file__)
     tmp = MARSHAL_LIB + ".tmp"
-    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+    cmd = [CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", "-I", os.path.join(ROOT, "include"),
            "-isystem", os.path.join(home, "include"), "-isystem", sysconfig.get_paths()["include"],
            os.path.join(CSRC, MARSHAL_SRC), "-o", tmp, "-L", os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cpu",
            "-lc10"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"g++ failed for {MARSHAL_SRC}:\n{r.stdout}\n{r.stderr}")
+        raise RuntimeError(f"{CXX} failed for {MARSHAL_SRC}:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, MARSHAL_LIB)
 
 
 def build(jobs: int | None = None) -> str:
-    """Compile every source and link libar.so (and libar_ceiling.so and _marshal.so); returns libar's path."""
+    """Compile every source and link libar.so (and libar_ceiling.so); returns libar's path. _marshal.so needs a host
+    compiler and the headers of Python and torch besides, and the binding does without it: where it cannot be built, a
+    warning says so, and an older one is taken away."""
     os.makedirs(BUILD, exist_ok=True)
-    _build_marshal()
     units = UNITS + [(CEILING_SRC, [])]
     jobs = jobs or min(len(units), max(1, (os.cpu_count() or 4)))
     # the slowest units first, so they are not left running alone at the end
@@ -105,6 +108,12 @@ def build(jobs: int | None = None) -> str:
     ceiling = objs.pop(CEILING_SRC)
     _link(list(objs.values()), LIB)
     _link([ceiling], CEILING_LIB)
+    try:
+        _build_marshal()
+    except (RuntimeError, OSError, ImportError) as e:
+        if os.path.exists(MARSHAL_LIB):
+            os.remove(MARSHAL_LIB)
+        warnings.warn(f"_marshal.so was not built, arguments will be checked in Python, slower: {e}")
     return LIB
 
 

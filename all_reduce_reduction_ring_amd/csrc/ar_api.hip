@@ -775,7 +775,7 @@ int ar_expert_dispatch(const void* x, const float* x_scales, const int32_t* pos,
   a.tokens = static_cast<int64_t>(tokens);
   a.rows = static_cast<int64_t>(rows);
   a.hidden = static_cast<int>(hidden);
-  a.k = static_cast<ar::choice_t>(k);
+  a.k = k;
   a.experts = nexperts;
   const hipError_t e = ar::launch_expert_dispatch(a, elem_size, static_cast<hipStream_t>(stream));
   return done(e == hipSuccess ? AR_OK : AR_ERR_HIP);
@@ -811,7 +811,7 @@ int ar_expert_combine(const void* ys, const int32_t* pos, const float* weights, 
   a.tokens = static_cast<int64_t>(tokens);
   a.rows = static_cast<int64_t>(rows);
   a.hidden = static_cast<int>(hidden);
-  a.k = static_cast<ar::choice_t>(k);
+  a.k = k;
   const hipError_t e = ar::launch_expert_combine(a, dtype, static_cast<hipStream_t>(stream));
   return done(e == hipSuccess ? AR_OK : AR_ERR_HIP);
 }
@@ -853,7 +853,7 @@ int ar_expert_combine_bwd(const void* dout, const void* ys, const int32_t* pos, 
   a.tokens = static_cast<int64_t>(tokens);
   a.rows = static_cast<int64_t>(rows);
   a.hidden = static_cast<int>(hidden);
-  a.k = static_cast<ar::choice_t>(k);
+  a.k = k;
   a.experts = nexperts;
   const hipError_t e = ar::launch_expert_combine_bwd(a, dtype, static_cast<hipStream_t>(stream));
   return done(e == hipSuccess ? AR_OK : AR_ERR_HIP);

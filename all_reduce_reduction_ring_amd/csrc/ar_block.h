@@ -71,7 +71,7 @@ struct MoveArgs {
   int64_t tokens;
   int64_t rows;
   int hidden;              // rows are below 2^31 bytes
-  choice_t k;
+  int k;
   int experts;
 };
 hipError_t launch_expert_dispatch(const MoveArgs& a, int esize, hipStream_t s);

@@ -205,7 +205,7 @@ __global__ __launch_bounds__(T) void sort_kernel(SortArgs a, int64_t tile) {
 // A workgroup of LANES threads (64, 128 or 256) takes a token. What it knows about the token's rows is kept in scalar
 // registers: the rows' addresses and the tests whether they are there.
 // The rows of choices j0 .. j0 + 7 of token t (-1: none); in scalar registers. One load for all of them.
-__device__ __forceinline__ void load_rows(const MoveArgs& a, int64_t t, choice_t j0, int (&p)[kChoices]) {
+__device__ __forceinline__ void load_rows(const MoveArgs& a, int64_t t, int j0, int (&p)[kChoices]) {
   const int lane = threadIdx.x & 63;
   int v = -1;
   if (lane < kChoices && j0 + lane < a.k) v = gptr<int32_t>(a.pos + t * a.k)[j0 + lane];
@@ -214,7 +214,7 @@ __device__ __forceinline__ void load_rows(const MoveArgs& a, int64_t t, choice_t
   for (int j = 0; j < kChoices; ++j) p[j] = __builtin_amdgcn_readlane(v, j);
 }
 // Their weights, 0 where there is no row.
-__device__ __forceinline__ void load_weights(const MoveArgs& a, int64_t t, choice_t j0, const int (&p)[kChoices],
+__device__ __forceinline__ void load_weights(const MoveArgs& a, int64_t t, int j0, const int (&p)[kChoices],
                                              float (&w)[kChoices]) {
   const int lane = threadIdx.x & 63;
   float v = 1.0f;
@@ -290,7 +290,8 @@ __global__ __launch_bounds__(kCopyLanes) void dispatch_kernel(MoveArgs a, row_by
     uint32_t at[U];
     if (row_bytes >= kVectorBytes) {
       if constexpr (MODE == kStream) {
-        for (choice_t j0 = 0; j0 < a.k; j0 += kChoices) {
+        for (int left = a.k; left > 0; left -= kChoices) {
+          const int j0 = a.k - left;
           load_rows(a, t, j0, p);
           for (row_bytes_t b0 = lane * 16; b0 < row_bytes; b0 += LANES * U * 16) {
             get(v, at, b0);
@@ -300,14 +301,16 @@ __global__ __launch_bounds__(kCopyLanes) void dispatch_kernel(MoveArgs a, row_by
       } else {
         for (row_bytes_t b0 = 0; b0 < row_bytes; b0 += LANES * U * 16) {
           get(v, at, b0 + lane * 16);
-          for (choice_t j0 = 0; j0 < a.k; j0 += kChoices) {
+          for (int left = a.k; left > 0; left -= kChoices) {
+            const int j0 = a.k - left;
             if (b0 == 0 || a.k > kChoices) load_rows(a, t, j0, p);
             put(v, at, b0 + lane * 16);
           }
         }
       }
     }
-    for (choice_t j0 = 0; j0 < a.k; j0 += kChoices) {
+    for (int left = a.k; left > 0; left -= kChoices) {
+      const int j0 = a.k - left;
       if (row_bytes < kVectorBytes || a.k > kChoices) load_rows(a, t, j0, p);
       if (row_bytes < kVectorBytes && lane < row_bytes) {
         const uint8_t v = gptr<uint8_t>(from)[lane];
@@ -356,7 +359,8 @@ __global__ __launch_bounds__(LANES) void combine_kernel(MoveArgs a) {
           add[u] = load_vec<DT, MODE>(static_cast<const char*>(a.extra) + t * row, b0 + u * LANES * V + lane_elem<DT>(),
                                        a.hidden);
       }
-      for (choice_t j0 = 0; j0 < a.k; j0 += kChoices) {
+      for (int left = a.k; left > 0; left -= kChoices) {
+        const int j0 = a.k - left;
         if (a.k > kChoices) {
           load_rows(a, t, j0, p);
           load_weights(a, t, j0, p, w);
@@ -415,7 +419,8 @@ __global__ __launch_bounds__(LANES) void combine_bwd_kernel(MoveArgs a, int pad_
   }
   int flip = 0;
   for (int64_t t = blockIdx.x - pad_groups; t < a.tokens; t += gridDim.x - pad_groups) {
-    for (choice_t j0 = 0; j0 < a.k; j0 += kChoices, flip ^= 1) {
+    for (int left = a.k; left > 0; left -= kChoices, flip ^= 1) {
+      const int j0 = a.k - left;
       u32x4 d[U];
       auto load_grad = [&](int b0) {
 #pragma unroll
@@ -474,7 +479,7 @@ __global__ __launch_bounds__(LANES) void combine_bwd_kernel(MoveArgs a, int pad_
           for (int j = 0; j < kChoices; ++j) lds[flip][threadIdx.x >> 6][j] = dot[j];
         }
         __syncthreads();  // one buffer is read while the next step fills the other
-        if (threadIdx.x < kChoices && j0 + threadIdx.x < a.k) {
+        if (threadIdx.x < kChoices && j0 + static_cast<int>(threadIdx.x) < a.k) {
           float sum = 0.0f;
 #pragma unroll
           for (int u = 0; u < kWaves; ++u) sum += lds[flip][u][threadIdx.x];
@@ -504,7 +509,7 @@ int64_t sort_tile(int64_t slots) {
 constexpr int kShortThreads = 256;
 
 // The rows of choices j0 .. j0 + 7 of token t (-1: none), one register each.
-__device__ __forceinline__ void load_rows_each(const MoveArgs& a, int64_t t, choice_t j0, int (&p)[kChoices]) {
+__device__ __forceinline__ void load_rows_each(const MoveArgs& a, int64_t t, int j0, int (&p)[kChoices]) {
 #pragma unroll
   for (int j = 0; j < kChoices; ++j) p[j] = j0 + j < a.k ? gptr<int32_t>(a.pos + t * a.k)[j0 + j] : -1;
 #pragma unroll
@@ -527,7 +532,8 @@ __global__ __launch_bounds__(kShortThreads) void dispatch_short_kernel(MoveArgs 
     const u32x4 v = ldu16(static_cast<const char*>(a.x) + t * row_bytes + at);
     uint32_t sc = 0;
     if (lane * 4 < scale_bytes) sc = *gptr<uint32_t>(static_cast<const char*>(a.x_scales) + t * scale_bytes + lane * 4);
-    for (choice_t j0 = 0; j0 < a.k; j0 += kChoices) {
+    for (int left = a.k; left > 0; left -= kChoices) {
+      const int j0 = a.k - left;
       int p[kChoices];
       load_rows_each(a, t, j0, p);
 #pragma unroll
@@ -553,7 +559,8 @@ __global__ __launch_bounds__(kShortThreads) void combine_short_kernel(MoveArgs a
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[i] = 0.0f;
     if (a.extra) add = load_vec<DT, MODE>(static_cast<const char*>(a.extra) + t * row, e, a.hidden);
-    for (choice_t j0 = 0; j0 < a.k; j0 += kChoices) {
+    for (int left = a.k; left > 0; left -= kChoices) {
+      const int j0 = a.k - left;
       int p[kChoices];
       float w[kChoices];
       load_rows_each(a, t, j0, p);
@@ -595,7 +602,8 @@ __global__ __launch_bounds__(kShortThreads) void combine_bwd_short_kernel(MoveAr
   for (int64_t t = static_cast<int64_t>(blockIdx.x - pad_groups) * kTokens + threadIdx.x / LANES; t < a.tokens;
        t += static_cast<int64_t>(gridDim.x - pad_groups) * kTokens) {
     const u32x4 d = load_vec<DT, MODE>(static_cast<const char*>(a.extra) + t * row, e, a.hidden);
-    for (choice_t j0 = 0; j0 < a.k; j0 += kChoices) {
+    for (int left = a.k; left > 0; left -= kChoices) {
+      const int j0 = a.k - left;
       int p[kChoices];
       float w[kChoices];
       load_rows_each(a, t, j0, p);
@@ -688,7 +696,7 @@ template <int DT> hipError_t combine_dt(const MoveArgs& a, hipStream_t s) {
   if (exact) return combine_run<DT, 64, 1, kExact>(a, s);
   const int64_t row = static_cast<int64_t>(a.hidden) * Traits<DT>::kSize;
   const int lanes = lanes_for((a.hidden + V - 1) / V, a.tokens);
-  return streams(a.tokens * row * (a.k + 2), row) ? combine_lanes<DT, kStream>(a, lanes, s)
+  return streams(a.tokens * row * (int64_t(a.k) + 2), row) ? combine_lanes<DT, kStream>(a, lanes, s)
                                                   : combine_lanes<DT, kCached>(a, lanes, s);
 }
 
@@ -724,7 +732,7 @@ template <int DT> hipError_t combine_bwd_dt(const MoveArgs& a, hipStream_t s) {
   const int lanes = lanes_for((a.hidden + V - 1) / V, a.tokens);
   // in place with the same lanes, so that dweights has the same bits
   if (exact) return combine_bwd_lanes<DT, 1, kExact>(a, lanes, s);
-  return streams(a.tokens * row * (2 * a.k + 1), row) ? combine_bwd_lanes<DT, kUnroll, kStream>(a, lanes, s)
+  return streams(a.tokens * row * (2 * int64_t(a.k) + 1), row) ? combine_bwd_lanes<DT, kUnroll, kStream>(a, lanes, s)
                                                       : combine_bwd_lanes<DT, kUnroll, kCached>(a, lanes, s);
 }
 
@@ -772,7 +780,7 @@ hipError_t launch_expert_dispatch(const MoveArgs& a, int esize, hipStream_t s) {
     return hipGetLastError();
   }
   const dim3 grid(static_cast<unsigned>(groups_for(a.tokens) + pads)), block(kCopyLanes);
-  if (streams(a.tokens * row * static_cast<int64_t>(a.k + 1), row))
+  if (streams(a.tokens * row * (int64_t(a.k) + 1), row))
     hipLaunchKernelGGL(dispatch_kernel<kStream>, grid, block, 0, s, a, row, scale, pads, parts);
   else
     hipLaunchKernelGGL(dispatch_kernel<kCached>, grid, block, 0, s, a, row, scale, pads, parts);

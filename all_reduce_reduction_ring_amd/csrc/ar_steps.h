@@ -20,9 +20,10 @@ constexpr row_bytes_t vector_place(row_bytes_t b, row_bytes_t row_bytes) {
   return b + kVectorBytes <= row_bytes ? b : row_bytes - kVectorBytes;
 }
 
-// A token has up to 2^31 - 1 choices; the loops over them step past the last by up to 8 as well.
-using choice_t = uint32_t;
-constexpr int kChoices = 8;  // choices of a token handled together
+// Choices of a token handled together. A token has up to 2^31 - 1; the loops count down those that are left, which ends at
+// -7 and no sum wraps. (Counted up without a sign, the combine kernel went from 113 to 179 registers and from 226 to 244 us
+// at 16,384 x 8 rows of 8 KiB.)
+constexpr int kChoices = 8;
 
 // Row numbers of the sorted rows are below 2^31; a segment's pads are walked 16 rows at a time, past its end by up to 15.
 using sorted_row_t = uint32_t;

@@ -12,9 +12,9 @@ ROWS = [2 ** 31 - d for d in (1, 2, 4, 15, 16, 17, 127, 2048, 8176, 8191, 8192, 
     16, 17, 511, 513, 2047, 2048, 2049, 8192, 8193, 1 << 20]
 
 
-def _build(tmp_path, include, name="row_steps"):
+def _build(tmp_path, include, name="row_steps", *flags):
     exe = str(tmp_path / name)
-    subprocess.run(["g++", "-std=c++17", "-O2", "-fwrapv", "-w", "-I", str(include), os.path.join(ROOT, "tests", "c", name + ".cpp"),
+    subprocess.run(["g++", "-std=c++17", "-O2", "-fwrapv", "-w", *flags, "-I", str(include), os.path.join(ROOT, "tests", "c", name + ".cpp"),
                     "-o", exe], check=True, capture_output=True, text=True)
     return exe
 
@@ -45,8 +45,9 @@ def test_every_number_of_choices(tmp_path):
     assert r.returncode == 0, r.stdout
 
 
-def test_a_sign_shows_in_the_choices(tmp_path):
-    exe = _build(tmp_path, _signed(tmp_path, "choice_t"), "choice_steps")
+def test_counting_up_shows_in_the_choices(tmp_path):
+    exe = _build(tmp_path, CSRC, "choice_steps", "-DCOUNT_UP")
+    assert subprocess.run([exe, str(2 ** 31 - 8)], capture_output=True, text=True, timeout=120).returncode == 0
     r = subprocess.run([exe, str(2 ** 31 - 1)], capture_output=True, text=True, timeout=120)
     assert r.returncode != 0
 

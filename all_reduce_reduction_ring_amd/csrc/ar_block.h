@@ -87,9 +87,8 @@ hipError_t launch_expert_combine_bwd(const MoveArgs& a, int dtype, hipStream_t s
 inline bool streams(int64_t bytes, int64_t row_bytes) { return bytes >= (int64_t(128) << 20) && row_bytes % 128 == 0; }
 
 // ------------------------------------------------------------------------------------------ device helpers
-// How a kernel reads and writes rows. kStream: non-temporal loads and stores, for calls whose rows are whole cache lines
-// and together far larger than the caches. kCached: default policy. kExact: default policy, and the vector that a row's
-// end cuts is read element by element in its own place.
+// How a kernel reads and writes rows. kStream: non-temporal loads and stores, for the calls that streams() names. kCached:
+// default policy. kExact: default policy, and the vector that a row's end cuts is read element by element in its own place.
 constexpr int kCached = 0, kStream = 1, kExact = 2;
 
 // 16-, 8- and 4-byte accesses at any byte address: rows of odd widths start anywhere. The unaligned type leaves one

@@ -72,7 +72,7 @@ __device__ __forceinline__ BlockScale scale_for(float amax) {
   const bool unit = !(amax > 0.0f) || __builtin_isinf(inv);
   return BlockScale{unit ? 1.0f : inv, unit ? 1.0f : scale};
 }
-// Block scale. All 64 lanes of the wave must call it (DPP).
+// Block scale. The 16 lanes that hold the block must all call it (DPP).
 __device__ __forceinline__ BlockScale block_scale(const float (&v)[kPerLane]) {
   return scale_for(row16_max(lane_amax<kPerLane>(v)));
 }

@@ -648,7 +648,7 @@ constexpr int kUnroll = 2;  // vectors of a row a lane takes at a time
 
 // Lanes per token: as many as have two vectors each, up to 256 (65,536 x 4 rows of 2 KiB, combine: 64 lanes 114 us, 128
 // 127, 256 185); with few tokens, where waves are short, twice as many (777 x 3 rows of 1025 fp32: 64 lanes 5.2 us, 256
-// 4.1).
+// 4.1). The gradient's dot products are added lane by lane, so their bits go by this too.
 int lanes_for(int64_t vectors, int64_t tokens) {
   if (tokens < 2048) vectors *= 2;
   return vectors > 256 ? 256 : vectors > 128 ? 128 : 64;
@@ -693,6 +693,8 @@ template <int DT> hipError_t combine_dt(const MoveArgs& a, hipStream_t s) {
     case 16: return combine_short<DT, 16>(a, exact, s);
     case 32: return combine_short<DT, 32>(a, exact, s);
   }
+  // In place at widths that a vector does not divide, one wave a token, against apart from the addend: 16,384 x 8 rows of
+  // 4097 bf16 291 / 270 us, 16,384 x 4 of 1001 fp32 90 / 79, 1000 x 4 of 4097 bf16 21.8 / 12.3, 48 x 4 of 1025 bf16 6.1 / 3.2.
   if (exact) return combine_run<DT, 64, 1, kExact>(a, s);
   const int64_t row = static_cast<int64_t>(a.hidden) * Traits<DT>::kSize;
   const int lanes = lanes_for((a.hidden + V - 1) / V, a.tokens);

@@ -390,7 +390,8 @@ int ar_expert_combine(const void* ys, const int32_t* pos, const float* weights, 
                       int k, size_t hidden, int dtype, size_t rows, void* out, void* stream);
 
 /* The gradient of ar_expert_combine: dys[pos[t][j]] = weights[t][j] * dout[t], pad rows zeroed as ar_expert_dispatch
- * does it; dweights[t][j] = <dout[t], ys[pos[t][j]]> (fp32), 0 for a slot without a row. (The addend's gradient is
+ * does it; dweights[t][j] = <dout[t], ys[pos[t][j]]> (fp32, in an order fixed by hidden, dtype and tokens, so the same
+ * token's sum may end in other bits in a batch of another size), 0 for a slot without a row. (The addend's gradient is
  * dout.) dys may equal ys. */
 int ar_expert_combine_bwd(const void* dout, const void* ys, const int32_t* pos, const float* weights,
                           const int32_t* offsets, const int32_t* counts, size_t tokens, int k, int nexperts,

@@ -423,11 +423,12 @@ __device__ __forceinline__ void columns_dgamma(const ArgsFor<NR>& a, int block, 
 // b R + i, + groups R, + 2 groups R, ... Every thread keeps its columns' sums of dy xhat in registers over all its rows;
 // the teams' sums are joined in LDS and leave as one row of partial sums per workgroup, which dgamma_kernel adds up in
 // order. One slot a lane (S = 1): the next row is read while this one's dot product is joined and its results are
-// stored; not so fp32 rows of 6 ranks and more, whose next row does not fit the registers beside this one (fp32, 6 ranks,
-// ahead against not: 5461 x 4096 252 / 235 us, 4096 x 4096 from 8 bits 182 / 166, 16,384 x 200 64 / 44, 600 x 2048
-// 24.5 / 19.4). Wider rows (S > 1) have one team and read their row when its turn comes.
+// stored; not so fp32 rows of 6 and 8 ranks, whose next row does not fit the registers beside this one (6 ranks, ahead
+// against not: 5461 x 4096 252 / 235 us, 4096 x 4096 from 8 bits 182 / 166, 16,384 x 200 64 / 44, 600 x 2048 24.5 / 19.4;
+// rank counts without a kernel of their own read a batch's slots ahead). Wider rows (S > 1) have one team and read their row
+// when its turn comes.
 // LANES > 0: a team is LANES lanes of a wave (rows of at most LANES slots).
-// 8 x 8192 x 4096 bf16 from 8 bits 213 us (5.5 TB/s), one rank, 16,384 x 2048 47 us (5.8 TB/s); a workgroup per row without
+// 8 x 8192 x 4096 bf16 from 8 bits 213 us (5.5 TB/s), one rank, 16,384 x 2048 48 us (5.6 TB/s); a workgroup per row without
 // reading ahead ran 231 and 55 us.
 // SMALL: no second launch; the workgroups from `groups` on each sum a block of columns instead, reading those again.
 template <int DT, int S, int NR, int MODE, bool SMALL, int LANES>

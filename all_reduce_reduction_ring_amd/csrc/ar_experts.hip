@@ -406,7 +406,8 @@ __global__ __launch_bounds__(LANES) void combine_kernel(MoveArgs a) {
 }
 
 // The waves' dot products are joined in LDS. The first pad_groups workgroups zero the pad rows. 8192 x 4 rows of 8 KiB:
-// 109 us, 5.5 TB/s.
+// 111 us, 5.5 TB/s. The token's gradient is read with the rows, behind the positions: ahead of them it was level in 2-byte
+// types and slower in fp32, by a wait in every step (16 x 4 rows of 8192 8.7 -> 11.7 us, 8192 x 8 of 1024 108 -> 122).
 template <int DT, int LANES, int U, int MODE>
 __global__ __launch_bounds__(LANES) void combine_bwd_kernel(MoveArgs a, int pad_groups, int pad_parts) {
   constexpr int V = Traits<DT>::kVec;
@@ -421,15 +422,6 @@ __global__ __launch_bounds__(LANES) void combine_bwd_kernel(MoveArgs a, int pad_
   for (int64_t t = blockIdx.x - pad_groups; t < a.tokens; t += gridDim.x - pad_groups) {
     for (int left = a.k; left > 0; left -= kChoices, flip ^= 1) {
       const int j0 = a.k - left;
-      u32x4 d[U];
-      auto load_grad = [&](int b0) {
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-          if (b0 + u * LANES * V < a.hidden)
-            d[u] = load_vec<DT, MODE>(static_cast<const char*>(a.extra) + t * row, b0 + u * LANES * V + lane_elem<DT>(),
-                                      a.hidden);
-      };
-      load_grad(wave_first<DT>());  // while the positions are on their way
       int p[kChoices];
       float w[kChoices], dot[kChoices];
       load_rows(a, t, j0, p);
@@ -437,8 +429,12 @@ __global__ __launch_bounds__(LANES) void combine_bwd_kernel(MoveArgs a, int pad_
 #pragma unroll
       for (int j = 0; j < kChoices; ++j) dot[j] = 0.0f;
       for (int b0 = wave_first<DT>(); b0 < a.hidden; b0 += LANES * V * U) {
-        u32x4 x[kChoices][U];
-        if (b0 != wave_first<DT>()) load_grad(b0);
+        u32x4 d[U], x[kChoices][U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (b0 + u * LANES * V < a.hidden)
+            d[u] = load_vec<DT, MODE>(static_cast<const char*>(a.extra) + t * row, b0 + u * LANES * V + lane_elem<DT>(),
+                                      a.hidden);
 #pragma unroll
         for (int j = 0; j < kChoices; ++j) {
           if (p[j] < 0) continue;

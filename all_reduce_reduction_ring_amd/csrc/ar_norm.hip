@@ -658,12 +658,17 @@ int64_t groups_of(int64_t rows, const Shape& sh, int n) {
 
 constexpr int64_t kMaxGrid = 1 << 21;  // a launch has fewer than 2^32 threads
 
-// Backward without partial sums, in one launch: dgamma's columns read the ranks' rows and the saved ones a second time.
-// Up to 256 rows and 24 MiB read twice (two launches against one: 1 row of 4096, 8 ranks 8.2 / 4.0 us, 128 of 1000, 2
-// ranks 6.7 / 4.6, 256 of 4096, 8 ranks 15.7 / 14.7; beyond: 512 of 1000, 2 ranks 7.8 / 9.4, 512 of 4096, 8 ranks
-// 20.6 / 29.4).
+// Backward without partial sums, in one launch: dgamma's columns read the ranks' rows and the saved ones a second time, each
+// block of columns by one workgroup, 64 rows at once. Up to 256 rows, 24 MiB read twice and kOnceReads vectors of the ranks
+// and the saved row under one another in a column. Two launches against one: 1 row of 4096 bf16, 8 ranks 8.2 / 4.0 us, 128 of
+// 1000, 2 ranks 6.7 / 4.6; 200 of 4096, 8 ranks 14.1 / 12.1; 128 of 4096 fp32, 4 ranks 11.3 / 8.5. Beyond: 512 of 1000 bf16,
+// 2 ranks 7.8 / 9.4, 256 of 200, 8 ranks 6.4 / 8.1, 200 of 1024, 16 ranks 11.4 / 14.2; fp32, 200 of 1024, 8 ranks 9.0 / 13.2,
+// 16 ranks 12.9 / 23.6, 256 of 4096, 4 ranks 15.0 / 14.1.
+constexpr int64_t kOnceReads = 2200;
 bool reads_twice(const NormArgs& a, int size) {
-  return a.hidden <= kMaxThreads * kPerLane && a.rows <= 256 && a.rows * a.hidden * size * (a.n + 1) <= (24 << 20);
+  const int64_t reads = a.rows * (a.n + 1) * (size == 2 ? 1 : 2);
+  return a.hidden <= kMaxThreads * kPerLane && a.rows <= 256 && reads <= kOnceReads &&
+         a.rows * a.hidden * size * (a.n + 1) <= (24 << 20);
 }
 bool over_inputs(const NormArgs& a) {
   for (int r = 0; r < a.n; ++r)

@@ -15,3 +15,13 @@ pytestmark = pytest.mark.gpu
     (600, 2048, BF16, True, True), (300, 8200, F32, False, False)])
 def test_norm_bwd(n, rows, hidden, dt, save8, in_place):
     check_bwd(n, rows, hidden, dt, True, save8, 0, in_place)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("n,rows,hidden,dt", [
+    (1, 256, 200, BF16), (7, 256, 520, BF16), (7, 255, 520, F32), (8, 244, 1024, BF16), (8, 245, 1024, BF16), (8, 122, 1024, F32),
+    (8, 123, 1024, F32), (16, 129, 300, BF16), (16, 130, 300, BF16), (40, 53, 4096, BF16), (64, 33, 200, BF16), (64, 34, 200, BF16),
+    (64, 16, 8192, F32), (64, 17, 8192, F32)])
+def test_one_launch_and_two(n, rows, hidden, dt, in_place):
+    """Both sides of the number of reads up to which the gradient is one launch."""
+    check_bwd(n, rows, hidden, dt, True, True, 0, in_place)

@@ -82,8 +82,10 @@ hipError_t launch_expert_combine_bwd(const MoveArgs& a, int dtype, hipStream_t s
 // last-level cache, in rows of whole lines. Default policy against streaming, three calls' data in turn, 4096 bf16 wide:
 // norm of 8 ranks, 75 MB 13.1 against 14.0 us, 151 MB 34.7 against 29.4, 8 x 8192 x 8192 with 8-bit results 370 against
 // 348; its gradient 20.3 / 19.7, 42.5 / 36.8 and (8 x 8192 x 4096) 238 / 214 us; combine 38 MB 8.9 / 7.9, 151 MB
-// 31.4 / 26.3, 1.3 GB 257 / 229 us; its gradient 71 MB 16.4 / 19.0, 143 MB 36.8 / 32.0, 600 MB 122 / 113 us. Rows that
-// share lines lose by non-temporal stores (8 x 4096 x 2050 fp32: 185 us streaming, 131 us cached).
+// 31.4 / 26.3, 1.3 GB 257 / 229 us; its gradient 71 MB 16.4 / 19.0, 143 MB 36.8 / 32.0, 600 MB 122 / 113 us. Norm of 300 x
+// 32,768 bf16, 4 and 8 ranks 51.9 / 40.7 and 83.6 / 72.0, of 1024 x 16,384 fp32, 2 ranks 79.9 / 75.9, its gradient 97.0 /
+// 87.7, of 4096 x 16,384 bf16, 8 ranks 473 / 462, its gradient 487 / 478. Rows that share lines lose by non-temporal
+// stores (8 x 4096 x 2050 fp32: 185 us streaming, 131 us cached).
 inline bool streams(int64_t bytes, int64_t row_bytes) { return bytes >= (int64_t(128) << 20) && row_bytes % 128 == 0; }
 
 // ------------------------------------------------------------------------------------------ device helpers

@@ -19,8 +19,8 @@ namespace {
 
 // A lane's slot of 8 elements is kVecs vectors: 2-byte types, elements [8 i, 8 i + 8) for slot index i. fp32, whole waves:
 // elements [512 u + 4 l, + 4) and the same + 256 for i = 64 u + l, so that every access of a wave is 1 KiB in one piece
-// (rows that share cache lines, 6 x 4993 x 3545: 201 us; in pieces of 256 bytes 224); a 128-element block lies in 32 lanes'
-// vectors. fp32, rows of 16 or 32 lanes (MODE without kWide): [128 b + 4 l, + 4) and the same + 64 for i = 16 b + l.
+// (rows that share cache lines, 6 x 4993 x 3545: 201 us; in pieces of 256 bytes 224; few rows with 8-bit results lose by the
+// longer way to a block's maximum, 8 x 16 x 4096 5.0 -> 5.7); a 128-element block lies in 32 lanes' vectors. fp32, rows of 16 or 32 lanes (MODE without kWide): [128 b + 4 l, + 4) and the same + 64 for i = 16 b + l.
 constexpr int kWide = 4;
 constexpr int policy(int mode) { return mode & 3; }
 template <int DT> constexpr int kVecs = Traits<DT>::kSize == 2 ? 1 : 2;
@@ -757,11 +757,12 @@ template <int DT> hipError_t launch(const NormArgs& a, float* dgamma, hipStream_
   if (a.hidden < Traits<DT>::kVec) return run<DT, 1, 0, kExact, 16>(a, dgamma, sh, s);
   if (sh.threads == 16) return run_n<DT, 1, kCached, 16>(a, dgamma, sh, s);
   if (sh.threads == 32) return run_n<DT, 1, kCached, 32>(a, dgamma, sh, s);
-  if (sh.slots == 1)
-    return streams(a.rows * row * (2 * a.n + 2), row) ? run_n<DT, 1, kStream | kWide, 0>(a, dgamma, sh, s)
-                                                      : run_n<DT, 1, kCached | kWide, 0>(a, dgamma, sh, s);
-  if (sh.slots == 2) return run_n<DT, 2, kCached | kWide, 0>(a, dgamma, sh, s);
-  return run_n<DT, 4, kCached | kWide, 0>(a, dgamma, sh, s);
+  const bool stream = streams(a.rows * row * (2 * a.n + 2), row);
+  switch (sh.slots) {
+    case 1: return stream ? run_n<DT, 1, kStream | kWide, 0>(a, dgamma, sh, s) : run_n<DT, 1, kCached | kWide, 0>(a, dgamma, sh, s);
+    case 2: return stream ? run_n<DT, 2, kStream | kWide, 0>(a, dgamma, sh, s) : run_n<DT, 2, kCached | kWide, 0>(a, dgamma, sh, s);
+    default: return stream ? run_n<DT, 4, kStream | kWide, 0>(a, dgamma, sh, s) : run_n<DT, 4, kCached | kWide, 0>(a, dgamma, sh, s);
+  }
 }
 
 }  // namespace

@@ -1,8 +1,12 @@
-"""Rows just below 2^31 bytes, the widest that the expert entry points take: every byte arrives, none beside them."""
+"""Wide rows: just below 2^31 bytes, the widest that the expert entry points take, where every byte arrives and none beside
+them; and the norm and its gradient above 8192 elements, streaming and not."""
 import pytest
 import torch
 
 import all_reduce_reduction_ring_amd as ar
+import block_ref as ref
+from test_gpu_block import BF16, E4M3, F16, F32, Guarded, norm_inputs
+from test_gpu_block_paths import check_bwd
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -69,3 +73,29 @@ def test_sort_up_to_the_last_row():
     assert off.tolist() == [0, rows] and cnt.tolist() == [1] and pos.tolist() == [[0]]
     assert src[0].item() == 0 and bool((src[1:] == -1).all())
     assert bool((base[:GUARD] == 77).all()) and bool((base[GUARD + rows:] == 77).all())
+
+
+@pytest.mark.parametrize("n,rows,hidden,dt,streaming", [
+    (1, 1100, 16384, BF16, True), (2, 600, 16384, F32, True), (4, 300, 32768, BF16, True), (5, 460, 12288, F16, True),
+    (8, 70, 32768, F32, True), (4, 100, 32768, BF16, False), (2, 100, 8256, F32, False)])
+def test_norm_and_its_gradient(n, rows, hidden, dt, streaming):
+    assert (rows * hidden * dt.itemsize * (2 * n + 2) >= 128 << 20) == streaming
+    ins, res, gamma = norm_inputs(n, rows, hidden, dt, True, False, 0)
+    nb, put = ref.blocks(hidden), Guarded(0)
+    h, rstd, y, dh, rel, dy = ref.norm(ins, res, gamma, 1e-4)
+    for out8 in (False, True):
+        outs = [put.new((rows, hidden), E4M3 if out8 else dt) for _ in range(n)]
+        sc = [put.new((rows, nb), F32) for _ in range(n)] if out8 else None
+        ro, rs = put.new((rows, hidden), dt), put.new((rows,), F32)
+        ar.ar_allreduce_rmsnorm(ins, gamma, outs, res, ro, rs, sc, eps=1e-4)
+        torch.cuda.synchronize()
+        put.check()
+        ref.close(ro, h, dh, "residual_out")
+        ref.close(rs[:, None], rstd, rel * rstd, "rstd")
+        for r in (0, n - 1):
+            if out8:
+                ref.close_codes(outs[r], sc[r], y, dy, f"out {r}")
+            else:
+                ref.close(outs[r], y, dy, f"out {r}")
+    for in_place in (False, True):
+        check_bwd(n, rows, hidden, dt, True, in_place, 0, in_place)

@@ -11,7 +11,8 @@ ar_allreduce_buckets, ar_allreduce_tensors, ar_reduce_scatter, ar_all_gather, ar
 ar_bucket_unpack, ar_fp8_quant, ar_fp8_dequant, ar_auto_algo, ar_chunk_bounds, ar_status_string, ar_last_call,
 ar_version; next to the reduction in a transformer layer: ar_allreduce_rmsnorm, ar_allreduce_rmsnorm_bwd,
 ar_allreduce_rmsnorm_bwd_workspace_size, ar_expert_rows, ar_expert_sort, ar_expert_sort_workspace_size,
-ar_expert_dispatch, ar_expert_combine, ar_expert_combine_bwd. Helpers: chunk_bounds, make_copy_descs,
+ar_expert_dispatch, ar_expert_combine, ar_expert_combine_bwd, and between dispatch and combine ar_expert_gated,
+ar_expert_gated_bwd, ar_expert_linear, ar_expert_linear_bwd. Helpers: chunk_bounds, make_copy_descs,
 BucketedAllReduce.
 """
 from __future__ import annotations
@@ -37,6 +38,8 @@ __all__ = [
     "AR_NORM_MAX_HIDDEN", "AR_MAX_EXPERTS", "ar_allreduce_rmsnorm", "ar_allreduce_rmsnorm_bwd",
     "ar_allreduce_rmsnorm_bwd_workspace_size", "ar_expert_rows", "ar_expert_sort", "ar_expert_sort_workspace_size",
     "ar_expert_dispatch", "ar_expert_combine", "ar_expert_combine_bwd",
+    "AR_PRODUCT_MAX_WIDTH", "AR_ACT_SILU", "AR_ACT_GELU", "AR_ACT_GELU_TANH", "ar_expert_gated", "ar_expert_gated_bwd",
+    "ar_expert_linear", "ar_expert_linear_bwd",
 ]
 
 AR_OK, AR_ERR_INVALID, AR_ERR_UNSUPPORTED, AR_ERR_ALIAS, AR_ERR_WORKSPACE, AR_ERR_HIP = 0, 1, 2, 3, 4, 5
@@ -49,6 +52,8 @@ AR_MAX_RANKS = 64
 AR_FP8_BLOCK = 128
 AR_NORM_MAX_HIDDEN = 32768
 AR_MAX_EXPERTS = 1024
+AR_PRODUCT_MAX_WIDTH = 1 << 20
+AR_ACT_SILU, AR_ACT_GELU, AR_ACT_GELU_TANH = 0, 1, 2
 AR_NOALLOC_WS_BYTES = 64 << 20
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -107,6 +112,11 @@ def lib():
         L.ar_expert_dispatch.argtypes = [vp, vp, vp, vp, vp, sz, i32, i32, sz, i32, vp, vp, sz, vp]
         L.ar_expert_combine.argtypes = [vp, vp, vp, vp, sz, i32, sz, i32, sz, vp, vp]
         L.ar_expert_combine_bwd.argtypes = [vp, vp, vp, vp, vp, vp, sz, i32, i32, sz, i32, sz, vp, vp, vp]
+        L.ar_expert_gated.argtypes = [vp, vp, vp, sz, vp, vp, i32, sz, sz, sz, i32, i32, vp, vp, vp, vp]
+        L.ar_expert_gated_bwd.argtypes = [vp, vp, vp, vp, vp, vp, sz, vp, vp, i32, sz, sz, sz, i32, i32, vp, vp, vp, vp,
+                                          vp, sz, vp]
+        L.ar_expert_linear.argtypes = [vp, vp, sz, vp, vp, i32, sz, sz, sz, i32, vp, vp]
+        L.ar_expert_linear_bwd.argtypes = [vp, vp, vp, sz, vp, vp, i32, sz, sz, sz, i32, vp, vp, sz, vp]
         L.ar_status_string.argtypes = [i32]
         L.ar_status_string.restype = ctypes.c_char_p
         L.ar_last_call.argtypes = [ctypes.POINTER(_CallRecord)]
@@ -117,7 +127,8 @@ def lib():
                      "ar_auto_algo", "ar_chunk_bounds", "ar_epilogue", "ar_allreduce_rmsnorm",
                      "ar_allreduce_rmsnorm_bwd", "ar_allreduce_rmsnorm_bwd_workspace_size", "ar_expert_rows",
                      "ar_expert_sort", "ar_expert_sort_workspace_size", "ar_expert_dispatch", "ar_expert_combine",
-                     "ar_expert_combine_bwd"):
+                     "ar_expert_combine_bwd", "ar_expert_gated", "ar_expert_gated_bwd", "ar_expert_linear",
+                     "ar_expert_linear_bwd"):
             getattr(L, name).restype = i32
         _lib = L
     return _lib
@@ -720,6 +731,149 @@ def ar_expert_combine_bwd(dout, ys, pos, weights, offsets, counts, dys, dweights
     with _on(device):
         _check(lib().ar_expert_combine_bwd(*at, off, cnt, tokens, *_ints(k=k, experts=experts), hidden, dtype_code(dt), rows, *to,
                                            _stream(stream, device)), "ar_expert_combine_bwd")
+
+
+# ------------------------------------------------------------------------------------------ experts' products
+def _segments(offsets, counts, dev):
+    """The addresses of offsets and counts (counts alone may be None; both: one segment of all rows), and the number
+    of experts (None without offsets)."""
+    if offsets is None:
+        if counts is not None:
+            raise ValueError("counts need offsets")
+        return None, None, None
+    i32, experts = _kinds()[3], offsets.numel() - 1
+    if experts < 1:
+        raise ValueError("offsets must hold one entry per expert and the end")
+    return (_addr(offsets, "offsets", i32, (experts + 1,), dev), _opt(counts, "counts", i32, (experts,), dev), experts)
+
+
+def _weights(w, what, dt, experts, out, inside, dev):
+    """The address of a weight [experts, out, inside] (without segments also [out, inside]) whose matrices are dense but
+    may lie apart, and the elements between them."""
+    if w is None:
+        return None, out * inside
+    shape = (1 if experts is None else experts, out, inside)
+    if w.dim() == 2 and experts is None:
+        w = w.unsqueeze(0)
+    if w.dtype is not dt or tuple(w.shape) != shape:
+        raise ValueError(f"{what} must be {dt} of the shape {shape}, not {w.dtype} {tuple(w.shape)}")
+    if w.get_device() != dev or dev < 0:
+        raise ValueError(f"{what} must be a GPU tensor on the device of the others")
+    if not w[0].is_contiguous():
+        raise ValueError(f"{what} must hold dense matrices")
+    return w.data_ptr(), w.stride(0) if shape[0] > 1 else out * inside
+
+
+def _pair(first, second, what):
+    """Two weights of one call lie alike: the elements between their matrices."""
+    if first[1] != second[1]:
+        raise ValueError(f"{what} must have the same distance between their matrices")
+    return first[0], second[0], first[1]
+
+
+def ar_expert_gated(xs, w_gate, w_up, out, offsets=None, counts=None, gate=None, up=None, act=AR_ACT_SILU, stream=None):
+    """out = act(xs w_gate[e]^T) * (xs w_up[e]^T) for the rows of every expert's segment (offsets, counts as
+    ar_expert_sort wrote them; both None: one matrix for all rows). xs [rows, hidden], out [rows, inner]; w_gate and w_up
+    [experts, inner, hidden] (without segments also [inner, hidden]) may be parts of one tensor, such as w[:, :inner] and
+    w[:, inner:]. gate, up [rows, inner] receive the two products for ar_expert_gated_bwd. Rows outside the segments are
+    neither read nor written."""
+    shape, dt, dev = _matrix(xs, "xs")
+    if out.dim() != 2:
+        raise ValueError("out must be a matrix [rows, inner]")
+    (rows, hidden), own = shape, (dt,)
+    wide = (rows, out.shape[1])
+    off, cnt, experts = _segments(offsets, counts, dev)
+    at = _addr(xs, "xs", own, shape, dev)
+    w = _pair(_weights(w_gate, "w_gate", dt, experts, wide[1], hidden, dev),
+              _weights(w_up, "w_up", dt, experts, wide[1], hidden, dev), "w_gate and w_up")
+    to = (_addr(out, "out", own, wide, dev), _opt(gate, "gate", own, wide, dev), _opt(up, "up", own, wide, dev))
+    numbers = _ints(experts=1 if experts is None else experts)
+    device = xs.device
+    with _on(device):
+        _check(lib().ar_expert_gated(at, *w, off, cnt, *numbers, rows, hidden, wide[1], dtype_code(dt), *_ints(act=act), *to,
+                                     _stream(stream, device)), "ar_expert_gated")
+
+
+def ar_expert_gated_bwd(dout, gate, up, xs, w_gate, w_up, dgate, dup, dxs=None, dw_gate=None, dw_up=None, offsets=None,
+                        counts=None, act=AR_ACT_SILU, stream=None):
+    """The gradient of ar_expert_gated: dout, gate and up [rows, inner] (gate and up as the forward wrote them) give dgate
+    and dup [rows, inner] (either may be dout, gate or up), and of these dxs [rows, hidden] (None: not wanted; w_gate and
+    w_up may then be None) and the weights' gradients dw_gate, dw_up [experts, inner, hidden] (None: not wanted; xs may
+    then be None), which may be parts of one tensor as the weights may."""
+    wide, dt, dev = _matrix(dout, "dout")
+    rows, inner = wide
+    known = [t for t in (xs, dxs) if t is not None]
+    if known and known[0].dim() != 2:
+        raise ValueError("xs and dxs must be matrices [rows, hidden]")
+    if not known:  # the gradients of the two products alone
+        if any(t is not None for t in (dw_gate, dw_up)):
+            raise ValueError("dw_gate and dw_up need xs")
+        w_gate = w_up = None
+    if (dw_gate is None) != (dw_up is None):
+        raise ValueError("dw_gate and dw_up go together")
+    if dw_gate is not None and xs is None:
+        raise ValueError("dw_gate and dw_up need xs")
+    if dxs is not None and (w_gate is None or w_up is None):
+        raise ValueError("dxs needs w_gate and w_up")
+    hidden = known[0].shape[1] if known else 1
+    own, narrow = (dt,), (rows, hidden)
+    off, cnt, experts = _segments(offsets, counts, dev)
+    at = (_addr(dout, "dout", own, wide, dev), _addr(gate, "gate", own, wide, dev), _addr(up, "up", own, wide, dev),
+          _opt(xs, "xs", own, narrow, dev))
+    both = lambda g, u, what: _pair(_weights(g, "w_gate", dt, experts, inner, hidden, dev),
+                                    _weights(u, "w_up", dt, experts, inner, hidden, dev), what)
+    w = both(w_gate, w_up, "w_gate and w_up") if dxs is not None else (None, None, inner * hidden)
+    to = (_addr(dgate, "dgate", own, wide, dev), _addr(dup, "dup", own, wide, dev), _opt(dxs, "dxs", own, narrow, dev),
+          *both(dw_gate, dw_up, "dw_gate and dw_up"))
+    numbers = _ints(experts=1 if experts is None else experts)
+    device = dout.device
+    with _on(device):
+        _check(lib().ar_expert_gated_bwd(*at, *w, off, cnt, *numbers, rows, hidden, inner, dtype_code(dt), *_ints(act=act),
+                                         *to, _stream(stream, device)), "ar_expert_gated_bwd")
+
+
+def ar_expert_linear(xs, w, out, offsets=None, counts=None, stream=None):
+    """out = xs w[e]^T for the rows of every expert's segment: xs [rows, in], w [experts, out, in] (without segments also
+    [out, in]), out [rows, out]. Segments and weights as in ar_expert_gated."""
+    shape, dt, dev = _matrix(xs, "xs")
+    if out.dim() != 2:
+        raise ValueError("out must be a matrix [rows, out]")
+    rows, inside = shape
+    off, cnt, experts = _segments(offsets, counts, dev)
+    at = _addr(xs, "xs", (dt,), shape, dev)
+    if w is None:
+        raise ValueError("w must be a tensor")
+    weight = _weights(w, "w", dt, experts, out.shape[1], inside, dev)
+    to = _addr(out, "out", (dt,), (rows, out.shape[1]), dev)
+    numbers = _ints(experts=1 if experts is None else experts)
+    device = xs.device
+    with _on(device):
+        _check(lib().ar_expert_linear(at, *weight, off, cnt, *numbers, rows, inside, out.shape[1], dtype_code(dt), to,
+                                      _stream(stream, device)), "ar_expert_linear")
+
+
+def ar_expert_linear_bwd(dout, xs, w, dxs=None, dw=None, offsets=None, counts=None, stream=None):
+    """The gradient of ar_expert_linear: dxs = dout w[e] [rows, in] (None: not wanted; w may then be None) and
+    dw[e] = dout^T xs [experts, out, in] over the expert's rows (None: not wanted; xs may then be None)."""
+    wide, dt, dev = _matrix(dout, "dout")
+    rows, out = wide
+    if dxs is not None and w is None:
+        raise ValueError("dxs needs w")
+    if dw is not None and xs is None:
+        raise ValueError("dw needs xs")
+    known = dxs if dxs is not None else xs
+    if known is None or known.dim() != 2:
+        raise ValueError("dxs or dw must be wanted, and xs and dxs must be matrices [rows, in]")
+    narrow = (rows, known.shape[1])
+    off, cnt, experts = _segments(offsets, counts, dev)
+    at = (_addr(dout, "dout", (dt,), wide, dev), _opt(xs, "xs", (dt,), narrow, dev))
+    weight = _weights(w if dxs is not None else None, "w", dt, experts, out, narrow[1], dev)
+    to = (_opt(dxs, "dxs", (dt,), narrow, dev), *_weights(dw, "dw", dt, experts, out, narrow[1], dev))
+    numbers = _ints(experts=1 if experts is None else experts)
+    device = dout.device
+    with _on(device):
+        _check(lib().ar_expert_linear_bwd(*at, *weight, off, cnt, *numbers, rows, narrow[1], out, dtype_code(dt), *to,
+                                          _stream(stream, device)), "ar_expert_linear_bwd")
 
 
 # ------------------------------------------------------------------------------------------ bucketing

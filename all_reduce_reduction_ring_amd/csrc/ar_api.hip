@@ -13,6 +13,7 @@
 #include "ar.h"
 #include "ar_block.h"
 #include "ar_internal.h"
+#include "ar_products.h"
 
 namespace ar {
 
@@ -856,6 +857,253 @@ int ar_expert_combine_bwd(const void* dout, const void* ys, const int32_t* pos, 
   a.k = k;
   a.experts = nexperts;
   const hipError_t e = ar::launch_expert_combine_bwd(a, dtype, static_cast<hipStream_t>(stream));
+  return done(e == hipSuccess ? AR_OK : AR_ERR_HIP);
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------------------------------ experts' products
+namespace {
+
+// The sizes of one call of the products: what all of them check of their common arguments. AR_OK goes on.
+struct ProductSizes {
+  size_t in_bytes, out_bytes;  // the buffers of rows of `in` and of `out` elements
+  size_t matrix;               // elements of a matrix
+};
+int product_common(size_t rows, size_t in, size_t out, int dtype, const int32_t* offsets, const int32_t* counts,
+                   int nexperts, ProductSizes* z) {
+  if (!valid_dtype(dtype) || in == 0 || out == 0 || rows > INT32_MAX) return AR_ERR_INVALID;
+  if (nexperts < 1 || nexperts > AR_MAX_EXPERTS || (!offsets && (counts || nexperts != 1))) return AR_ERR_INVALID;
+  if (dtype == AR_I32 || in > AR_PRODUCT_MAX_WIDTH || out > AR_PRODUCT_MAX_WIDTH) return AR_ERR_UNSUPPORTED;
+  const size_t es = static_cast<size_t>(esize_of(dtype));
+  z->in_bytes = rows * in * es;  // below 2^53
+  z->out_bytes = rows * out * es;
+  z->matrix = in * out;
+  return AR_OK;
+}
+
+// Adds one matrix per expert, `stride` elements apart (none but the size of a matrix matters for a single expert), and a
+// second set of the same layout (or NULL) that may lie in the gaps of the first, as the halves of one tensor do.
+bool add_matrices(Ranges& g, const void* p0, const void* p1, size_t matrix, size_t stride, int nexperts, size_t es) {
+  size_t span = 0;
+  if (nexperts == 1) stride = matrix;
+  if (stride < matrix || !mul(stride, static_cast<size_t>(nexperts - 1), &span) || !mul(span + matrix, es, &span))
+    return false;
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p0), b = reinterpret_cast<uintptr_t>(p1);
+  const uintptr_t lo = a < b ? a : b, d = a < b ? b - a : a - b;
+  if (p0 && p1 && d < span && nexperts > 1 && a % es == 0 && b % es == 0) {
+    const size_t off = d % (stride * es), size = matrix * es;
+    if (off >= size && stride * es - off >= size) {
+      g.add(reinterpret_cast<const void*>(lo), d + span, es);
+      return true;
+    }
+  }
+  g.add(p0, span, es, false);
+  g.add(p1, span, es, false);
+  return true;
+}
+
+bool too_many_tiles(const ar::ProductArgs& a, int64_t in, int64_t out) {
+  const int64_t wide = in > out ? in : out;
+  return ar::row_tiles(a, 1, 16) * ar::tiles_up(wide, 16) > ar::kMostTiles ||
+         ar::matrices(a) * ar::tiles_up(in, 64) * ar::tiles_up(out, 64) > ar::kMostTiles;
+}
+
+void add_segments(Ranges& g, const int32_t* offsets, const int32_t* counts, int nexperts) {
+  g.add(offsets, (static_cast<size_t>(nexperts) + 1) * 4, 4, false);
+  g.add(counts, static_cast<size_t>(nexperts) * 4, 4, false);
+}
+
+ar::ProductArgs product_args(size_t rows, const int32_t* offsets, const int32_t* counts, int nexperts) {
+  ar::ProductArgs a{};
+  a.offsets = offsets;
+  a.counts = counts;
+  a.rows = static_cast<int>(rows);
+  a.experts = nexperts;
+  return a;
+}
+
+bool valid_act(int act) { return act >= AR_ACT_SILU && act <= AR_ACT_GELU_TANH; }
+
+}  // namespace
+
+extern "C" {
+
+int ar_expert_gated(const void* xs, const void* w_gate, const void* w_up, size_t w_stride, const int32_t* offsets,
+                    const int32_t* counts, int nexperts, size_t rows, size_t hidden, size_t inner, int dtype, int act,
+                    void* out, void* gate, void* up, void* stream) {
+  auto done = [&](int st) { return finish("ar_expert_gated", 0, rows, dtype, -1, -1, st); };
+  ProductSizes z;
+  const int st = product_common(rows, hidden, inner, dtype, offsets, counts, nexperts, &z);
+  if (st != AR_OK) return done(st);
+  if (!valid_act(act) || (gate == nullptr) != (up == nullptr)) return done(AR_ERR_INVALID);
+  if (rows == 0) return done(AR_OK);
+  const size_t es = static_cast<size_t>(esize_of(dtype));
+  Ranges g;
+  g.add(xs, z.in_bytes, es);
+  if (!w_gate || !w_up || !add_matrices(g, w_gate, w_up, z.matrix, w_stride, nexperts, es)) return done(AR_ERR_INVALID);
+  add_segments(g, offsets, counts, nexperts);
+  g.add(out, z.out_bytes, es);
+  g.add(gate, z.out_bytes, es, false);
+  g.add(up, z.out_bytes, es, false);
+  if (g.bad) return done(AR_ERR_INVALID);
+  if (any_overlap(g.r, g.m)) return done(AR_ERR_ALIAS);
+  ar::ProductArgs a = product_args(rows, offsets, counts, nexperts);
+  a.a0 = xs;
+  a.b0 = w_gate;
+  a.b1 = w_up;
+  a.c0 = out;
+  a.c1 = gate;
+  a.c2 = up;
+  a.w_stride = static_cast<int64_t>(w_stride);
+  a.n = static_cast<int>(inner);
+  a.k = static_cast<int>(hidden);
+  a.act = act;
+  if (too_many_tiles(a, a.k, a.n)) return done(AR_ERR_UNSUPPORTED);
+  return done(ar::launch_gated(a, dtype, static_cast<hipStream_t>(stream)) == hipSuccess ? AR_OK : AR_ERR_HIP);
+}
+
+int ar_expert_gated_bwd(const void* dout, const void* gate, const void* up, const void* xs, const void* w_gate,
+                        const void* w_up, size_t w_stride, const int32_t* offsets, const int32_t* counts, int nexperts,
+                        size_t rows, size_t hidden, size_t inner, int dtype, int act, void* dgate, void* dup, void* dxs,
+                        void* dw_gate, void* dw_up, size_t dw_stride, void* stream) {
+  auto done = [&](int st) { return finish("ar_expert_gated_bwd", 0, rows, dtype, -1, -1, st); };
+  ProductSizes z;
+  const int st = product_common(rows, hidden, inner, dtype, offsets, counts, nexperts, &z);
+  if (st != AR_OK) return done(st);
+  if (!valid_act(act) || (dw_gate == nullptr) != (dw_up == nullptr)) return done(AR_ERR_INVALID);
+  const size_t es = static_cast<size_t>(esize_of(dtype));
+  const bool some = rows > 0;
+  Ranges g;
+  g.add(dout, z.out_bytes, es, some);
+  g.add(gate, z.out_bytes, es, some);
+  g.add(up, z.out_bytes, es, some);
+  auto in_place = [&](const void* p) { return p == dout || p == gate || p == up; };
+  if (some && (!dgate || !dup)) return done(AR_ERR_INVALID);
+  if (!in_place(dgate)) g.add(dgate, z.out_bytes, es, some);
+  if (!in_place(dup)) g.add(dup, z.out_bytes, es, some);
+  // the rows' gradient needs the weights, and the weights' the rows
+  g.add(xs, z.in_bytes, es, some && dw_gate);
+  if (some && dxs && (!w_gate || !w_up)) return done(AR_ERR_INVALID);
+  if (!add_matrices(g, w_gate, w_up, z.matrix, w_stride, nexperts, es) ||
+      !add_matrices(g, dw_gate, dw_up, z.matrix, dw_stride, nexperts, es))
+    return done(AR_ERR_INVALID);
+  add_segments(g, offsets, counts, nexperts);
+  g.add(dxs, z.in_bytes, es, false);
+  if (g.bad) return done(AR_ERR_INVALID);
+  if ((some && dgate == dup) || any_overlap(g.r, g.m)) return done(AR_ERR_ALIAS);
+  ar::ProductArgs a = product_args(rows, offsets, counts, nexperts);
+  a.act = act;
+  const int in = static_cast<int>(hidden), wide = static_cast<int>(inner);
+  if (too_many_tiles(a, in, wide)) return done(AR_ERR_UNSUPPORTED);
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  hipError_t e = hipSuccess;
+  if (some) {
+    ar::ProductArgs b = a;
+    b.a0 = dout;
+    b.b0 = gate;
+    b.b1 = up;
+    b.c0 = dgate;
+    b.c1 = dup;
+    b.n = wide;
+    e = ar::launch_slopes(b, dtype, s);
+  }
+  if (e == hipSuccess && some && dxs) {
+    ar::ProductArgs b = a;
+    b.a0 = dgate;
+    b.a1 = dup;
+    b.b0 = w_gate;
+    b.b1 = w_up;
+    b.w_stride = static_cast<int64_t>(w_stride);
+    b.c0 = dxs;
+    b.n = in;
+    b.k = wide;
+    e = ar::launch_input_grad(b, dtype, s);
+  }
+  if (e == hipSuccess && dw_gate) {
+    ar::ProductArgs b = a;
+    b.a0 = dgate;
+    b.a1 = dup;
+    b.b0 = xs;
+    b.c0 = dw_gate;
+    b.c1 = dw_up;
+    b.c_stride = static_cast<int64_t>(dw_stride);
+    b.m = wide;
+    b.n = in;
+    if (b.a1 == nullptr) b.a1 = dw_up;  // without rows nothing is read, and both gradients are still set to zero
+    e = ar::launch_weight_grad(b, dtype, s);
+  }
+  return done(e == hipSuccess ? AR_OK : AR_ERR_HIP);
+}
+
+int ar_expert_linear(const void* xs, const void* w, size_t w_stride, const int32_t* offsets, const int32_t* counts,
+                     int nexperts, size_t rows, size_t in, size_t out, int dtype, void* ys, void* stream) {
+  auto done = [&](int st) { return finish("ar_expert_linear", 0, rows, dtype, -1, -1, st); };
+  ProductSizes z;
+  const int st = product_common(rows, in, out, dtype, offsets, counts, nexperts, &z);
+  if (st != AR_OK) return done(st);
+  if (rows == 0) return done(AR_OK);
+  const size_t es = static_cast<size_t>(esize_of(dtype));
+  Ranges g;
+  g.add(xs, z.in_bytes, es);
+  if (!w || !add_matrices(g, w, nullptr, z.matrix, w_stride, nexperts, es)) return done(AR_ERR_INVALID);
+  add_segments(g, offsets, counts, nexperts);
+  g.add(ys, z.out_bytes, es);
+  if (g.bad) return done(AR_ERR_INVALID);
+  if (any_overlap(g.r, g.m)) return done(AR_ERR_ALIAS);
+  ar::ProductArgs a = product_args(rows, offsets, counts, nexperts);
+  a.a0 = xs;
+  a.b0 = w;
+  a.c0 = ys;
+  a.w_stride = static_cast<int64_t>(w_stride);
+  a.n = static_cast<int>(out);
+  a.k = static_cast<int>(in);
+  if (too_many_tiles(a, a.k, a.n)) return done(AR_ERR_UNSUPPORTED);
+  return done(ar::launch_linear(a, dtype, static_cast<hipStream_t>(stream)) == hipSuccess ? AR_OK : AR_ERR_HIP);
+}
+
+int ar_expert_linear_bwd(const void* dys, const void* xs, const void* w, size_t w_stride, const int32_t* offsets,
+                         const int32_t* counts, int nexperts, size_t rows, size_t in, size_t out, int dtype, void* dxs,
+                         void* dw, size_t dw_stride, void* stream) {
+  auto done = [&](int st) { return finish("ar_expert_linear_bwd", 0, rows, dtype, -1, -1, st); };
+  ProductSizes z;
+  const int st = product_common(rows, in, out, dtype, offsets, counts, nexperts, &z);
+  if (st != AR_OK) return done(st);
+  const size_t es = static_cast<size_t>(esize_of(dtype));
+  const bool some = rows > 0;
+  Ranges g;
+  g.add(dys, z.out_bytes, es, some);
+  g.add(xs, z.in_bytes, es, some && dw);
+  if (some && dxs && !w) return done(AR_ERR_INVALID);
+  if (!add_matrices(g, w, nullptr, z.matrix, w_stride, nexperts, es) ||
+      !add_matrices(g, dw, nullptr, z.matrix, dw_stride, nexperts, es))
+    return done(AR_ERR_INVALID);
+  add_segments(g, offsets, counts, nexperts);
+  g.add(dxs, z.in_bytes, es, false);
+  if (g.bad) return done(AR_ERR_INVALID);
+  if (any_overlap(g.r, g.m)) return done(AR_ERR_ALIAS);
+  ar::ProductArgs a = product_args(rows, offsets, counts, nexperts);
+  if (too_many_tiles(a, static_cast<int64_t>(in), static_cast<int64_t>(out))) return done(AR_ERR_UNSUPPORTED);
+  a.a0 = dys;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  hipError_t e = hipSuccess;
+  if (some && dxs) {
+    ar::ProductArgs b = a;
+    b.b0 = w;
+    b.w_stride = static_cast<int64_t>(w_stride);
+    b.c0 = dxs;
+    b.n = static_cast<int>(in);
+    b.k = static_cast<int>(out);
+    e = ar::launch_input_grad(b, dtype, s);
+  }
+  if (e == hipSuccess && dw) {
+    a.b0 = xs;
+    a.c0 = dw;
+    a.c_stride = static_cast<int64_t>(dw_stride);
+    a.m = static_cast<int>(out);
+    a.n = static_cast<int>(in);
+    e = ar::launch_weight_grad(a, dtype, s);
+  }
   return done(e == hipSuccess ? AR_OK : AR_ERR_HIP);
 }
 

@@ -48,6 +48,7 @@ extern "C" {
 #define AR_FP8_BLOCK 128   /* elements per E4M3 scaling block */
 #define AR_NORM_MAX_HIDDEN 32768 /* widest row of the norm entry points */
 #define AR_MAX_EXPERTS 1024
+#define AR_PRODUCT_MAX_WIDTH (1 << 20) /* widest row of the experts' products */
 
 enum ar_status {
     AR_OK = 0,
@@ -60,6 +61,9 @@ enum ar_status {
 
 enum ar_dtype { AR_F32 = 0, AR_BF16 = 1, AR_F16 = 2, AR_I32 = 3 };
 enum ar_op { AR_SUM = 0, AR_AVG = 1, AR_MIN = 2, AR_MAX = 3 };
+/* Activations of the gated block: x / (1 + exp(-x)); x times the normal distribution's Phi(x); and its approximation
+ * x / 2 (1 + tanh(sqrt(2 / pi) (x + 0.044715 x^3))). */
+enum ar_act { AR_ACT_SILU = 0, AR_ACT_GELU = 1, AR_ACT_GELU_TANH = 2 };
 
 /* Algorithms. All of them return, on every rank, the same element-wise reduction; they differ in the
  * order in which floating-point partials are associated, and in how many passes over HBM they take.
@@ -396,6 +400,50 @@ int ar_expert_combine(const void* ys, const int32_t* pos, const float* weights, 
 int ar_expert_combine_bwd(const void* dout, const void* ys, const int32_t* pos, const float* weights,
                           const int32_t* offsets, const int32_t* counts, size_t tokens, int k, int nexperts,
                           size_t hidden, int dtype, size_t rows, void* dys, float* dweights, void* stream);
+
+/* The experts' products, between ar_expert_dispatch and ar_expert_combine. Expert e owns the rows offsets[e] to
+ * offsets[e] + counts[e] - 1 of the sorted buffers (as ar_expert_sort wrote the two; counts NULL: up to
+ * offsets[e + 1]) and one [out][in] matrix of every weight, w_stride (at least in * out) elements after the previous
+ * expert's; a weight may be a part of a wider tensor. Rows outside the segments, pad rows among them, are neither read
+ * nor written. offsets and counts NULL with nexperts 1: one matrix for all rows (a dense layer).
+ * The tables are read on the device: segments that leave [0, rows) are cut off, and segments that overlap give
+ * unspecified values.
+ * Products are summed in fp32; bf16 and f16 operands are multiplied exactly. The order of a sum is fixed by the call's
+ * sizes, types and addresses' alignment, not by what lies in the segments of other experts.
+ * Any address that is a multiple of the element size; multiples of 16 bytes, in addresses and in rows, run faster.
+ * No workspace. rows == 0 returns AR_OK; gradients of weights are then set to zero.
+ * Errors of all four: AR_ERR_INVALID (enum, NULL, alignment, sizes 0, strides, more than 2^31 - 1 rows, nexperts outside
+ * 1..AR_MAX_EXPERTS), AR_ERR_UNSUPPORTED (AR_I32; in or out above AR_PRODUCT_MAX_WIDTH; more than 2^30 tiles of 16 x 16),
+ * AR_ERR_ALIAS (any overlap that is not named), AR_ERR_HIP. */
+
+/* The gated feed-forward block's way up: g = x w_gate^T, u = x w_up^T, h = act(g) * u, in one pass over x.
+ *   xs: [rows][hidden].   w_gate, w_up: [nexperts][inner][hidden], w_stride apart.   out: h, [rows][inner].
+ *   gate, up: g and u rounded into dtype, [rows][inner], for the gradient; both or neither NULL. h is taken of g and u
+ *     before they are rounded, and rounded once. */
+int ar_expert_gated(const void* xs, const void* w_gate, const void* w_up, size_t w_stride, const int32_t* offsets,
+                    const int32_t* counts, int nexperts, size_t rows, size_t hidden, size_t inner, int dtype, int act,
+                    void* out, void* gate, void* up, void* stream);
+
+/* Its gradient. With dh = dout and g, u as the forward wrote them:
+ *   dgate = dh * u * act'(g),   dup = dh * act(g)                       (rounded into dtype, [rows][inner])
+ *   dxs = dgate w_gate + dup w_up                                       (of the rounded dgate and dup, in one sum)
+ *   dw_gate = dgate^T xs,   dw_up = dup^T xs   over every expert's rows (dw_stride apart, zero without rows)
+ * dgate and dup are different buffers; either may be dout, gate or up. dxs may be NULL (then w_gate and w_up are not
+ * read and may be), and so may dw_gate and dw_up together (then xs is not read). */
+int ar_expert_gated_bwd(const void* dout, const void* gate, const void* up, const void* xs, const void* w_gate,
+                        const void* w_up, size_t w_stride, const int32_t* offsets, const int32_t* counts, int nexperts,
+                        size_t rows, size_t hidden, size_t inner, int dtype, int act, void* dgate, void* dup, void* dxs,
+                        void* dw_gate, void* dw_up, size_t dw_stride, void* stream);
+
+/* One projection, as the block's way down: ys = xs w^T. xs: [rows][in], w: [nexperts][out][in], ys: [rows][out]. */
+int ar_expert_linear(const void* xs, const void* w, size_t w_stride, const int32_t* offsets, const int32_t* counts,
+                     int nexperts, size_t rows, size_t in, size_t out, int dtype, void* ys, void* stream);
+
+/* Its gradient: dxs = dys w and dw = dys^T xs over every expert's rows (zero without rows). dxs may be NULL (then w is
+ * not read and may be), and so may dw (then xs may be). */
+int ar_expert_linear_bwd(const void* dys, const void* xs, const void* w, size_t w_stride, const int32_t* offsets,
+                         const int32_t* counts, int nexperts, size_t rows, size_t in, size_t out, int dtype, void* dxs,
+                         void* dw, size_t dw_stride, void* stream);
 
 /* ------------------------------------------------------------------------------------------------ */
 /* Diagnostics ([V] "hangをtimeoutだけで再起動しない": keep the last collective entered, its sequence number,

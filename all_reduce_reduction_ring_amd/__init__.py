@@ -12,7 +12,8 @@ ar_bucket_unpack, ar_fp8_quant, ar_fp8_dequant, ar_auto_algo, ar_chunk_bounds, a
 ar_version; next to the reduction in a transformer layer: ar_allreduce_rmsnorm, ar_allreduce_rmsnorm_bwd,
 ar_allreduce_rmsnorm_bwd_workspace_size, ar_expert_rows, ar_expert_sort, ar_expert_sort_workspace_size,
 ar_expert_dispatch, ar_expert_combine, ar_expert_combine_bwd, and between dispatch and combine ar_expert_gated,
-ar_expert_gated_bwd, ar_expert_linear, ar_expert_linear_bwd. Helpers: chunk_bounds, make_copy_descs,
+ar_expert_gated_bwd, ar_expert_linear, ar_expert_linear_bwd; behind the gradients' all-reduce: ar_grad_plan,
+ar_grad_norm, ar_grad_norm_workspace_size, ar_grad_clip. Helpers: chunk_bounds, make_copy_descs,
 BucketedAllReduce.
 """
 from __future__ import annotations
@@ -40,6 +41,7 @@ __all__ = [
     "ar_expert_dispatch", "ar_expert_combine", "ar_expert_combine_bwd",
     "AR_PRODUCT_MAX_WIDTH", "AR_ACT_SILU", "AR_ACT_GELU", "AR_ACT_GELU_TANH", "ar_expert_gated", "ar_expert_gated_bwd",
     "ar_expert_linear", "ar_expert_linear_bwd",
+    "AR_NORM_L2", "AR_NORM_MAX", "ar_grad_plan", "ar_grad_norm", "ar_grad_norm_workspace_size", "ar_grad_clip",
 ]
 
 AR_OK, AR_ERR_INVALID, AR_ERR_UNSUPPORTED, AR_ERR_ALIAS, AR_ERR_WORKSPACE, AR_ERR_HIP = 0, 1, 2, 3, 4, 5
@@ -54,6 +56,7 @@ AR_NORM_MAX_HIDDEN = 32768
 AR_MAX_EXPERTS = 1024
 AR_PRODUCT_MAX_WIDTH = 1 << 20
 AR_ACT_SILU, AR_ACT_GELU, AR_ACT_GELU_TANH = 0, 1, 2
+AR_NORM_L2, AR_NORM_MAX = 0, 1
 AR_NOALLOC_WS_BYTES = 64 << 20
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -117,6 +120,10 @@ def lib():
                                           vp, sz, vp]
         L.ar_expert_linear.argtypes = [vp, vp, sz, vp, vp, i32, sz, sz, sz, i32, vp, vp]
         L.ar_expert_linear_bwd.argtypes = [vp, vp, vp, sz, vp, vp, i32, sz, sz, sz, i32, vp, vp, sz, vp]
+        L.ar_grad_plan.argtypes = [vp, i32, vp, ctypes.POINTER(sz)]
+        L.ar_grad_norm_workspace_size.argtypes = [sz, ctypes.POINTER(sz)]
+        L.ar_grad_norm.argtypes = [vp, sz, i32, vp, vp, sz, vp]
+        L.ar_grad_clip.argtypes = [vp, sz, i32, f32, f32, vp, vp, sz, vp]
         L.ar_status_string.argtypes = [i32]
         L.ar_status_string.restype = ctypes.c_char_p
         L.ar_last_call.argtypes = [ctypes.POINTER(_CallRecord)]
@@ -128,7 +135,8 @@ def lib():
                      "ar_allreduce_rmsnorm_bwd", "ar_allreduce_rmsnorm_bwd_workspace_size", "ar_expert_rows",
                      "ar_expert_sort", "ar_expert_sort_workspace_size", "ar_expert_dispatch", "ar_expert_combine",
                      "ar_expert_combine_bwd", "ar_expert_gated", "ar_expert_gated_bwd", "ar_expert_linear",
-                     "ar_expert_linear_bwd"):
+                     "ar_expert_linear_bwd", "ar_grad_plan", "ar_grad_norm_workspace_size", "ar_grad_norm",
+                     "ar_grad_clip"):
             getattr(L, name).restype = i32
         _lib = L
     return _lib
@@ -874,6 +882,72 @@ def ar_expert_linear_bwd(dout, xs, w, dxs=None, dw=None, offsets=None, counts=No
     with _on(device):
         _check(lib().ar_expert_linear_bwd(*at, *weight, off, cnt, *numbers, rows, narrow[1], out, dtype_code(dt), *to,
                                           _stream(stream, device)), "ar_expert_linear_bwd")
+
+
+# ------------------------------------------------------------------------------------------ gradients' norm
+_PIECE = np.dtype([("in", np.uint64), ("out", np.uint64), ("numel", np.int64), ("dtype", np.int32), ("reserved", np.int32)])
+
+
+def ar_grad_plan(tensors, outs=None):
+    """The table that ar_grad_norm and ar_grad_clip work through, for the gradients `tensors` (contiguous GPU tensors of
+    float32, bfloat16 and float16, any shapes), int64 [pieces, 4] on their device. outs: where clipping writes, one tensor
+    of the same type and size each (None: in place). The table holds addresses: it is built once, and the tensors are to
+    stay as long as it is used."""
+    import torch
+    tensors = list(tensors)
+    outs = tensors if outs is None else list(outs)
+    if not tensors or len(outs) != len(tensors):
+        raise ValueError("tensors must hold at least one tensor, and outs one for each")
+    device, kinds = tensors[0].device, _kinds()[0]
+    table = np.zeros(len(tensors), _PIECE)
+    for i, (t, o) in enumerate(zip(tensors, outs)):
+        if t.dtype not in kinds:
+            raise ValueError(f"tensors must be float32, bfloat16 or float16, not {t.dtype}")
+        _gpu_tensor(t, "a gradient", device=device)
+        _gpu_tensor(o, "an output", dtype=t.dtype, device=device)
+        if o.numel() != t.numel():
+            raise ValueError("an output must have its gradient's size")
+        table[i] = (t.data_ptr(), 0 if o is t else o.data_ptr(), t.numel(), dtype_code(t.dtype), 0)
+    n = ctypes.c_size_t(0)
+    _check(lib().ar_grad_plan(table.ctypes.data, *_ints(ntensors=len(table)), None, ctypes.byref(n)), "ar_grad_plan")
+    pieces = np.zeros(n.value, _PIECE)
+    if n.value:
+        _check(lib().ar_grad_plan(table.ctypes.data, len(table), pieces.ctypes.data, ctypes.byref(n)), "ar_grad_plan")
+    return torch.from_numpy(pieces.view(np.int64).reshape(-1, 4)).to(device)
+
+
+def ar_grad_norm_workspace_size(npieces) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().ar_grad_norm_workspace_size(*_sizes(npieces=npieces), ctypes.byref(out)), "ar_grad_norm_workspace_size")
+    return out.value
+
+
+def _plan_args(plan, norm, workspace):
+    import torch
+    if plan.dim() != 2 or plan.shape[1] != 4:
+        raise ValueError("plan must be a table of ar_grad_plan")
+    dev = plan.get_device()
+    at = _addr(plan, "plan", (torch.int64,), plan.shape, dev)
+    if norm.numel() != 1:
+        raise ValueError("norm must hold one element")
+    return at, plan.shape[0], _addr(norm, "norm", _kinds()[2], norm.shape, dev), _workspace_arg(workspace, dev)
+
+
+def ar_grad_norm(plan, norm, kind=AR_NORM_L2, workspace=None, stream=None):
+    """norm (float32, one element) = the norm over all gradients of a plan: the square root of the sum of squares
+    (AR_NORM_L2) or the largest magnitude (AR_NORM_MAX). workspace: a GPU tensor of
+    ar_grad_norm_workspace_size(plan.shape[0]) bytes."""
+    at, n, to, ws = _plan_args(plan, norm, workspace)
+    with _on(plan.device):
+        _check(lib().ar_grad_norm(at, n, *_ints(kind=kind), to, *ws, _stream(stream, plan.device)), "ar_grad_norm")
+
+
+def ar_grad_clip(plan, max_norm, norm, kind=AR_NORM_L2, eps=1e-6, workspace=None, stream=None):
+    """ar_grad_norm, and all gradients times min(1, max_norm / (norm + eps)) into the plan's outputs."""
+    at, n, to, ws = _plan_args(plan, norm, workspace)
+    with _on(plan.device):
+        _check(lib().ar_grad_clip(at, n, *_ints(kind=kind), max_norm, eps, to, *ws, _stream(stream, plan.device)),
+               "ar_grad_clip")
 
 
 # ------------------------------------------------------------------------------------------ bucketing

@@ -12,6 +12,7 @@
 
 #include "ar.h"
 #include "ar_block.h"
+#include "ar_grads.h"
 #include "ar_internal.h"
 #include "ar_products.h"
 
@@ -1105,6 +1106,113 @@ int ar_expert_linear_bwd(const void* dys, const void* xs, const void* w, size_t 
     e = ar::launch_weight_grad(a, dtype, s);
   }
   return done(e == hipSuccess ? AR_OK : AR_ERR_HIP);
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------------------------------ gradients' norm
+namespace {
+
+bool float_dtype(int dtype) { return dtype == AR_F32 || dtype == AR_BF16 || dtype == AR_F16; }
+
+int grad_norm_impl(const char* entry, const ar_grad_piece* d_pieces, size_t npieces, int kind, bool clip, float max_norm,
+                   float eps, float* norm, void* workspace, size_t ws_bytes, void* stream) {
+  auto done = [&](int st) { return finish(entry, 0, npieces, AR_F32, -1, -1, st); };
+  if ((kind != AR_NORM_L2 && kind != AR_NORM_MAX) || npieces > INT32_MAX) return done(AR_ERR_INVALID);
+  if (clip && (!(max_norm >= 0.0f) || !(eps >= 0.0f) || !(eps <= 3.402823466e38f))) return done(AR_ERR_INVALID);
+  const size_t need = static_cast<size_t>(ar::grad_groups(static_cast<int64_t>(npieces))) * sizeof(double);
+  Ranges g;
+  g.add(d_pieces, npieces * sizeof(ar_grad_piece), 8, npieces > 0);
+  g.add(norm, 4, 4);
+  if (g.bad) return done(AR_ERR_INVALID);
+  if (need > 0) {
+    if (!workspace || ws_bytes < need) return done(AR_ERR_WORKSPACE);
+    g.add(workspace, need, 256);
+    if (g.bad) return done(AR_ERR_INVALID);
+  }
+  if (any_overlap(g.r, g.m)) return done(AR_ERR_ALIAS);
+  const ar::GradArgs a{d_pieces, static_cast<int64_t>(npieces), static_cast<double*>(workspace), norm, max_norm, eps, 0};
+  const hipError_t e = ar::launch_grad_norm(a, kind == AR_NORM_MAX, clip, static_cast<hipStream_t>(stream));
+  return done(e == hipSuccess ? AR_OK : AR_ERR_HIP);
+}
+
+// The tensors' ranges, and whether any two of them overlap. `room` holds two for each tensor.
+int check_tensors(const ar_grad_piece* t, int n, Range* room, int64_t* total) {
+  int m = 0;
+  *total = 0;
+  for (int i = 0; i < n; ++i) {
+    if (t[i].numel < 0 || !valid_dtype(t[i].dtype)) return AR_ERR_INVALID;
+    if (!float_dtype(t[i].dtype)) return AR_ERR_UNSUPPORTED;
+    if (t[i].numel == 0) continue;
+    const size_t es = static_cast<size_t>(esize_of(t[i].dtype));
+    const uintptr_t in = reinterpret_cast<uintptr_t>(t[i].in), out = reinterpret_cast<uintptr_t>(t[i].out);
+    if (t[i].numel > (int64_t(1) << 60)) return AR_ERR_INVALID;
+    const size_t bytes = static_cast<size_t>(t[i].numel) * es;
+    if (!in || in % es || out % es || in > UINTPTR_MAX - bytes || out > UINTPTR_MAX - bytes) return AR_ERR_INVALID;
+    room[m++] = Range{in, in + bytes};
+    if (out && out != in) room[m++] = Range{out, out + bytes};
+    *total += static_cast<int64_t>(bytes);
+    if (*total > (int64_t(1) << 62)) return AR_ERR_INVALID;
+  }
+  return any_overlap(room, m) ? AR_ERR_ALIAS : AR_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int ar_grad_plan(const ar_grad_piece* tensors, int ntensors, ar_grad_piece* pieces, size_t* npieces) {
+  auto done = [&](int st) {
+    return finish("ar_grad_plan", 0, static_cast<size_t>(ntensors < 0 ? 0 : ntensors), AR_F32, -1, -1, st);
+  };
+  if (!npieces || ntensors < 0 || (ntensors > 0 && !tensors)) return done(AR_ERR_INVALID);
+  const size_t room = pieces ? *npieces : 0;
+  *npieces = 0;
+  if (ntensors == 0) return done(AR_OK);
+  Range* ranges = static_cast<Range*>(std::malloc(2 * sizeof(Range) * static_cast<size_t>(ntensors)));
+  if (!ranges) return done(AR_ERR_INVALID);
+  int64_t total = 0;
+  const int st = check_tensors(tensors, ntensors, ranges, &total);
+  std::free(ranges);
+  if (st != AR_OK) return done(st);
+  const uint64_t piece = static_cast<uint64_t>(ar::piece_bytes(total));
+  size_t n = 0;
+  for (int i = 0; i < ntensors; ++i) {
+    const uint64_t es = static_cast<uint64_t>(esize_of(tensors[i].dtype));
+    const uint64_t bytes = static_cast<uint64_t>(tensors[i].numel) * es;
+    const uintptr_t in = reinterpret_cast<uintptr_t>(tensors[i].in), out = reinterpret_cast<uintptr_t>(tensors[i].out);
+    // cuts at multiples of the piece's size from the 256 bytes that the tensor starts in
+    uint64_t next = piece - in % 256;
+    for (uint64_t at = 0; at < bytes; at = next, next += piece, ++n) {
+      if (!pieces) {  // the rest of the count at once
+        n += next >= bytes ? 1 : 1 + (bytes - next + piece - 1) / piece;
+        break;
+      }
+      if (n >= room) return done(AR_ERR_INVALID);
+      const uint64_t end = next < bytes ? next : bytes;
+      pieces[n] = ar_grad_piece{reinterpret_cast<const void*>(in + at), out ? reinterpret_cast<void*>(out + at) : nullptr,
+                                static_cast<int64_t>((end - at) / es), tensors[i].dtype, 0};
+    }
+  }
+  *npieces = n;
+  return done(AR_OK);
+}
+
+int ar_grad_norm_workspace_size(size_t npieces, size_t* bytes) {
+  auto done = [&](int st) { return finish("ar_grad_norm_workspace_size", 0, npieces, AR_F32, -1, -1, st); };
+  if (!bytes || npieces > INT32_MAX) return done(AR_ERR_INVALID);
+  *bytes = static_cast<size_t>(ar::grad_groups(static_cast<int64_t>(npieces))) * sizeof(double);
+  return done(AR_OK);
+}
+
+int ar_grad_norm(const ar_grad_piece* d_pieces, size_t npieces, int kind, float* norm, void* workspace, size_t ws_bytes,
+                 void* stream) {
+  return grad_norm_impl("ar_grad_norm", d_pieces, npieces, kind, false, 0.0f, 0.0f, norm, workspace, ws_bytes, stream);
+}
+
+int ar_grad_clip(const ar_grad_piece* d_pieces, size_t npieces, int kind, float max_norm, float eps, float* norm,
+                 void* workspace, size_t ws_bytes, void* stream) {
+  return grad_norm_impl("ar_grad_clip", d_pieces, npieces, kind, true, max_norm, eps, norm, workspace, ws_bytes, stream);
 }
 
 }  // extern "C"

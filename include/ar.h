@@ -446,6 +446,49 @@ int ar_expert_linear_bwd(const void* dys, const void* xs, const void* w, size_t 
                          void* dw, size_t dw_stride, void* stream);
 
 /* ------------------------------------------------------------------------------------------------ */
+/* The norm over all gradients, and the gradients scaled down to a largest norm: the step between the gradients'
+ * all-reduce ([G] "パフォーマンスチューニング" and [W] "在 DDP 中的角色": what data-parallel training averages) and the
+ * optimizer. Tensors of AR_F32, AR_BF16 and AR_F16 may be mixed, of any sizes, at any multiple of their element size. */
+enum ar_norm { AR_NORM_L2 = 0, AR_NORM_MAX = 1 };
+
+/* A tensor, or a piece of one, of numel elements of dtype. */
+typedef struct ar_grad_piece {
+    const void* in;
+    void* out;          /* where clipping writes; NULL or `in`: in place */
+    int64_t numel;
+    int32_t dtype;
+    int32_t reserved;   /* 0 */
+} ar_grad_piece;
+
+/* Cuts tensors into pieces of 4 to 32 KiB, which the kernels spread over the GPU: host only. The caller copies the table to
+ * the device once and keeps it as long as the tensors stay where they are.
+ *   tensors: host array [ntensors].   pieces: host array of *npieces entries, or NULL to be told how many it takes.
+ *   *npieces: on entry the room in pieces (unused if NULL), on return the entries of the plan. Empty tensors take none.
+ * Errors: AR_ERR_INVALID (NULL, negative numel or ntensors, dtype, alignment, too little room), AR_ERR_UNSUPPORTED
+ * (AR_I32), AR_ERR_ALIAS (two tensors overlap, or one's out with another's in or out, or out with its own in other than
+ * in place). */
+int ar_grad_plan(const ar_grad_piece* tensors, int ntensors, ar_grad_piece* pieces, size_t* npieces);
+
+/* norm[0] = the norm over all elements of the table: sqrt of the sum of squares (AR_NORM_L2, summed in 64 bits, rounded
+ * once) or the largest magnitude (AR_NORM_MAX). Any NaN gives NaN. Without elements 0. The order of the sum is fixed by
+ * the table.
+ *   d_pieces: DEVICE array [npieces], as ar_grad_plan made it. (Pieces of other lengths are right, but slow; one with a
+ *     negative numel or another dtype counts as empty.)
+ *   norm: device float[1].   workspace: ar_grad_norm_workspace_size() bytes, 256-byte aligned; clobbered. Calls that
+ *   overlap in time take one each.
+ * Errors: AR_ERR_INVALID (kind, NULL, alignment, npieces above 2^31 - 1), AR_ERR_WORKSPACE, AR_ERR_ALIAS, AR_ERR_HIP. */
+int ar_grad_norm_workspace_size(size_t npieces, size_t* bytes);
+int ar_grad_norm(const ar_grad_piece* d_pieces, size_t npieces, int kind, float* norm, void* workspace, size_t ws_bytes,
+                 void* stream);
+
+/* The same, and out = in * min(1, max_norm / (norm + eps)) for every element, in fp32, rounded once. Where that is 1,
+ * pieces in place are not written. A norm of NaN makes every element NaN, one of infinity (an infinite element, with a
+ * finite max_norm) zero or, from infinities, NaN: check norm before the step. max_norm and eps: not negative, not NaN, eps
+ * finite. Errors as ar_grad_norm. */
+int ar_grad_clip(const ar_grad_piece* d_pieces, size_t npieces, int kind, float max_norm, float eps, float* norm,
+                 void* workspace, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------------------------------ */
 /* Diagnostics ([V] "hangをtimeoutだけで再起動しない": keep the last collective entered, its sequence number,
  * shape and dtype, and the error before it). */
 

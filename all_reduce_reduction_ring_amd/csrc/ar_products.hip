@@ -20,6 +20,8 @@
 #include "ar_internal.h"
 #include "ar_products.h"
 
+#include <type_traits>
+
 namespace ar {
 namespace {
 
@@ -28,9 +30,6 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef short i16x4 __attribute__((ext_vector_type(4)));
 #define AR_LDS __attribute__((address_space(3)))
-
-constexpr int kStep = 128;            // bytes of the sum per step and row
-constexpr int kChunks = kStep / 16;   // 16-byte chunks of a step
 
 enum Kind { kGated = 0, kLinear = 1, kInput = 2, kWeight = 3 };
 
@@ -70,14 +69,20 @@ __device__ __forceinline__ int all_tiles(const ProductArgs& a, int64_t width, in
   return uniform(sum);
 }
 
-// The expert that tile t (below all_tiles) belongs to, and the tile's number among the expert's.
-__device__ __forceinline__ void find_tile(const ProductArgs& a, int t, int64_t width, int unit, int* expert, int* index) {
-  *expert = 0;
-  *index = t;
-  if (!a.offsets) return;
+// Tile t of all: its expert, its number among the expert's tiles, and the expert's rows. False if no expert has it.
+struct Place {
+  int expert, index, first, n;
+};
+__device__ __forceinline__ bool find_tile(const ProductArgs& a, int t, int64_t width, int unit, Place* at) {
+  if (!a.offsets) {
+    *at = Place{0, t, 0, a.rows};
+    return true;
+  }
   const int lane = threadIdx.x & 63;
   for (int e0 = 0, before = 0; e0 < a.experts; e0 += 64) {
-    const int own = e0 + lane < a.experts ? tiles_of(a, e0 + lane, width, unit) : 0;
+    int first = 0, n = 0;
+    if (e0 + lane < a.experts) segment(a, e0 + lane, &first, &n);
+    const int own = static_cast<int>((n * width + unit - 1) / unit);
     int upto = own;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
@@ -88,12 +93,13 @@ __device__ __forceinline__ void find_tile(const ProductArgs& a, int t, int64_t w
     const uint64_t mine = __ballot(t >= upto - own && t < upto);
     if (mine) {
       const int l = __builtin_ctzll(mine);
-      *expert = uniform(e0 + l);
-      *index = uniform(t - __shfl(upto - own, l, 64));
-      return;
+      auto of = [&](int v) { return __builtin_amdgcn_readlane(v, l); };
+      *at = Place{uniform(e0 + l), t - of(upto - own), of(first), of(n)};
+      return true;
     }
-    before = __shfl(upto, 63, 64);
+    before = __builtin_amdgcn_readlane(upto, 63);
   }
+  return false;
 }
 
 // ------------------------------------------------------------------------------------------ operands
@@ -112,15 +118,18 @@ template <int DT> __device__ __forceinline__ f32x4 mma(const u32x4& x, const u32
   }
 }
 
-// How an operand's tile lies in LDS, in 16-byte chunks. KC: [row][8 chunks along the sum]; KS: [sum][row chunks]. Chunks
-// are exchanged within an LDS row by an exclusive or, so that the 64 lanes of a fragment read spread over all banks.
-//   KC, rows in order:  16 rows a read, one chunk each: bits 1 to 3 of the row (bit 0 is the half of the 256-byte bank
-//                       row that it lies in).
-//   KC, PAIRED:         the read takes rows 0-3, 8-11, 16-19, 24-27 (see n_of): bits 1, 3 and 4.
-//   KS, 16-bit:         4 rows of the sum of 32 bytes each for 16 lanes, the next 16 lanes 8 rows on.
-//   KS, fp32:           one row of the sum of 64 bytes for 16 lanes, the next 16 lanes 4 rows on.
-template <bool PAIRED> __device__ __forceinline__ int mix_kc(int row) {
-  return PAIRED ? ((row >> 1) & 1) | ((row >> 2) & 6) : (row >> 1) & 7;
+// How an operand's tile lies in LDS, in 16-byte chunks. KC: [row][CH chunks along the sum]; KS: [sum][row chunks]. Chunks
+// are exchanged within an LDS row by an exclusive or, so that the 64 lanes of a fragment read spread over all banks (no
+// conflicts were counted).
+//   KC: 16 rows a read, one chunk each, and the next chunk for the next 16 lanes. With 8 chunks in an LDS row, bits 1 to 3
+//       of the row (bit 0 is the half of the 256-byte bank row that it lies in); with 4, bits 2 and 3 in Gray order.
+//       PAIRED reads take rows 0-3, 8-11, 16-19, 24-27 (see n_of): bits 3 and 4 in the place of 2 and 3.
+//   KS, 16-bit: 4 rows of the sum of 32 bytes each for 16 lanes, the next 16 lanes 8 rows on.
+//   KS, fp32: one row of the sum of 64 bytes for 16 lanes, the next 16 lanes 4 rows on.
+template <int CH, bool PAIRED> __device__ __forceinline__ int mix_kc(int row) {
+  if constexpr (CH == 8) return PAIRED ? ((row >> 1) & 1) | ((row >> 2) & 6) : (row >> 1) & 7;
+  const int t = PAIRED ? row >> 3 : row >> 2;
+  return ((t >> 1) & 1) | ((t ^ (t >> 1)) & 1) << 1;
 }
 template <int DT> __device__ __forceinline__ int mix_ks(int k) {
   if constexpr (Traits<DT>::kSize == 2) return ((k & 3) << 1) | (k & 8);
@@ -133,16 +142,44 @@ template <bool PAIRED> __device__ __forceinline__ int n_of(int j, int q, int i) 
   return PAIRED ? (j / 2) * 32 + q * 8 + (j % 2) * 4 + i : j * 16 + q * 4 + i;
 }
 
-// One operand's tile of R rows, for NT threads: from memory through registers into LDS.
-template <int DT, bool KS, bool PAIRED, int R, int NT> struct Tile {
+// 16 bytes per lane from memory straight into LDS: lane l's go to `lds` (uniform, an LDS byte address) + 16 l. `base` and
+// `bytes` are uniform too; a lane whose offset reaches `bytes` gets zeros. Nothing waits here (see ready).
+constexpr uint32_t kNowhere = 0x80000000u, kMostBytes = 0x7FFFFFF0u;
+__device__ __forceinline__ void load_lds(const char* base, uint32_t bytes, uint32_t at, uint32_t lds) {
+  const uint64_t b = reinterpret_cast<uint64_t>(base);
+  auto scalar = [](uint32_t v) { return static_cast<uint32_t>(uniform(static_cast<int>(v))); };
+  const u32x4 rsrc = {scalar(static_cast<uint32_t>(b)), scalar(static_cast<uint32_t>(b >> 32) & 0xFFFFu), scalar(bytes), 0x00020000u};
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 4\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(at), "s"(rsrc), "s"(scalar(lds))
+               : "memory");
+}
+// All but the last N of a wave's loads have landed and its reads of LDS are done, for all waves of the workgroup.
+template <int N> __device__ __forceinline__ void ready() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+// The first n elements of a 16-byte chunk, zeros behind them.
+template <int DT> __device__ __forceinline__ u32x4 first_elements(const char* p, int n) {
+  u32x4 w = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < Traits<DT>::kVec; ++i) {
+    const uint32_t bits = i < n ? load_elem<DT>(p, i) : 0;
+    if constexpr (Traits<DT>::kSize == 2) w[i >> 1] |= bits << (16 * (i & 1));
+    else w[i] = bits;
+  }
+  return w;
+}
+
+// One operand's tile of R rows and CH chunks of the sum, for NT threads: from memory through registers into LDS, or (DIRECT)
+// straight into it, for rows and addresses that are multiples of 16 bytes.
+template <int DT, bool KS, bool PAIRED, bool DIRECT, int CH, int R, int NT> struct Tile {
   static constexpr int V = Traits<DT>::kVec, ES = Traits<DT>::kSize;
-  static constexpr int kRowChunks = KS ? R / V : kChunks;      // chunks of an LDS row
-  static constexpr int kLoads = R * kChunks / NT;               // chunks a thread moves
+  static constexpr int kRowChunks = KS ? R / V : CH;           // chunks of an LDS row
+  static constexpr int kLoads = R * CH / NT;                    // chunks a thread moves
   static constexpr int kStride = NT / kRowChunks;               // LDS rows between a thread's chunks
-  static_assert(R * kChunks % NT == 0 && NT % kRowChunks == 0, "whole loads");
+  static_assert(R * CH % NT == 0 && NT % kRowChunks == 0, "whole loads");
   static_assert(KS ? (kStride % 4 == 0) : (kStride % 32 == 0), "a thread's chunks are mixed alike");
 
-  uint32_t at[kLoads];  // KC: byte offset of the row (clamped to the last one)
+  uint32_t at[kLoads];  // KC: byte offset of the row (clamped to the last one). DIRECT: of the chunk in the step
   int lds_row, chunk;   // of the first chunk: where it lies in LDS, and the chunk of the row in memory
   int limit;            // KS: rows (columns in memory) left in the matrix from the tile's first
 
@@ -152,13 +189,26 @@ template <int DT, bool KS, bool PAIRED, int R, int NT> struct Tile {
     lds_row = tid / kRowChunks;
     limit = nrows;
     if constexpr (!KS) {
-      chunk = (tid % kRowChunks) ^ mix_kc<PAIRED>(lds_row);
+      chunk = (tid % kRowChunks) ^ mix_kc<CH, PAIRED>(lds_row);
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
         const int r = map(lds_row + i * kStride);
-        at[i] = static_cast<uint32_t>(r < nrows ? r : nrows - 1) * stride;
+        at[i] = static_cast<uint32_t>(r < nrows ? r : nrows - 1) * stride + (DIRECT ? chunk * 16 : 0);
+      }
+    } else if constexpr (DIRECT) {
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int k = lds_row + i * kStride;
+        at[i] = static_cast<uint32_t>(k) * stride + (static_cast<uint32_t>(tid % kRowChunks) ^ mix_ks<DT>(k)) * 16;
       }
     }
+  }
+
+  // Load i of a step of the sum straight into LDS. `base` is the matrix at the tile's first row and the step's first element;
+  // lanes whose chunk is not `in` the sum (KC) or lies `bytes` or more behind base (KS: the rest of the matrix) leave zeros.
+  // (KS: a chunk past a row's end reads the next row's start, whose results go nowhere, and nothing past the matrix.)
+  __device__ __forceinline__ void load(int i, const char* base, uint32_t bytes, bool in, uint32_t to) const {
+    load_lds(base, bytes, KS || in ? at[i] : kNowhere, to + i * NT * 16);
   }
 
   // Reads the step of the sum that starts `k0` elements in: `base` is the matrix at the tile's first row and sum element
@@ -170,7 +220,7 @@ template <int DT, bool KS, bool PAIRED, int R, int NT> struct Tile {
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
         if (k + V <= K) v[i] = ldu16(p + at[i]);
-        else v[i] = part(p + at[i], K - k);
+        else v[i] = first_elements<DT>(p + at[i], K - k);
       }
     } else {
 #pragma unroll
@@ -179,21 +229,9 @@ template <int DT, bool KS, bool PAIRED, int R, int NT> struct Tile {
         const int c = ((static_cast<int>(threadIdx.x) % kRowChunks) ^ mix_ks<DT>(row)) * V;
         const char* p = base + static_cast<int64_t>(k) * stride + c * ES;
         if (k < K && c + V <= limit) v[i] = ldu16(p);
-        else v[i] = part(p, k < K ? limit - c : 0);
+        else v[i] = first_elements<DT>(p, k < K ? limit - c : 0);
       }
     }
-  }
-  // The first n elements of a chunk, zeros behind them.
-  __device__ static __forceinline__ u32x4 part(const char* p, int n) {
-    u32x4 w = {0, 0, 0, 0};
-    if (n <= 0) return w;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const uint32_t bits = i < n ? load_elem<DT>(p, i) : 0;
-      if constexpr (ES == 2) w[i >> 1] |= bits << (16 * (i & 1));
-      else w[i] = bits;
-    }
-    return w;
   }
   __device__ __forceinline__ void put(const u32x4 (&v)[kLoads], AR_LDS char* lds) const {
 #pragma unroll
@@ -206,7 +244,7 @@ template <int DT, bool KS, bool PAIRED, int R, int NT> struct Tile {
     if constexpr (!KS) {
       const int j = (r0 / 16) & 3;
       const int row = PAIRED ? (r0 & ~63) + n_of<true>(j, l >> 2, l & 3) : r0 + l;
-      return *(const AR_LDS u32x4*)(lds + row * kStep + (((kk * 4 + q) ^ mix_kc<PAIRED>(row)) * 16));
+      return *(const AR_LDS u32x4*)(lds + row * (CH * 16) + (((kk * 4 + q) ^ mix_kc<CH, PAIRED>(row)) * 16));
     } else if constexpr (ES == 2) {
       const int k = kk * 32 + q * 8 + (l >> 2), c = r0 + (l & 3) * 4;
       const AR_LDS char* p = lds + k * (R * ES) + (((c / V) ^ mix_ks<DT>(k)) * 16) + (c % V) * ES;
@@ -283,16 +321,34 @@ template <int DT, int N> __device__ __forceinline__ void store_run(char* p, cons
 template <int KIND> constexpr bool kRowsKS = KIND == kWeight;                        // operand of the tile's rows
 template <int KIND> constexpr bool kColsKS = KIND == kWeight || KIND == kInput;      // operand of its columns
 
-template <int DT, int KIND, int BM, int BN, int WM, int WN>
+// Tiles follow each other so that the workgroups of one XCD (every eighth one) work on neighbouring tiles, kRaster tiles
+// down before the next column, and share the operands in its L2.
+constexpr int kRaster = 4;
+__device__ __forceinline__ int xcd_order(int id, int total) {
+  const int x = id & 7, q = total >> 3, r = total & 7;
+  return x * q + (x < r ? x : r) + (id >> 3);
+}
+__device__ __forceinline__ void raster(int t, int down, int across, int* row, int* col) {
+  const int group = t / (kRaster * across), in = t - group * (kRaster * across);
+  const int high = min(kRaster, down - group * kRaster);
+  *col = in / high;
+  *row = group * kRaster + in - *col * high;
+}
+
+template <int DT, int KIND, bool DIRECT, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(WM* WN * 64) void tile_kernel(const ProductArgs a) {
-  constexpr int NT = WM * WN * 64, ES = Traits<DT>::kSize, K_STEP = kStep / ES;
+  // chunks of the sum per step, and steps that LDS holds
+  constexpr int CH = 8, PLACES = DIRECT ? 5 : 4;  // chunks of the sum per step; operand tiles that LDS holds
+  constexpr int NT = WM * WN * 64, ES = Traits<DT>::kSize, V = 16 / ES, K_STEP = CH * V;
   constexpr int MI = BM / WM / 16, NI = BN / WN / 16;
   constexpr bool PAIRED = !kColsKS<KIND>;
-  static_assert(BN / WN == 64, "a wave has 64 columns");
+  constexpr int WCOLS = BN / WN;  // a wave's columns, in blocks of 64
+  static_assert(WCOLS % 64 == 0 && MI % 2 == 0, "whole blocks");
   constexpr int COLS = KIND == kGated ? BN / 2 : BN;  // columns of the result
-  using A = Tile<DT, kRowsKS<KIND>, false, BM, NT>;
-  using B = Tile<DT, kColsKS<KIND>, PAIRED, BN, NT>;
-  __shared__ __align__(128) char smem[2][(BM + BN) * kStep];
+  using A = Tile<DT, kRowsKS<KIND>, false, DIRECT, CH, BM, NT>;
+  using B = Tile<DT, kColsKS<KIND>, PAIRED, DIRECT, CH, BN, NT>;
+  static_assert(BM == BN, "operand tiles take each other's places");
+  __shared__ __align__(1024) char smem[PLACES][BM * CH * 16];
   const int wave = uniform(threadIdx.x >> 6), wm = wave / WN, wn = wave % WN;
   const int l = threadIdx.x & 15, q = (threadIdx.x >> 4) & 3;
 
@@ -310,21 +366,27 @@ __global__ __launch_bounds__(WM* WN * 64) void tile_kernel(const ProductArgs a) 
     // which tile
     int e, mt, nt, which = 0, first, n, K;
     if constexpr (KIND == kWeight) {
-      nt = id % across;
-      mt = id / across % down;
+      // every matrix's tiles go to all XCDs: experts differ in rows, and so in work
       const int z = id / (across * down);
+      raster(xcd_order(id - z * (across * down), across * down), down, across, &mt, &nt);
       e = a.a1 ? z >> 1 : z;
       which = a.a1 ? z & 1 : 0;
     } else {
-      nt = id % across;
-      find_tile(a, id / across, 1, BM, &e, &mt);
+      int row;
+      raster(xcd_order(id, total), down, across, &row, &nt);
+      Place at{};
+      if (!find_tile(a, row, 1, BM, &at)) continue;  // tables that changed meanwhile
+      e = at.expert;
+      mt = at.index;
+      first = at.first;
+      n = at.n;
     }
-    segment(a, e, &first, &n);
+    e = uniform(e);
+    if constexpr (KIND == kWeight) segment(a, e, &first, &n);
     first = uniform(first);
     n = uniform(n);
-    const int m0 = mt * BM, n0 = nt * COLS;
-    if (KIND != kWeight && m0 >= n) continue;  // tables that describe no segments
-    // the operands at the tile's first row or column and sum element 0
+    const int m0 = uniform(mt) * BM, n0 = uniform(nt) * COLS;
+    // the operands at the tile's first row or column and sum element 0, and the bytes of them per row and per step
     const char *pa, *pb, *pa1 = nullptr, *pb1 = nullptr;
     uint32_t sa, sb;
     int rows_left, cols_left = a.n - n0;
@@ -365,51 +427,185 @@ __global__ __launch_bounds__(WM* WN * 64) void tile_kernel(const ProductArgs a) 
 #pragma unroll
       for (int i = 0; i < MI; ++i) acc[j][i] = f32x4{0, 0, 0, 0};
 
-    u32x4 va[A::kLoads], vb[B::kLoads];
-    auto fetch = [&](int s) {
-      const bool second = s >= steps1;
-      const int k0 = (second ? s - steps1 : s) * K_STEP;
-      ta.fetch(va, second ? pa1 : pa, sa, k0, K);
-      if constexpr (KIND == kGated) {
-        // rows 32 to 63 of every 64 in LDS are of w_up; whole waves read one matrix
+    // A wave's part of the tile may lie wholly or in its second half past the result: it is not computed there.
+    const int rows_wave = rows_left - wm * (BM / WM);
+    const bool none = rows_wave <= 0 || cols_left <= wn * (KIND == kGated ? WCOLS / 2 : WCOLS), half = rows_wave <= BM / WM / 2;
+    auto read_a = [&](const AR_LDS char* at, int i, int kk) { return A::read(at, wm * (BM / WM) + i * 16, kk); };
+    auto read_b = [&](const AR_LDS char* at, int j, int kk) { return B::read(at, wn * WCOLS + j * 16, kk); };
+    // the products of one step, for the first `N` of the wave's MI times 16 rows
+    auto simple = [&](const AR_LDS char* at_a, const AR_LDS char* at_b, auto N) {
 #pragma unroll
-        for (int i = 0; i < B::kLoads; ++i) {
-          const int r = tb.lds_row + i * B::kStride, k = k0 + tb.chunk * B::V;
-          const char* p = ((r & 32) ? pb1 : pb) + static_cast<int64_t>(k) * ES + tb.at[i];
-          vb[i] = k + B::V <= K ? ldu16(p) : B::part(p, K - k);
-        }
-      } else {
-        tb.fetch(vb, second ? pb1 : pb, sb, k0, K);
-      }
-    };
-    auto put = [&](int s) {
-      AR_LDS char* at = (AR_LDS char*)(smem[s & 1]);
-      ta.put(va, at);
-      tb.put(vb, at + BM * kStep);
-    };
-    if (steps > 0) {
-      fetch(0);
-      put(0);
-    }
-    for (int s = 0; s < steps; ++s) {
-      __syncthreads();  // the buffer of this step is filled, and nobody reads the other one any more
-      if (s + 1 < steps) fetch(s + 1);
-      const AR_LDS char* at = (const AR_LDS char*)(smem[s & 1]);
+      for (int kk = 0; kk < CH / 4; ++kk) {
+        u32x4 fb[NI], fa[N];
 #pragma unroll
-      for (int kk = 0; kk < 2; ++kk) {
-        u32x4 fb[NI], fa[MI];
+        for (int j = 0; j < NI; ++j) fb[j] = read_b(at_b, j, kk);
 #pragma unroll
-        for (int j = 0; j < NI; ++j) fb[j] = B::read(at + BM * kStep, wn * 64 + j * 16, kk);
-#pragma unroll
-        for (int i = 0; i < MI; ++i) fa[i] = A::read(at, wm * (BM / WM) + i * 16, kk);
+        for (int i = 0; i < N; ++i) fa[i] = read_a(at_a, i, kk);
 #pragma unroll
         for (int j = 0; j < NI; ++j)
 #pragma unroll
-          for (int i = 0; i < MI; ++i) acc[j][i] = mma<DT>(fb[j], fa[i], acc[j][i]);
+          for (int i = 0; i < N; ++i) acc[j][i] = mma<DT>(fb[j], fa[i], acc[j][i]);
       }
-      if (s + 1 < steps) put(s + 1);
+    };
+    constexpr std::integral_constant<int, MI> kAll{};
+    constexpr std::integral_constant<int, MI / 2> kHalf{};
+    if constexpr (DIRECT) {
+      // A step's products go in groups of NI, 16 rows and 4 chunks each. Fragments of rows are read four groups ahead, so
+      // that the last four groups of a step need nothing more from LDS: before them all waves meet, the next step has
+      // arrived and this one's places are free, and while they run the next step's first fragments are read. LDS has five
+      // places for the two operands' tiles in turn: the columns' loads start one step ahead, the rows' two, a few in every
+      // group, so that no wave's products wait for its loads to be issued.
+      const int64_t step_a = kRowsKS<KIND> ? static_cast<int64_t>(sa) * K_STEP : CH * 16;
+      const int64_t step_b = kColsKS<KIND> ? static_cast<int64_t>(sb) * K_STEP : CH * 16;
+      constexpr int kPlace = BM * CH * 16, kGroups = 2 * MI;
+      AR_LDS char* const places = (AR_LDS char*)(smem[0]);
+      const uint32_t to_wave = uniform(static_cast<int>(reinterpret_cast<uintptr_t>(places))) + wave * 1024;
+      auto advance = [](int& place) { place = place >= PLACES - 2 ? place - (PLACES - 2) : place + 2; };
+      // What a load of a step may read: KS, in a product's last step, the rest of the matrix. Nothing behind the last step;
+      // loads are issued then too, so that their number in flight stays the same.
+      const uint32_t rest_a = static_cast<uint32_t>(K - (steps1 - 1) * K_STEP) * sa - static_cast<uint32_t>(m0) * ES;
+      const uint32_t rest_b = static_cast<uint32_t>(K - (steps1 - 1) * K_STEP) * sb - static_cast<uint32_t>(n0) * ES;
+      auto bytes = [&](bool ks, uint32_t rest, int step) {
+        const bool last = step + 1 == steps1 || step + 1 == steps;
+        return step >= steps ? 0u : ks && last ? rest : kMostBytes;
+      };
+      int next_a = 0, next_b = 0, ka = 0, kb = 0, to_a = 0, to_b = 1;  // the steps to load, their first elements, places
+      auto load_a = [&](int i) {
+        ta.load(i, pa, bytes(kRowsKS<KIND>, rest_a, next_a), ka + ta.chunk * V < K, to_wave + to_a * kPlace);
+        if (i + 1 < A::kLoads) return;
+        pa += step_a;
+        ka += K_STEP;
+        if (KIND == kInput && ++next_a == steps1) {  // on to the second product of the sum
+          pa = pa1;
+          ka = 0;
+        }
+        if (KIND != kInput) ++next_a;
+        advance(to_a);
+      };
+      auto load_b = [&](int i) {
+        // gated: LDS rows 32 to 63 of every 64 are of w_up; whole waves read one matrix
+        const bool of_up = KIND == kGated && ((wave * (64 / CH) + i * B::kStride) & 32) != 0;
+        tb.load(i, of_up ? pb1 : pb, bytes(kColsKS<KIND>, rest_b, next_b), kb + tb.chunk * V < K, to_wave + to_b * kPlace);
+        if (i + 1 < B::kLoads) return;
+        pb += step_b;
+        if (KIND == kGated) pb1 += step_b;
+        kb += K_STEP;
+        if (KIND == kInput && ++next_b == steps1) {
+          pb = pb1;
+          kb = 0;
+        }
+        if (KIND != kInput) ++next_b;
+        advance(to_b);
+      };
+      auto all_a = [&] {
+#pragma unroll
+        for (int i = 0; i < A::kLoads; ++i) load_a(i);
+      };
+      auto all_b = [&] {
+#pragma unroll
+        for (int i = 0; i < B::kLoads; ++i) load_b(i);
+      };
+      int at_a = 0, at_b = 1;
+      if (steps > 0) {
+        all_a();
+        all_b();
+        all_a();
+        ready<A::kLoads>();
+        all_b();
+      }
+      if (none || half) {
+        for (int s = 0; s < steps; ++s) {
+          all_a();
+          if (!none) simple(places + at_a * kPlace, places + at_b * kPlace, kHalf);
+          advance(at_a);
+          advance(at_b);
+          ready<A::kLoads>();
+          all_b();
+        }
+      } else if (steps > 0) {
+        u32x4 b0[NI], b1[NI], rows[4];
+#pragma unroll
+        for (int j = 0; j < NI; ++j) b0[j] = read_b(places + at_b * kPlace, j, 0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) rows[i] = read_a(places + at_a * kPlace, i % MI, i / MI);
+        // Scalar loads are done here too: with some possibly on their way, every wait for a fragment in the loop would be one
+        // for all of them.
+        __builtin_amdgcn_s_waitcnt(0xC07F);
+        auto group = [&](int g, const u32x4(&b)[NI]) {
+#pragma unroll
+          for (int j = 0; j < NI; ++j) acc[j][g % MI] = mma<DT>(b[j], rows[g % 4], acc[j][g % MI]);
+        };
+        constexpr int kReads = NI / 4;
+        static_assert(A::kLoads % 4 == 0 && B::kLoads % 4 == 0 && kGroups >= 8, "loads in groups");
+        for (int s = 0; s < steps; ++s) {
+          const AR_LDS char *now_a = places + at_a * kPlace, *now_b = places + at_b * kPlace;
+          advance(at_a);
+          advance(at_b);
+          const AR_LDS char *then_a = places + at_a * kPlace, *then_b = places + at_b * kPlace;
+#pragma unroll
+          for (int g = 0; g < kGroups - 4; ++g) {
+            group(g, g < MI ? b0 : b1);
+            if (g < 4) {
+#pragma unroll
+              for (int j = g * kReads; j < (g + 1) * kReads; ++j) b1[j] = read_b(now_b, j, 1);
+            }
+            rows[g % 4] = read_a(now_a, (g + 4) % MI, (g + 4) / MI);
+            if (g < 4) {
+#pragma unroll
+              for (int i = g * (A::kLoads / 4); i < (g + 1) * (A::kLoads / 4); ++i) load_a(i);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+          }
+          ready<A::kLoads>();
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            group(kGroups - 4 + h, b1);
+#pragma unroll
+            for (int j = h * kReads; j < (h + 1) * kReads; ++j) b0[j] = read_b(then_b, j, 0);
+            rows[h] = read_a(then_a, h % MI, h / MI);
+#pragma unroll
+            for (int i = h * (B::kLoads / 4); i < (h + 1) * (B::kLoads / 4); ++i) load_b(i);
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        }
+      }
+      ready<0>();  // nothing is in flight when the workgroup goes on or ends
+    } else {
+      u32x4 va[A::kLoads], vb[B::kLoads];
+      auto fetch = [&](int s) {
+        const bool second = s >= steps1;
+        const int k0 = (second ? s - steps1 : s) * K_STEP;
+        ta.fetch(va, second ? pa1 : pa, sa, k0, K);
+        if constexpr (KIND == kGated) {
+          // LDS rows 32 to 63 of every 64 are of w_up; whole waves read one matrix
+#pragma unroll
+          for (int i = 0; i < B::kLoads; ++i) {
+            const int r = tb.lds_row + i * B::kStride, k = k0 + tb.chunk * V;
+            const char* p = ((r & 32) ? pb1 : pb) + static_cast<int64_t>(k) * ES + tb.at[i];
+            vb[i] = k + V <= K ? ldu16(p) : first_elements<DT>(p, K - k);
+          }
+        } else {
+          tb.fetch(vb, second ? pb1 : pb, sb, k0, K);
+        }
+      };
+      auto put = [&](int s) {
+        ta.put(va, (AR_LDS char*)(smem[2 * (s & 1)]));
+        tb.put(vb, (AR_LDS char*)(smem[2 * (s & 1) + 1]));
+      };
+      if (steps > 0) {
+        fetch(0);
+        put(0);
+      }
+      for (int s = 0; s < steps; ++s) {
+        __syncthreads();  // the buffer of this step is filled, and nobody reads the other one any more
+        if (s + 1 < steps) fetch(s + 1);
+        const AR_LDS char *now_a = (const AR_LDS char*)(smem[2 * (s & 1)]), *now_b = (const AR_LDS char*)(smem[2 * (s & 1) + 1]);
+        if (!none && half) simple(now_a, now_b, kHalf);
+        else if (!none) simple(now_a, now_b, kAll);
+        if (s + 1 < steps) put(s + 1);
+      }
+      __syncthreads();  // the next tile's first step goes to a buffer that slower waves may still read
     }
-    __syncthreads();  // the next tile's first step goes to the buffer that slower waves may still read
 
     // results: lane l of group q has row l of every 16 and four neighbouring columns of every subtile
 #pragma unroll
@@ -417,21 +613,24 @@ __global__ __launch_bounds__(WM* WN * 64) void tile_kernel(const ProductArgs a) 
       const int r = wm * (BM / WM) + i * 16 + l;
       if (r >= rows_left) continue;
       if constexpr (KIND == kGated) {
-        const int c = wn * 32 + q * 8, left = a.n - n0 - c;
-        if (left <= 0) continue;
-        const int64_t ofs = (static_cast<int64_t>(first + m0 + r) * a.n + n0 + c) * ES;
-        float g[8], u[8], h[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          g[k] = acc[k / 4][i][k % 4];
-          u[k] = acc[2 + k / 4][i][k % 4];
-          activate<DT, false>(a.act, g[k], &h[k], nullptr);
-          h[k] *= u[k];
-        }
-        store_run<DT, 8>(static_cast<char*>(a.c0) + ofs, h, left);
-        if (a.c1) {
-          store_run<DT, 8>(static_cast<char*>(a.c1) + ofs, g, left);
-          store_run<DT, 8>(static_cast<char*>(a.c2) + ofs, u, left);
+        for (int j = 0; j < NI; j += 4) {
+          const int c = wn * (WCOLS / 2) + j * 8 + q * 8, left = a.n - n0 - c;
+          if (left <= 0) continue;
+          const int64_t ofs = (static_cast<int64_t>(first + m0 + r) * a.n + n0 + c) * ES;
+          float g[8], u[8], h[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            g[k] = acc[j + k / 4][i][k % 4];
+            u[k] = acc[j + 2 + k / 4][i][k % 4];
+            activate<DT, false>(a.act, g[k], &h[k], nullptr);
+            h[k] *= u[k];
+          }
+          store_run<DT, 8>(static_cast<char*>(a.c0) + ofs, h, left);
+          if (a.c1) {
+            store_run<DT, 8>(static_cast<char*>(a.c1) + ofs, g, left);
+            store_run<DT, 8>(static_cast<char*>(a.c2) + ofs, u, left);
+          }
         }
       } else {
         char* out;
@@ -442,13 +641,141 @@ __global__ __launch_bounds__(WM* WN * 64) void tile_kernel(const ProductArgs a) 
         constexpr int RUN = PAIRED ? 8 : 4;
 #pragma unroll
         for (int j = 0; j < NI; j += RUN / 4) {
-          const int c = wn * 64 + n_of<PAIRED>(j, q, 0), left = a.n - n0 - c;
+          const int c = wn * WCOLS + n_of<PAIRED>(j, q, 0), left = a.n - n0 - c;
           float v[RUN];
 #pragma unroll
           for (int k = 0; k < RUN; ++k) v[k] = acc[j + k / 4][i][k % 4];
           if (left > 0) store_run<DT, RUN>(out + c * ES, v, left);
         }
       }
+    }
+  }
+}
+
+// ------------------------------------------------------------------------------------------ few rows
+// The forward products where an expert has a few rows only: bound by reading the weights once. A workgroup takes 32 rows of
+// weights (gated: 16 of either) and all of the expert's rows, 16 at a time. Its four waves split the sum in blocks of a
+// cache line (128 bytes of every row), in turn, straight into the registers that the matrix instruction takes, the next
+// block ahead of the products of this one; their sums meet in LDS. Many short workgroups keep more loads in flight than
+// 128-row tiles do where those are few. Workgroups of neighbouring columns start at different blocks: rows of a power of
+// two of bytes would have all of them read the same few memory channels at a time (8 of 64 experts, 2 x 1024 x 2048 bf16:
+// 18.2 -> 14.6 us; 8 experts, 8192 x 4096: 114 -> 95).
+constexpr int kFewThreads = 256, kFewWaves = kFewThreads / 64;
+constexpr int kUnits = 2;      // loads of a row's 64 bytes per block (4: 10% slower at 64 experts of 1024 x 1024)
+constexpr int kFirstStep = 9;  // blocks between the first ones of neighbouring workgroups
+
+template <int DT, int KIND> __global__ __launch_bounds__(kFewThreads) void few_kernel(const ProductArgs a) {
+  constexpr int ES = Traits<DT>::kSize, V = Traits<DT>::kVec, BLOCK = kUnits * 4 * V;  // elements of a block
+  constexpr int COLS = KIND == kGated ? 16 : 32;
+  __shared__ f32x4 sums[kFewWaves][2][64];
+  const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, l = lane & 15, q = lane >> 4;
+  const int across = (a.n + COLS - 1) / COLS;
+  const int total = a.most * across;  // one "tile" for each expert with rows; there may be fewer
+  const uint32_t row_bytes = static_cast<uint32_t>(a.k) * ES;
+  const int blocks = a.k / BLOCK;
+  for (int id = blockIdx.x; id < total; id += gridDim.x) {
+    Place at{};
+    if (!find_tile(a, id / across, 1, INT32_MAX, &at)) return;
+    const int n0 = id % across * COLS, cols_left = a.n - n0;
+    const char* w[2];
+    uint32_t wofs[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int row = KIND == kGated ? l : j * 16 + l;
+      w[j] = static_cast<const char*>(KIND == kGated && j ? a.b1 : a.b0) +
+             (static_cast<int64_t>(at.expert) * a.w_stride + static_cast<int64_t>(n0) * a.k) * ES;
+      wofs[j] = static_cast<uint32_t>(row < cols_left ? row : cols_left - 1) * row_bytes + q * 16;
+    }
+    const int turn = blocks > 0 ? id % across * kFirstStep % blocks : 0;
+    for (int m0 = 0; m0 < at.n; m0 += 16) {
+      const int last = at.n - m0 - 1;
+      const char* x = static_cast<const char*>(a.a0) + static_cast<int64_t>(at.first + m0) * row_bytes;
+      const uint32_t xofs = static_cast<uint32_t>(l < last ? l : last) * row_bytes + q * 16;
+      f32x4 acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+      struct Block {
+        u32x4 w[2][kUnits], x[kUnits];
+      };
+      auto load = [&](Block& f, int block) {
+        block += turn;
+        const int64_t from = static_cast<int64_t>(block >= blocks ? block - blocks : block) * (BLOCK * ES);
+#pragma unroll
+        for (int u = 0; u < kUnits; ++u) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) f.w[j][u] = ldu16(w[j] + from + wofs[j] + u * 64);
+        }
+#pragma unroll
+        for (int u = 0; u < kUnits; ++u) f.x[u] = ldu16(x + from + xofs + u * 64);
+      };
+      auto multiply = [&](const Block& f) {
+#pragma unroll
+        for (int u = 0; u < kUnits; ++u)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) acc[j] = mma<DT>(f.w[j][u], f.x[u], acc[j]);
+      };
+      Block f0, f1;
+      int b = wave;
+      if (b < blocks) load(f0, b);
+      for (; b < blocks; b += 2 * kFewWaves) {
+        if (b + kFewWaves < blocks) load(f1, b + kFewWaves);
+        multiply(f0);
+        if (b + 2 * kFewWaves < blocks) load(f0, b + 2 * kFewWaves);
+        if (b + kFewWaves < blocks) multiply(f1);
+      }
+      // what is left behind the last whole block, 64 bytes of every row or less for a wave
+      static_assert(kUnits <= kFewWaves, "a wave takes one load's worth of the rest");
+      const int rest = blocks * BLOCK + wave * 4 * V, k = rest + q * V;
+      if (rest < a.k) {
+        const int64_t from = static_cast<int64_t>(rest) * ES;
+        auto end = [&](const char* p) {
+          u32x4 v = {0, 0, 0, 0};
+          if (k + V <= a.k) v = ldu16(p);
+          else if (k < a.k) v = first_elements<DT>(p, a.k - k);
+          return v;
+        };
+        const u32x4 xt = end(x + from + xofs);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc[j] = mma<DT>(end(w[j] + from + wofs[j]), xt, acc[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) sums[wave][j][lane] = acc[j];
+      __syncthreads();
+      // results: lane l of group q has row l and four neighbouring columns of either half
+      if (wave == 0 && l <= last) {
+        f32x4 sum[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          sum[j] = sums[0][j][lane];
+#pragma unroll
+          for (int v = 1; v < kFewWaves; ++v) sum[j] += sums[v][j][lane];
+        }
+        const int64_t ofs = (static_cast<int64_t>(at.first + m0 + l) * a.n + n0) * ES;
+        if constexpr (KIND == kGated) {
+          const int c = q * 4, left = cols_left - c;
+          float g[4], u[4], h[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            g[i] = sum[0][i];
+            u[i] = sum[1][i];
+            activate<DT, false>(a.act, g[i], &h[i], nullptr);
+            h[i] *= u[i];
+          }
+          if (left > 0) {
+            store_run<DT, 4>(static_cast<char*>(a.c0) + ofs + c * ES, h, left);
+            if (a.c1) {
+              store_run<DT, 4>(static_cast<char*>(a.c1) + ofs + c * ES, g, left);
+              store_run<DT, 4>(static_cast<char*>(a.c2) + ofs + c * ES, u, left);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int c = j * 16 + q * 4, left = cols_left - c;
+            const float v[4] = {sum[j][0], sum[j][1], sum[j][2], sum[j][3]};
+            if (left > 0) store_run<DT, 4>(static_cast<char*>(a.c0) + ofs + c * ES, v, left);
+          }
+        }
+      }
+      __syncthreads();  // the sums are read before the next ones come
     }
   }
 }
@@ -461,12 +788,10 @@ template <int DT> __global__ __launch_bounds__(kSlopeThreads) void slopes_kernel
   constexpr int V = Traits<DT>::kVec, ES = Traits<DT>::kSize;
   const int total = min(all_tiles(a, a.n, kSlopeUnit), a.most);
   for (int id = blockIdx.x; id < total; id += gridDim.x) {
-    int e, t, first, n;
-    find_tile(a, id, a.n, kSlopeUnit, &e, &t);
-    segment(a, e, &first, &n);
-    const int64_t base = static_cast<int64_t>(uniform(first)) * a.n + static_cast<int64_t>(t) * kSlopeUnit;
-    const int64_t rest = static_cast<int64_t>(uniform(n)) * a.n - static_cast<int64_t>(t) * kSlopeUnit;
-    if (rest <= 0) continue;  // tables that describe no segments
+    Place at;
+    if (!find_tile(a, id, a.n, kSlopeUnit, &at)) continue;  // tables that changed meanwhile
+    const int64_t base = static_cast<int64_t>(at.first) * a.n + static_cast<int64_t>(at.index) * kSlopeUnit;
+    const int64_t rest = static_cast<int64_t>(at.n) * a.n - static_cast<int64_t>(at.index) * kSlopeUnit;
     const int len = rest < kSlopeUnit ? static_cast<int>(rest) : kSlopeUnit;
     for (int i = threadIdx.x * V; i < len; i += kSlopeThreads * V) {
       const int64_t ofs = (base + i) * ES;
@@ -502,19 +827,66 @@ template <int DT> __global__ __launch_bounds__(kSlopeThreads) void slopes_kernel
 }
 
 // ------------------------------------------------------------------------------------------ launches
+constexpr int kMostGroups = 1024;  // workgroups per compute unit and launch; what is left is taken in turn
+int64_t most_experts(const ProductArgs& a) { return !a.offsets ? 1 : a.experts < a.rows ? a.experts : a.rows; }
 int grid_of(int64_t most, int per_cu) {
   const int64_t cap = static_cast<int64_t>(cu_count()) * per_cu;
   return static_cast<int>(most < cap ? most : cap);
 }
 
-template <int DT, int KIND> hipError_t launch_tiles(ProductArgs a, hipStream_t s) {
-  constexpr int BM = 128, BN = 128, COLS = KIND == kGated ? BN / 2 : BN;
+template <int DT, int KIND, bool DIRECT, int BM, int BN, int WM, int WN>
+hipError_t launch_tile(ProductArgs a, hipStream_t s) {
+  constexpr int COLS = KIND == kGated ? BN / 2 : BN;
   const int64_t across = tiles_up(a.n, COLS);
   const int64_t down = KIND == kWeight ? matrices(a) * tiles_up(a.m, BM) : row_tiles(a, 1, BM);
   a.most = static_cast<int>(down);
   if (down == 0) return hipSuccess;
-  tile_kernel<DT, KIND, BM, BN, 2, 2><<<grid_of(down * across, 2), 256, 0, s>>>(a);
+  tile_kernel<DT, KIND, DIRECT, BM, BN, WM, WN><<<grid_of(down * across, kMostGroups), WM * WN * 64, 0, s>>>(a);
   return hipGetLastError();
+}
+
+// Whether all rows and addresses are multiples of 16 bytes, which loads straight into LDS take.
+bool in_vectors(const ProductArgs& a, int kind, int esize) {
+  const int64_t v = 16 / esize;
+  uintptr_t p = 0;
+  for (const void* x : {a.a0, a.a1, a.b0, a.b1}) p |= reinterpret_cast<uintptr_t>(x);
+  const int64_t in = kind == kWeight ? a.m : a.k, cols = kind == kInput || kind == kWeight ? a.n : 0;
+  const int64_t apart = kind == kWeight || a.experts == 1 ? 0 : a.w_stride;
+  return p % 16 == 0 && in % v == 0 && cols % v == 0 && apart % v == 0;
+}
+
+template <int DT, int KIND> hipError_t launch_few(ProductArgs a, hipStream_t s) {
+  a.most = most_experts(a);
+  const int64_t across = tiles_up(a.n, KIND == kGated ? 16 : 32);
+  few_kernel<DT, KIND><<<grid_of(a.most * across, kMostGroups), kFewThreads, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+// Which kernel. The host knows rows and experts, not how the rows are spread.
+//   Few rows (forward products, up to 8 an expert) where 128-row tiles would leave the GPU short of workgroups: few_kernel.
+//     One dense matrix of 4096 x 4096, bf16, 1 to 16 rows: 12-15 us against 33; 8 of 64 experts, gated 2 x 1024 x 2048:
+//     14.3 / 27; 8 experts, gated 2 x 8192 x 4096, 1 to 8 rows each (1024 tiles): 177-185 / 243; but 64 experts of 1024 x
+//     1024 with 16 rows: 30 / 29 (gated 60 / 56), and 48 tokens x 4 of 128 experts, where some experts have many rows:
+//     76 / 55 (4096 tiles).
+//   256 x 256 tiles (16-bit types): half the reads of the operands, but one workgroup a CU. From 192 rows an expert and
+//     three tiles for four CUs on. 16 experts of 2048 x 2048, bf16: 128 rows each, gated 76 us with small tiles / 81 with
+//     large ones; 256 rows 104 / 87, linear (128 large tiles) 54 / 60; 1024 rows 338 / 248. Gradients of weights write
+//     more than they multiply when rows are few, and take large tiles whenever there are enough: 16 x 2048 x 2048, 1 row
+//     58 / 48, 128 rows 75 / 66, 1024 rows 195 / 157; one of 4096 x 4096, 1024 rows 48 / 38.
+constexpr int kFewRows = 8;
+template <int DT, int KIND> hipError_t launch_tiles(const ProductArgs& a, hipStream_t s) {
+  constexpr int COLS = KIND == kGated ? 64 : 128;
+  if constexpr (KIND == kGated || KIND == kLinear) {
+    if (a.rows <= static_cast<int64_t>(kFewRows) * a.experts && most_experts(a) * tiles_up(a.n, COLS) <= 4 * cu_count())
+      return launch_few<DT, KIND>(a, s);
+  }
+  if (!in_vectors(a, KIND, Traits<DT>::kSize)) return launch_tile<DT, KIND, false, 128, 128, 2, 2>(a, s);
+  if constexpr (Traits<DT>::kSize == 2) {
+    const int64_t down = KIND == kWeight ? matrices(a) * tiles_up(a.m, 256) : a.rows / 256;
+    const bool high = KIND == kWeight || a.rows >= 192 * static_cast<int64_t>(a.experts);
+    if (high && down * tiles_up(a.n, 2 * COLS) * 4 >= 3 * cu_count()) return launch_tile<DT, KIND, true, 256, 256, 2, 4>(a, s);
+  }
+  return launch_tile<DT, KIND, true, 128, 128, 2, 2>(a, s);
 }
 
 template <int KIND> hipError_t launch_kind(const ProductArgs& a, int dtype, hipStream_t s) {

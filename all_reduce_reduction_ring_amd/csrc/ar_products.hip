@@ -131,9 +131,11 @@ template <int CH, bool PAIRED> __device__ __forceinline__ int mix_kc(int row) {
   const int t = PAIRED ? row >> 3 : row >> 2;
   return ((t >> 1) & 1) | ((t ^ (t >> 1)) & 1) << 1;
 }
-template <int DT> __device__ __forceinline__ int mix_ks(int k) {
-  if constexpr (Traits<DT>::kSize == 2) return ((k & 3) << 1) | (k & 8);
-  else return k & 12;
+//   KS with 128-byte LDS rows: two of them share a bank row, and 8 chunks are there to exchange.
+template <int DT, int R> __device__ __forceinline__ int mix_ks(int k) {
+  if constexpr (Traits<DT>::kSize == 4) return k & 12;
+  else if constexpr (R * 2 >= 256) return ((k & 3) << 1) | (k & 8);
+  else return (k & 2) | ((k & 8) >> 1);
 }
 
 // The column (0 to 63 of a wave's 64) of result element i of lane group q in subtile j. KS operands: in order. KC operands:
@@ -144,7 +146,7 @@ template <bool PAIRED> __device__ __forceinline__ int n_of(int j, int q, int i) 
 
 // 16 bytes per lane from memory straight into LDS: lane l's go to `lds` (uniform, an LDS byte address) + 16 l. `base` and
 // `bytes` are uniform too; a lane whose offset reaches `bytes` gets zeros. Nothing waits here (see ready).
-constexpr uint32_t kNowhere = 0x80000000u, kMostBytes = 0x7FFFFFF0u;
+constexpr uint32_t kNowhere = 0x80000000u;
 __device__ __forceinline__ void load_lds(const char* base, uint32_t bytes, uint32_t at, uint32_t lds) {
   const uint64_t b = reinterpret_cast<uint64_t>(base);
   auto scalar = [](uint32_t v) { return static_cast<uint32_t>(uniform(static_cast<int>(v))); };
@@ -170,7 +172,7 @@ template <int DT> __device__ __forceinline__ u32x4 first_elements(const char* p,
 }
 
 // One operand's tile of R rows and CH chunks of the sum, for NT threads: from memory through registers into LDS, or (DIRECT)
-// straight into it, for rows and addresses that are multiples of 16 bytes.
+// straight into it, for rows and addresses that are multiples of 4 bytes.
 template <int DT, bool KS, bool PAIRED, bool DIRECT, int CH, int R, int NT> struct Tile {
   static constexpr int V = Traits<DT>::kVec, ES = Traits<DT>::kSize;
   static constexpr int kRowChunks = KS ? R / V : CH;           // chunks of an LDS row
@@ -199,16 +201,30 @@ template <int DT, bool KS, bool PAIRED, bool DIRECT, int CH, int R, int NT> stru
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
         const int k = lds_row + i * kStride;
-        at[i] = static_cast<uint32_t>(k) * stride + (static_cast<uint32_t>(tid % kRowChunks) ^ mix_ks<DT>(k)) * 16;
+        at[i] = static_cast<uint32_t>(k) * stride + (static_cast<uint32_t>(tid % kRowChunks) ^ mix_ks<DT, R>(k)) * 16;
       }
     }
   }
 
   // Load i of a step of the sum straight into LDS. `base` is the matrix at the tile's first row and the step's first element;
-  // lanes whose chunk is not `in` the sum (KC) or lies `bytes` or more behind base (KS: the rest of the matrix) leave zeros.
-  // (KS: a chunk past a row's end reads the next row's start, whose results go nowhere, and nothing past the matrix.)
+  // what lies `bytes` or more behind it, and (KC) chunks that are not `in` the sum, leave zeros. (KS: a chunk past a row's
+  // end reads the start of the next ones, whose results go nowhere.)
   __device__ __forceinline__ void load(int i, const char* base, uint32_t bytes, bool in, uint32_t to) const {
     load_lds(base, bytes, KS || in ? at[i] : kNowhere, to + i * NT * 16);
+  }
+
+  // KC: zeros for the elements of the chunk that the end of the sum cuts, `n` elements into the step: their loads brought the
+  // next row's first ones.
+  __device__ __forceinline__ static void cut(AR_LDS char* lds, int n) {
+    static_assert(!KS, "across the sum, whole rows are left out");
+#pragma unroll
+    for (int row = threadIdx.x; row < R; row += NT) {
+      AR_LDS char* p = lds + row * (CH * 16) + ((n / V) ^ mix_kc<CH, PAIRED>(row)) * 16;
+      for (int e = n % V; e < V; ++e) {
+        if constexpr (ES == 2) ((AR_LDS uint16_t*)p)[e] = 0;
+        else ((AR_LDS uint32_t*)p)[e] = 0;
+      }
+    }
   }
 
   // Reads the step of the sum that starts `k0` elements in: `base` is the matrix at the tile's first row and sum element
@@ -226,7 +242,7 @@ template <int DT, bool KS, bool PAIRED, bool DIRECT, int CH, int R, int NT> stru
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
         const int row = lds_row + i * kStride, k = k0 + row;
-        const int c = ((static_cast<int>(threadIdx.x) % kRowChunks) ^ mix_ks<DT>(row)) * V;
+        const int c = ((static_cast<int>(threadIdx.x) % kRowChunks) ^ mix_ks<DT, R>(row)) * V;
         const char* p = base + static_cast<int64_t>(k) * stride + c * ES;
         if (k < K && c + V <= limit) v[i] = ldu16(p);
         else v[i] = first_elements<DT>(p, k < K ? limit - c : 0);
@@ -247,7 +263,7 @@ template <int DT, bool KS, bool PAIRED, bool DIRECT, int CH, int R, int NT> stru
       return *(const AR_LDS u32x4*)(lds + row * (CH * 16) + (((kk * 4 + q) ^ mix_kc<CH, PAIRED>(row)) * 16));
     } else if constexpr (ES == 2) {
       const int k = kk * 32 + q * 8 + (l >> 2), c = r0 + (l & 3) * 4;
-      const AR_LDS char* p = lds + k * (R * ES) + (((c / V) ^ mix_ks<DT>(k)) * 16) + (c % V) * ES;
+      const AR_LDS char* p = lds + k * (R * ES) + (((c / V) ^ mix_ks<DT, R>(k)) * 16) + (c % V) * ES;
       const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((AR_LDS i16x4*)(p));
       const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((AR_LDS i16x4*)(p + 4 * R * ES));
       return __builtin_bit_cast(u32x4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
@@ -256,7 +272,7 @@ template <int DT, bool KS, bool PAIRED, bool DIRECT, int CH, int R, int NT> stru
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int k = kk * 16 + q * 4 + i, c = r0 + l;
-        w[i] = *(const AR_LDS uint32_t*)(lds + k * (R * ES) + (((c / V) ^ mix_ks<DT>(k)) * 16) + (c % V) * ES);
+        w[i] = *(const AR_LDS uint32_t*)(lds + k * (R * ES) + (((c / V) ^ mix_ks<DT, R>(k)) * 16) + (c % V) * ES);
       }
       return w;
     }
@@ -335,15 +351,20 @@ __device__ __forceinline__ void raster(int t, int down, int across, int* row, in
   *row = group * kRaster + in - *col * high;
 }
 
-template <int DT, int KIND, bool DIRECT, int BM, int BN, int WM, int WN>
+// How operands come into LDS: through registers; straight, in whole 16-byte chunks of the sum; or straight, with the chunk
+// that the end of the sum cuts mended in LDS (which costs the large tiles registers that they do not have).
+enum Loads { kRegisters = 0, kWhole = 1, kCut = 2 };
+
+template <int DT, int KIND, int LOADS, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(WM* WN * 64) void tile_kernel(const ProductArgs a) {
+  constexpr bool DIRECT = LOADS != kRegisters;
   // chunks of the sum per step, and steps that LDS holds
   constexpr int CH = 8, PLACES = DIRECT ? 5 : 4;  // chunks of the sum per step; operand tiles that LDS holds
   constexpr int NT = WM * WN * 64, ES = Traits<DT>::kSize, V = 16 / ES, K_STEP = CH * V;
   constexpr int MI = BM / WM / 16, NI = BN / WN / 16;
   constexpr bool PAIRED = !kColsKS<KIND>;
   constexpr int WCOLS = BN / WN;  // a wave's columns, in blocks of 64
-  static_assert(WCOLS % 64 == 0 && MI % 2 == 0, "whole blocks");
+  static_assert(WCOLS % 64 == 0 && MI * 16 * WM == BM, "whole blocks");
   constexpr int COLS = KIND == kGated ? BN / 2 : BN;  // columns of the result
   using A = Tile<DT, kRowsKS<KIND>, false, DIRECT, CH, BM, NT>;
   using B = Tile<DT, kColsKS<KIND>, PAIRED, DIRECT, CH, BN, NT>;
@@ -429,14 +450,15 @@ __global__ __launch_bounds__(WM* WN * 64) void tile_kernel(const ProductArgs a) 
 
     // A wave's part of the tile may lie wholly or in its second half past the result: it is not computed there.
     const int rows_wave = rows_left - wm * (BM / WM);
-    const bool none = rows_wave <= 0 || cols_left <= wn * (KIND == kGated ? WCOLS / 2 : WCOLS), half = rows_wave <= BM / WM / 2;
+    const bool none = rows_wave <= 0 || cols_left <= wn * (KIND == kGated ? WCOLS / 2 : WCOLS), half = MI > 1 && rows_wave <= BM / WM / 2;
     auto read_a = [&](const AR_LDS char* at, int i, int kk) { return A::read(at, wm * (BM / WM) + i * 16, kk); };
     auto read_b = [&](const AR_LDS char* at, int j, int kk) { return B::read(at, wn * WCOLS + j * 16, kk); };
-    // the products of one step, for the first `N` of the wave's MI times 16 rows
-    auto simple = [&](const AR_LDS char* at_a, const AR_LDS char* at_b, auto N) {
+    // the products of one step, for the first `count` of the wave's MI times 16 rows
+    auto simple = [&](const AR_LDS char* at_a, const AR_LDS char* at_b, auto count) {
+      constexpr int N = decltype(count)::value;
 #pragma unroll
-      for (int kk = 0; kk < CH / 4; ++kk) {
-        u32x4 fb[NI], fa[N];
+      for (int kk = 0; kk < (N > 0 ? CH / 4 : 0); ++kk) {
+        u32x4 fb[NI], fa[N > 0 ? N : 1];
 #pragma unroll
         for (int j = 0; j < NI; ++j) fb[j] = read_b(at_b, j, kk);
 #pragma unroll
@@ -449,6 +471,7 @@ __global__ __launch_bounds__(WM* WN * 64) void tile_kernel(const ProductArgs a) 
     };
     constexpr std::integral_constant<int, MI> kAll{};
     constexpr std::integral_constant<int, MI / 2> kHalf{};
+    constexpr std::integral_constant<int, 0> kNone{};
     if constexpr (DIRECT) {
       // A step's products go in groups of NI, 16 rows and 4 chunks each. Fragments of rows are read four groups ahead, so
       // that the last four groups of a step need nothing more from LDS: before them all waves meet, the next step has
@@ -461,37 +484,47 @@ __global__ __launch_bounds__(WM* WN * 64) void tile_kernel(const ProductArgs a) 
       AR_LDS char* const places = (AR_LDS char*)(smem[0]);
       const uint32_t to_wave = uniform(static_cast<int>(reinterpret_cast<uintptr_t>(places))) + wave * 1024;
       auto advance = [](int& place) { place = place >= PLACES - 2 ? place - (PLACES - 2) : place + 2; };
-      // What a load of a step may read: KS, in a product's last step, the rest of the matrix. Nothing behind the last step;
-      // loads are issued then too, so that their number in flight stays the same.
-      const uint32_t rest_a = static_cast<uint32_t>(K - (steps1 - 1) * K_STEP) * sa - static_cast<uint32_t>(m0) * ES;
-      const uint32_t rest_b = static_cast<uint32_t>(K - (steps1 - 1) * K_STEP) * sb - static_cast<uint32_t>(n0) * ES;
-      auto bytes = [&](bool ks, uint32_t rest, int step) {
-        const bool last = step + 1 == steps1 || step + 1 == steps;
-        return step >= steps ? 0u : ks && last ? rest : kMostBytes;
-      };
       int next_a = 0, next_b = 0, ka = 0, kb = 0, to_a = 0, to_b = 1;  // the steps to load, their first elements, places
+      // What the loads of a step may read from its base on; nothing behind the last step, where loads are issued too, so
+      // that their number in flight stays the same.
+      const int high = rows_left < BM ? rows_left : BM, wide = cols_left < COLS ? cols_left : COLS;
+      int64_t left_a = kRowsKS<KIND> ? across_left(K, 0, sa, m0, ES) : along_left(high, sa, K, 0, ES);
+      int64_t left_b = kColsKS<KIND> ? across_left(K, 0, sb, n0, ES) : along_left(wide, sb, K, 0, ES);
+      const int64_t again_a = left_a, again_b = left_b;
+      uint32_t bytes_a = 0, bytes_b = 0;
+      auto allowed = [&](int64_t left, int step) {
+        // the upper half apart: a comparison of 64 bits is none for scalar registers
+        const uint32_t b = load_bytes(uniform(static_cast<int>(left >> 32)), static_cast<uint32_t>(left));
+        return step < steps ? b : 0;
+      };
       auto load_a = [&](int i) {
-        ta.load(i, pa, bytes(kRowsKS<KIND>, rest_a, next_a), ka + ta.chunk * V < K, to_wave + to_a * kPlace);
+        if (i == 0) bytes_a = allowed(left_a, next_a);
+        ta.load(i, pa, bytes_a, ka + ta.chunk * V < K, to_wave + to_a * kPlace);
         if (i + 1 < A::kLoads) return;
         pa += step_a;
+        left_a -= step_a;
         ka += K_STEP;
         if (KIND == kInput && ++next_a == steps1) {  // on to the second product of the sum
           pa = pa1;
+          left_a = again_a;
           ka = 0;
         }
         if (KIND != kInput) ++next_a;
         advance(to_a);
       };
       auto load_b = [&](int i) {
+        if (i == 0) bytes_b = allowed(left_b, next_b);
         // gated: LDS rows 32 to 63 of every 64 are of w_up; whole waves read one matrix
         const bool of_up = KIND == kGated && ((wave * (64 / CH) + i * B::kStride) & 32) != 0;
-        tb.load(i, of_up ? pb1 : pb, bytes(kColsKS<KIND>, rest_b, next_b), kb + tb.chunk * V < K, to_wave + to_b * kPlace);
+        tb.load(i, of_up ? pb1 : pb, bytes_b, kb + tb.chunk * V < K, to_wave + to_b * kPlace);
         if (i + 1 < B::kLoads) return;
         pb += step_b;
         if (KIND == kGated) pb1 += step_b;
+        left_b -= step_b;
         kb += K_STEP;
         if (KIND == kInput && ++next_b == steps1) {
           pb = pb1;
+          left_b = again_b;
           kb = 0;
         }
         if (KIND != kInput) ++next_b;
@@ -506,22 +539,40 @@ __global__ __launch_bounds__(WM* WN * 64) void tile_kernel(const ProductArgs a) 
         for (int i = 0; i < B::kLoads; ++i) load_b(i);
       };
       int at_a = 0, at_b = 1;
+      // The chunk that a product's end cuts, once its last step has arrived.
+      const int cut_at = K - (steps1 - 1) * K_STEP;
+      auto cut_last = [&](int step) {
+        if (KIND == kWeight || LOADS != kCut || cut_at % V == 0 || (step + 1 != steps1 && step + 1 != steps)) return;
+        if constexpr (!kRowsKS<KIND>) A::cut(places + at_a * kPlace, cut_at);
+        if constexpr (!kColsKS<KIND>) B::cut(places + at_b * kPlace, cut_at);
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      };
       if (steps > 0) {
         all_a();
         all_b();
         all_a();
         ready<A::kLoads>();
         all_b();
+        cut_last(0);
       }
-      if (none || half) {
+      // Steps in which a wave multiplies `count` times 16 rows, one fragment after the other.
+      auto plain_steps = [&](auto count) {
         for (int s = 0; s < steps; ++s) {
           all_a();
-          if (!none) simple(places + at_a * kPlace, places + at_b * kPlace, kHalf);
+          simple(places + at_a * kPlace, places + at_b * kPlace, count);
           advance(at_a);
           advance(at_b);
           ready<A::kLoads>();
+          cut_last(s + 1);
           all_b();
         }
+      };
+      if (none) {
+        plain_steps(kNone);
+      } else if (half) {
+        plain_steps(kHalf);
+      } else if constexpr (kGroups < 8) {
+        plain_steps(kAll);
       } else if (steps > 0) {
         u32x4 b0[NI], b1[NI], rows[4];
 #pragma unroll
@@ -557,6 +608,7 @@ __global__ __launch_bounds__(WM* WN * 64) void tile_kernel(const ProductArgs a) 
             __builtin_amdgcn_sched_barrier(0);
           }
           ready<A::kLoads>();
+          cut_last(s + 1);
 #pragma unroll
           for (int h = 0; h < 4; ++h) {
             group(kGroups - 4 + h, b1);
@@ -834,25 +886,25 @@ int grid_of(int64_t most, int per_cu) {
   return static_cast<int>(most < cap ? most : cap);
 }
 
-template <int DT, int KIND, bool DIRECT, int BM, int BN, int WM, int WN>
+template <int DT, int KIND, int LOADS, int BM, int BN, int WM, int WN>
 hipError_t launch_tile(ProductArgs a, hipStream_t s) {
   constexpr int COLS = KIND == kGated ? BN / 2 : BN;
   const int64_t across = tiles_up(a.n, COLS);
   const int64_t down = KIND == kWeight ? matrices(a) * tiles_up(a.m, BM) : row_tiles(a, 1, BM);
   a.most = static_cast<int>(down);
   if (down == 0) return hipSuccess;
-  tile_kernel<DT, KIND, DIRECT, BM, BN, WM, WN><<<grid_of(down * across, kMostGroups), WM * WN * 64, 0, s>>>(a);
+  tile_kernel<DT, KIND, LOADS, BM, BN, WM, WN><<<grid_of(down * across, kMostGroups), WM * WN * 64, 0, s>>>(a);
   return hipGetLastError();
 }
 
-// Whether all rows and addresses are multiples of 16 bytes, which loads straight into LDS take.
-bool in_vectors(const ProductArgs& a, int kind, int esize) {
-  const int64_t v = 16 / esize;
+// Whether all rows and addresses are multiples of 4 bytes, which loads straight into LDS take.
+bool in_words(const ProductArgs& a, int kind, int esize) {
+  const int64_t v = 4 / esize;
   uintptr_t p = 0;
   for (const void* x : {a.a0, a.a1, a.b0, a.b1}) p |= reinterpret_cast<uintptr_t>(x);
   const int64_t in = kind == kWeight ? a.m : a.k, cols = kind == kInput || kind == kWeight ? a.n : 0;
   const int64_t apart = kind == kWeight || a.experts == 1 ? 0 : a.w_stride;
-  return p % 16 == 0 && in % v == 0 && cols % v == 0 && apart % v == 0;
+  return p % 4 == 0 && in % v == 0 && cols % v == 0 && apart % v == 0;
 }
 
 template <int DT, int KIND> hipError_t launch_few(ProductArgs a, hipStream_t s) {
@@ -862,31 +914,44 @@ template <int DT, int KIND> hipError_t launch_few(ProductArgs a, hipStream_t s) 
   return hipGetLastError();
 }
 
-// Which kernel. The host knows rows and experts, not how the rows are spread.
-//   Few rows (forward products, up to 8 an expert) where 128-row tiles would leave the GPU short of workgroups: few_kernel.
-//     One dense matrix of 4096 x 4096, bf16, 1 to 16 rows: 12-15 us against 33; 8 of 64 experts, gated 2 x 1024 x 2048:
-//     14.3 / 27; 8 experts, gated 2 x 8192 x 4096, 1 to 8 rows each (1024 tiles): 177-185 / 243; but 64 experts of 1024 x
-//     1024 with 16 rows: 30 / 29 (gated 60 / 56), and 48 tokens x 4 of 128 experts, where some experts have many rows:
-//     76 / 55 (4096 tiles).
-//   256 x 256 tiles (16-bit types): half the reads of the operands, but one workgroup a CU. From 192 rows an expert and
-//     three tiles for four CUs on. 16 experts of 2048 x 2048, bf16: 128 rows each, gated 76 us with small tiles / 81 with
-//     large ones; 256 rows 104 / 87, linear (128 large tiles) 54 / 60; 1024 rows 338 / 248. Gradients of weights write
-//     more than they multiply when rows are few, and take large tiles whenever there are enough: 16 x 2048 x 2048, 1 row
-//     58 / 48, 128 rows 75 / 66, 1024 rows 195 / 157; one of 4096 x 4096, 1024 rows 48 / 38.
-constexpr int kFewRows = 8;
+// Which kernel. The host knows rows and experts, not how the rows are spread. (bf16, one MI355X, rows for each expert.)
+//   Few rows (forward products: up to 16 of a dense matrix, 8 an expert on average) where 128-wide tiles would leave the
+//     GPU short of workgroups: few_kernel. One of 4096 x 4096, 1 to 16 rows: 12-15 us against 27 with 64 x 64 tiles and 33
+//     with 128 x 128; 8 of 64 experts, gated 2 x 1024 x 2048: 14.3 / 24 / 27; 8 experts, gated 2 x 8192 x 4096, 1 to 8 rows
+//     (1024 tiles): 179-185 / 235 / 232; but 64 of 1024 x 1024, 16 rows: 31 / 29 / 29, and 48 tokens x 4 to 128 experts of
+//     4096 x 1024, where some have many rows: 75 / 55 / 56 (4096 tiles).
+//   256 x 256 tiles (16-bit types, whole chunks): half the reads of the operands, but one workgroup a CU. From 192 rows an
+//     expert and three tiles for four CUs on. 16 of 2048 x 2048: 128 rows, gated 75 us with 128 x 128 tiles / 81 with
+//     256 x 256; 256 rows 112 / 86, linear (128 large tiles) 53 / 58; 1024 rows 329 / 249. Gradients of weights write more
+//     than they multiply when rows are few, and take large tiles whenever there are enough: 16 of 2048 x 2048, 1 row
+//     56 / 50, 1024 rows 191 / 142; one of 4096 x 4096, 1024 rows 47 / 36.
+//   64 x 64 tiles where there is not one of 128 x 128 for each CU: one of 4096 x 4096, 128 rows 28 / 48, 1024 rows (256
+//     tiles) 57 / 55; 32 of 512 x 512, 128 rows 9.3 / 12.5; 16 of 2048 x 2048, 128 rows (256 tiles) 54 / 44.
+template <int DT, int KIND, int LOADS> hipError_t launch_small(const ProductArgs& a, bool least, hipStream_t s) {
+  if (least) return launch_tile<DT, KIND, LOADS, 64, 64, 4, 1>(a, s);
+  return launch_tile<DT, KIND, LOADS, 128, 128, 2, 2>(a, s);
+}
+
 template <int DT, int KIND> hipError_t launch_tiles(const ProductArgs& a, hipStream_t s) {
-  constexpr int COLS = KIND == kGated ? 64 : 128;
+  constexpr int COLS = KIND == kGated ? 64 : 128, V = Traits<DT>::kVec;
+  const int64_t cus = cu_count(), across = tiles_up(a.n, COLS);
   if constexpr (KIND == kGated || KIND == kLinear) {
-    if (a.rows <= static_cast<int64_t>(kFewRows) * a.experts && most_experts(a) * tiles_up(a.n, COLS) <= 4 * cu_count())
+    if (a.rows <= (a.offsets ? 8 * static_cast<int64_t>(a.experts) : 16) && most_experts(a) * across <= 4 * cus)
       return launch_few<DT, KIND>(a, s);
   }
-  if (!in_vectors(a, KIND, Traits<DT>::kSize)) return launch_tile<DT, KIND, false, 128, 128, 2, 2>(a, s);
+  const int64_t down = KIND == kWeight ? matrices(a) * tiles_up(a.m, 128) : tiles_up(a.rows, 128);
+  const bool least = down * across < cus, whole = KIND == kWeight || a.k % V == 0;
   if constexpr (Traits<DT>::kSize == 2) {
-    const int64_t down = KIND == kWeight ? matrices(a) * tiles_up(a.m, 256) : a.rows / 256;
-    const bool high = KIND == kWeight || a.rows >= 192 * static_cast<int64_t>(a.experts);
-    if (high && down * tiles_up(a.n, 2 * COLS) * 4 >= 3 * cu_count()) return launch_tile<DT, KIND, true, 256, 256, 2, 4>(a, s);
+    if (!in_words(a, KIND, 2)) return launch_tile<DT, KIND, kRegisters, 128, 128, 2, 2>(a, s);
+    const int64_t large = KIND == kWeight ? matrices(a) * tiles_up(a.m, 256) : a.rows / 256;
+    if (whole && (KIND == kWeight || a.rows >= 192 * static_cast<int64_t>(a.experts)) &&
+        large * tiles_up(a.n, 2 * COLS) * 4 >= 3 * cus)
+      return launch_tile<DT, KIND, kWhole, 256, 256, 2, 4>(a, s);
   }
-  return launch_tile<DT, KIND, true, 128, 128, 2, 2>(a, s);
+  if constexpr (KIND != kWeight) {
+    if (!whole || Traits<DT>::kSize == 4) return launch_small<DT, KIND, kCut>(a, least, s);
+  }
+  if constexpr (KIND == kWeight || Traits<DT>::kSize == 2) return launch_small<DT, KIND, kWhole>(a, least, s);
 }
 
 template <int KIND> hipError_t launch_kind(const ProductArgs& a, int dtype, hipStream_t s) {

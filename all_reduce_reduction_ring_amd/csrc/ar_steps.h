@@ -29,4 +29,21 @@ constexpr int kChoices = 8;
 using sorted_row_t = uint32_t;
 constexpr int kPadLanes = 16;
 
+// The experts' products load operand tiles in chunks of 16 bytes, also where a chunk runs past a row's end or a row lies past
+// the matrix; a load stops at the number of bytes that it is given, so that number has to be exact. From a tile's base on,
+// the matrix at its first row (or column) and the step's first element k of a sum of `sum`:
+//   along the sum (rows of a tile lie `stride` bytes apart, all of them in the matrix): up to the end of the last of `rows`
+//   across it (every element of the sum is a row of `stride` bytes, the tile starts at element `first` of it): the rest
+constexpr int64_t along_left(int rows, uint32_t stride, int sum, int k, int size) {
+  return static_cast<int64_t>(rows - 1) * stride + static_cast<int64_t>(sum - k) * size;
+}
+constexpr int64_t across_left(int sum, int k, uint32_t stride, int first, int size) {
+  return static_cast<int64_t>(sum - k) * stride - static_cast<int64_t>(first) * size;
+}
+// As a load takes it, from its two halves. Tiles stay below 2^31 bytes, so more than that need not be told apart.
+constexpr uint32_t kMostLoadBytes = 0x7FFFFFF0u;
+constexpr uint32_t load_bytes(uint32_t high, uint32_t low) {
+  return high != 0 ? kMostLoadBytes : low < kMostLoadBytes ? low : kMostLoadBytes;
+}
+
 }  // namespace ar

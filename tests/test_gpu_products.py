@@ -235,3 +235,41 @@ def test_small_numbers_are_kept():
     w, y = torch.full((16, 64), 16.0, dtype=torch.float16, device=DEV), torch.empty(2, 16, dtype=torch.float16, device=DEV)
     ar.ar_expert_linear(tiny, w, y)
     assert (y == 2.0 ** -10).all()
+
+
+# widths at which an operand's rows are multiples of 16 bytes, of 4, and of neither, on either side of a step's and a tile's
+# end; lengths of the sum over one, two and several steps
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("hidden,inner", [(64, 66), (66, 64), (126, 130), (62, 58), (190, 258), (258, 190), (129, 127), (322, 34),
+                                          (2, 200), (200, 2), (4, 6)])
+def test_widths_around_a_step(hidden, inner, dtype):
+    counts = [130, 0, 1, 17, 65]
+    c, dt = make(hidden, inner, counts, 1, dtype, seed=11), DT[dtype]
+    x, wg, wu, dy = c["row"](hidden), c["mat"](inner, hidden), c["mat"](inner, hidden), c["row"](inner)
+    out, gate, up, dgate, dup = (c["new"](inner) for _ in range(5))
+    dxs, dwg, dwu, dx1 = c["new"](hidden), torch.empty_like(wg), torch.empty_like(wu), c["new"](hidden)
+    ar.ar_expert_gated(x, wg, wu, out, gate=gate, up=up, **c["seg"])
+    ar.ar_expert_gated_bwd(dy, gate, up, x, wg, wu, dgate, dup, dxs=dxs, dw_gate=dwg, dw_up=dwu, **c["seg"])
+    ar.ar_expert_linear_bwd(dy, x, wg, dxs=dx1, **c["seg"])
+    untouched(c, out, gate, up, dgate, dup, dxs, dx1)
+    for e, rows in c["spans"]:
+        ref.close(out[rows], *ref.gated(x[rows], wg[e], wu[e], ar.AR_ACT_SILU, dt)[0], "out")
+        both = torch.cat([dgate[rows], dup[rows]], 1), torch.cat([wg[e], wu[e]], 0)
+        ref.close(dxs[rows], *ref.rounded(ref.mm(*both), dt), "dxs")
+        ref.close(dx1[rows], *ref.rounded(ref.mm(dy[rows], wg[e]), dt), "dxs of one projection")
+        ref.close(dwu[e], *ref.rounded(ref.mm(dup[rows].t(), x[rows]), dt), "dw_up")
+
+
+@pytest.mark.parametrize("rows,hidden,inner", [(128, 2046, 2050), (300, 2050, 2046), (20, 1022, 6)])
+def test_matrices_at_the_end_of_their_memory(rows, hidden, inner):
+    """Weights that end a few bytes before a 2 MiB boundary, rows that are no multiples of 16 bytes, narrow matrices: no load
+    runs past them."""
+    c, dt = make(hidden, inner, [rows], 1, "bf16", dense=True, seed=12), torch.bfloat16
+    x, wg, wu, dy = c["row"](hidden), c["mat"](inner, hidden)[0], c["mat"](inner, hidden)[0], c["row"](inner)
+    out, gate, up, dgate, dup = (c["new"](inner) for _ in range(5))
+    dxs, dwg, dwu = c["new"](hidden), torch.empty_like(wg), torch.empty_like(wu)
+    ar.ar_expert_gated(x, wg, wu, out, gate=gate, up=up)
+    ar.ar_expert_gated_bwd(dy, gate, up, x, wg, wu, dgate, dup, dxs=dxs, dw_gate=dwg, dw_up=dwu)
+    ref.close(out, *ref.gated(x, wg, wu, ar.AR_ACT_SILU, dt)[0], "out")
+    ref.close(dxs, *ref.rounded(ref.mm(torch.cat([dgate, dup], 1), torch.cat([wg, wu], 0)), dt), "dxs")
+    ref.close(dwg, *ref.rounded(ref.mm(dgate.t(), x), dt), "dw_gate")

@@ -467,6 +467,9 @@ def _load_native():
         from . import _marshal
         entries = (L.ar_allreduce_rmsnorm, L.ar_allreduce_rmsnorm_bwd, L.ar_expert_sort, L.ar_expert_dispatch,
                    L.ar_expert_combine, L.ar_expert_combine_bwd)
+        products = (L.ar_expert_gated, L.ar_expert_gated_bwd, L.ar_expert_linear, L.ar_expert_linear_bwd, L.ar_grad_norm,
+                    L.ar_grad_clip)
+        _marshal.bind_products(*(ctypes.cast(f, ctypes.c_void_p).value for f in products))
         _marshal.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in entries), torch._C._cuda_getDevice,
                       torch._C._cuda_getCurrentRawStream)
         _native = _marshal
@@ -785,6 +788,9 @@ def ar_expert_gated(xs, w_gate, w_up, out, offsets=None, counts=None, gate=None,
     [experts, inner, hidden] (without segments also [inner, hidden]) may be parts of one tensor, such as w[:, :inner] and
     w[:, inner:]. gate, up [rows, inner] receive the two products for ar_expert_gated_bwd. Rows outside the segments are
     neither read nor written."""
+    native = _native if _native is not None else _load_native()
+    if native and _done(native.expert_gated(xs, w_gate, w_up, out, offsets, counts, gate, up, act, stream), "ar_expert_gated"):
+        return
     shape, dt, dev = _matrix(xs, "xs")
     if out.dim() != 2:
         raise ValueError("out must be a matrix [rows, inner]")
@@ -808,6 +814,10 @@ def ar_expert_gated_bwd(dout, gate, up, xs, w_gate, w_up, dgate, dup, dxs=None, 
     and dup [rows, inner] (either may be dout, gate or up), and of these dxs [rows, hidden] (None: not wanted; w_gate and
     w_up may then be None) and the weights' gradients dw_gate, dw_up [experts, inner, hidden] (None: not wanted; xs may
     then be None), which may be parts of one tensor as the weights may."""
+    native = _native if _native is not None else _load_native()
+    if native and _done(native.expert_gated_bwd(dout, gate, up, xs, w_gate, w_up, dgate, dup, dxs, dw_gate, dw_up, offsets, counts,
+                                               act, stream), "ar_expert_gated_bwd"):
+        return
     wide, dt, dev = _matrix(dout, "dout")
     rows, inner = wide
     known = [t for t in (xs, dxs) if t is not None]
@@ -843,6 +853,9 @@ def ar_expert_gated_bwd(dout, gate, up, xs, w_gate, w_up, dgate, dup, dxs=None, 
 def ar_expert_linear(xs, w, out, offsets=None, counts=None, stream=None):
     """out = xs w[e]^T for the rows of every expert's segment: xs [rows, in], w [experts, out, in] (without segments also
     [out, in]), out [rows, out]. Segments and weights as in ar_expert_gated."""
+    native = _native if _native is not None else _load_native()
+    if native and _done(native.expert_linear(xs, w, out, offsets, counts, stream), "ar_expert_linear"):
+        return
     shape, dt, dev = _matrix(xs, "xs")
     if out.dim() != 2:
         raise ValueError("out must be a matrix [rows, out]")
@@ -863,6 +876,9 @@ def ar_expert_linear(xs, w, out, offsets=None, counts=None, stream=None):
 def ar_expert_linear_bwd(dout, xs, w, dxs=None, dw=None, offsets=None, counts=None, stream=None):
     """The gradient of ar_expert_linear: dxs = dout w[e] [rows, in] (None: not wanted; w may then be None) and
     dw[e] = dout^T xs [experts, out, in] over the expert's rows (None: not wanted; xs may then be None)."""
+    native = _native if _native is not None else _load_native()
+    if native and _done(native.expert_linear_bwd(dout, xs, w, dxs, dw, offsets, counts, stream), "ar_expert_linear_bwd"):
+        return
     wide, dt, dev = _matrix(dout, "dout")
     rows, out = wide
     if dxs is not None and w is None:
@@ -937,6 +953,9 @@ def ar_grad_norm(plan, norm, kind=AR_NORM_L2, workspace=None, stream=None):
     """norm (float32, one element) = the norm over all gradients of a plan: the square root of the sum of squares
     (AR_NORM_L2) or the largest magnitude (AR_NORM_MAX). workspace: a GPU tensor of
     ar_grad_norm_workspace_size(plan.shape[0]) bytes."""
+    native = _native if _native is not None else _load_native()
+    if native and _done(native.grad_norm(plan, norm, kind, workspace, stream), "ar_grad_norm"):
+        return
     at, n, to, ws = _plan_args(plan, norm, workspace)
     with _on(plan.device):
         _check(lib().ar_grad_norm(at, n, *_ints(kind=kind), to, *ws, _stream(stream, plan.device)), "ar_grad_norm")
@@ -944,6 +963,9 @@ def ar_grad_norm(plan, norm, kind=AR_NORM_L2, workspace=None, stream=None):
 
 def ar_grad_clip(plan, max_norm, norm, kind=AR_NORM_L2, eps=1e-6, workspace=None, stream=None):
     """ar_grad_norm, and all gradients times min(1, max_norm / (norm + eps)) into the plan's outputs."""
+    native = _native if _native is not None else _load_native()
+    if native and _done(native.grad_clip(plan, max_norm, norm, kind, eps, workspace, stream), "ar_grad_clip"):
+        return
     at, n, to, ws = _plan_args(plan, norm, workspace)
     with _on(plan.device):
         _check(lib().ar_grad_clip(at, n, *_ints(kind=kind), max_norm, eps, to, *ws, _stream(stream, plan.device)),

@@ -907,7 +907,7 @@ bool add_matrices(Ranges& g, const void* p0, const void* p1, size_t matrix, size
 bool too_many_tiles(const ar::ProductArgs& a, int64_t in, int64_t out) {
   const int64_t wide = in > out ? in : out;
   return ar::row_tiles(a, 1, 16) * ar::tiles_up(wide, 16) > ar::kMostTiles ||
-         ar::matrices(a) * ar::tiles_up(in, 64) * ar::tiles_up(out, 64) > ar::kMostTiles;
+         2 * static_cast<int64_t>(a.experts) * ar::tiles_up(in, 64) * ar::tiles_up(out, 64) > ar::kMostTiles;
 }
 
 void add_segments(Ranges& g, const int32_t* offsets, const int32_t* counts, int nexperts) {

@@ -24,6 +24,12 @@ decltype(&ar_expert_sort) g_sort;
 decltype(&ar_expert_dispatch) g_dispatch;
 decltype(&ar_expert_combine) g_combine;
 decltype(&ar_expert_combine_bwd) g_combine_bwd;
+decltype(&ar_expert_gated) g_gated;
+decltype(&ar_expert_gated_bwd) g_gated_bwd;
+decltype(&ar_expert_linear) g_linear;
+decltype(&ar_expert_linear_bwd) g_linear_bwd;
+decltype(&ar_grad_norm) g_grad_norm;
+decltype(&ar_grad_clip) g_grad_clip;
 PyObject* g_current_device;
 PyObject* g_current_stream;
 
@@ -301,6 +307,192 @@ int expert_combine_bwd(PyObject* const* a) {  // dout ys pos weights offsets cou
   return rc;
 }
 
+// The tables of the experts' segments: offsets and counts, offsets alone, or neither.
+struct Segments {
+  const int32_t *offsets = nullptr, *counts = nullptr;
+  int experts = 1;
+  Segments(const Call& c, PyObject* off, PyObject* cnt) {
+    if (off == Py_None) {
+      if (cnt != Py_None) throw Misfit();
+      return;
+    }
+    const int64_t n = tensor(off).numel() - 1;
+    if (n < 1 || n > AR_MAX_EXPERTS) throw Misfit();
+    experts = static_cast<int>(n);
+    offsets = static_cast<int32_t*>(c.at_(off, at::kInt, n + 1));
+    if (cnt != Py_None) counts = static_cast<int32_t*>(c.at_(cnt, at::kInt, n));
+  }
+};
+
+// A weight [experts][out][in] (without segments also [out][in]) of dense matrices, and the elements from one to the next.
+struct Weight {
+  void* p = nullptr;
+  int64_t stride;
+  Weight(const Call& c, PyObject* o, at::ScalarType type, const Segments& seg, int64_t out, int64_t in) : stride(out * in) {
+    if (o == Py_None) return;
+    const at::Tensor& t = tensor(o);
+    const int64_t d = t.dim() - 2;
+    if (t.scalar_type() != type || t.get_device() != c.device || d > 1 || d < (seg.offsets ? 1 : 0) ||
+        (d == 1 && t.size(0) != seg.experts) || t.size(d) != out || t.size(d + 1) != in || t.stride(d + 1) != 1 || t.stride(d) != in)
+      throw Misfit();
+    if (seg.experts > 1) stride = t.stride(0);
+    p = t.data_ptr();
+    if (!p) throw Misfit();
+  }
+};
+
+int number(PyObject* o) {
+  const long v = PyLong_Check(o) ? PyLong_AsLong(o) : -1;
+  if (v < 0 || v > INT32_MAX) throw Misfit();
+  return static_cast<int>(v);
+}
+
+int expert_gated(PyObject* const* a) {  // xs w_gate w_up out offsets counts gate up act stream
+  const at::Tensor &x = matrix(a[0]), &out = matrix(a[3]);
+  const at::ScalarType type = x.scalar_type();
+  const int dtype = code_of(type);
+  const int64_t rows = x.size(0), hidden = x.size(1), inner = out.size(1);
+  const Call c(x);
+  const Segments seg(c, a[4], a[5]);
+  const void* xs = c.at_(a[0], type, rows, hidden);
+  const Weight g(c, a[1], type, seg, inner, hidden), u(c, a[2], type, seg, inner, hidden);
+  if (g.stride != u.stride) throw Misfit();
+  void* to = c.at_(a[3], type, rows, inner);
+  void* gate = c.opt(a[6], type, rows, inner);
+  void* up = c.opt(a[7], type, rows, inner);
+  const int act = number(a[8]);
+  void* s = c.stream(a[9]);
+  int rc;
+  Py_BEGIN_ALLOW_THREADS
+  rc = g_gated(xs, g.p, u.p, g.stride, seg.offsets, seg.counts, seg.experts, rows, hidden, inner, dtype, act, to, gate, up, s);
+  Py_END_ALLOW_THREADS
+  return rc;
+}
+
+// dout gate up xs w_gate w_up dgate dup dxs dw_gate dw_up offsets counts act stream; with xs or dxs, and both weights' gradients
+// or neither (what else the binding takes goes through its own checks)
+int expert_gated_bwd(PyObject* const* a) {
+  const at::Tensor& d = matrix(a[0]);
+  const at::ScalarType type = d.scalar_type();
+  const int dtype = code_of(type);
+  const bool weights = a[9] != Py_None, rows_too = a[8] != Py_None;
+  if (weights != (a[10] != Py_None) || (!weights && !rows_too) || (weights && a[3] == Py_None)) throw Misfit();
+  const at::Tensor& x = matrix(a[3] != Py_None ? a[3] : a[8]);
+  const int64_t rows = d.size(0), inner = d.size(1), hidden = x.size(1);
+  const Call c(d);
+  const Segments seg(c, a[11], a[12]);
+  const void* dout = c.at_(a[0], type, rows, inner);
+  const void* gate = c.at_(a[1], type, rows, inner);
+  const void* up = c.at_(a[2], type, rows, inner);
+  const void* xs = c.opt(a[3], type, rows, hidden);
+  PyObject* none = Py_None;
+  const Weight g(c, rows_too ? a[4] : none, type, seg, inner, hidden), u(c, rows_too ? a[5] : none, type, seg, inner, hidden);
+  if (rows_too && (!g.p || !u.p || g.stride != u.stride)) throw Misfit();
+  void* dgate = c.at_(a[6], type, rows, inner);
+  void* dup = c.at_(a[7], type, rows, inner);
+  void* dxs = c.opt(a[8], type, rows, hidden);
+  const Weight dg(c, a[9], type, seg, inner, hidden), du(c, a[10], type, seg, inner, hidden);
+  if (dg.stride != du.stride) throw Misfit();
+  const int act = number(a[13]);
+  void* s = c.stream(a[14]);
+  int rc;
+  Py_BEGIN_ALLOW_THREADS
+  rc = g_gated_bwd(dout, gate, up, xs, g.p, u.p, g.stride, seg.offsets, seg.counts, seg.experts, rows, hidden, inner, dtype, act,
+                   dgate, dup, dxs, dg.p, du.p, dg.stride, s);
+  Py_END_ALLOW_THREADS
+  return rc;
+}
+
+int expert_linear(PyObject* const* a) {  // xs w out offsets counts stream
+  const at::Tensor &x = matrix(a[0]), &out = matrix(a[2]);
+  const at::ScalarType type = x.scalar_type();
+  const int dtype = code_of(type);
+  const int64_t rows = x.size(0), in = x.size(1), wide = out.size(1);
+  const Call c(x);
+  const Segments seg(c, a[3], a[4]);
+  const void* xs = c.at_(a[0], type, rows, in);
+  const Weight w(c, a[1], type, seg, wide, in);
+  if (!w.p) throw Misfit();
+  void* to = c.at_(a[2], type, rows, wide);
+  void* s = c.stream(a[5]);
+  int rc;
+  Py_BEGIN_ALLOW_THREADS
+  rc = g_linear(xs, w.p, w.stride, seg.offsets, seg.counts, seg.experts, rows, in, wide, dtype, to, s);
+  Py_END_ALLOW_THREADS
+  return rc;
+}
+
+int expert_linear_bwd(PyObject* const* a) {  // dout xs w dxs dw offsets counts stream
+  const at::Tensor& d = matrix(a[0]);
+  const at::ScalarType type = d.scalar_type();
+  const int dtype = code_of(type);
+  const bool rows_too = a[3] != Py_None;
+  if ((!rows_too && a[4] == Py_None) || (a[4] != Py_None && a[1] == Py_None)) throw Misfit();
+  const at::Tensor& x = matrix(rows_too ? a[3] : a[1]);
+  const int64_t rows = d.size(0), wide = d.size(1), in = x.size(1);
+  const Call c(d);
+  const Segments seg(c, a[5], a[6]);
+  const void* dys = c.at_(a[0], type, rows, wide);
+  const void* xs = c.opt(a[1], type, rows, in);
+  PyObject* none = Py_None;
+  const Weight w(c, rows_too ? a[2] : none, type, seg, wide, in);
+  if (rows_too && !w.p) throw Misfit();
+  void* dxs = c.opt(a[3], type, rows, in);
+  const Weight dw(c, a[4], type, seg, wide, in);
+  void* s = c.stream(a[7]);
+  int rc;
+  Py_BEGIN_ALLOW_THREADS
+  rc = g_linear_bwd(dys, xs, w.p, w.stride, seg.offsets, seg.counts, seg.experts, rows, in, wide, dtype, dxs, dw.p, dw.stride, s);
+  Py_END_ALLOW_THREADS
+  return rc;
+}
+
+// A plan's pieces and the norm that they give.
+struct Plan {
+  const Call c;
+  const ar_grad_piece* pieces;
+  int64_t n;
+  float* norm;
+  void* ws;
+  size_t bytes;
+  Plan(PyObject* plan, PyObject* to, PyObject* workspace) : c(matrix(plan)), n(tensor(plan).size(0)) {
+    pieces = static_cast<ar_grad_piece*>(c.at_(plan, at::kLong, n, sizeof(ar_grad_piece) / 8));
+    const at::Tensor& t = tensor(to);
+    if (t.scalar_type() != at::kFloat || t.get_device() != c.device || t.numel() != 1) throw Misfit();
+    norm = static_cast<float*>(t.data_ptr());
+    ws = c.workspace(workspace, &bytes);
+  }
+};
+
+float real(PyObject* o) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) throw Misfit();
+  return static_cast<float>(v);
+}
+
+int grad_norm(PyObject* const* a) {  // plan norm kind workspace stream
+  const Plan p(a[0], a[1], a[3]);
+  const int kind = number(a[2]);
+  void* s = p.c.stream(a[4]);
+  int rc;
+  Py_BEGIN_ALLOW_THREADS
+  rc = g_grad_norm(p.pieces, p.n, kind, p.norm, p.ws, p.bytes, s);
+  Py_END_ALLOW_THREADS
+  return rc;
+}
+
+int grad_clip(PyObject* const* a) {  // plan max_norm norm kind eps workspace stream
+  const Plan p(a[0], a[2], a[5]);
+  const float most = real(a[1]), eps = real(a[4]);
+  const int kind = number(a[3]);
+  void* s = p.c.stream(a[6]);
+  int rc;
+  Py_BEGIN_ALLOW_THREADS
+  rc = g_grad_clip(p.pieces, p.n, kind, most, eps, p.norm, p.ws, p.bytes, s);
+  Py_END_ALLOW_THREADS
+  return rc;
+}
+
 // F with its N arguments; whatever is thrown becomes None.
 template <int (*F)(PyObject* const*), int N> PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
   if (n == N && g_current_stream) {
@@ -342,11 +534,44 @@ PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
   Py_RETURN_NONE;
 }
 
+// bind_products(addresses of the six entry points behind those of bind, in the order above), before bind
+PyObject* bind_products(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  if (n != 6) {
+    PyErr_SetString(PyExc_TypeError, "bind_products takes six addresses");
+    return nullptr;
+  }
+  void* p[6];
+  for (int i = 0; i < 6; ++i) {
+    p[i] = PyLong_AsVoidPtr(args[i]);
+    if (!p[i]) {
+      if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "an entry point's address is 0");
+      return nullptr;
+    }
+  }
+  g_gated = reinterpret_cast<decltype(g_gated)>(p[0]);
+  g_gated_bwd = reinterpret_cast<decltype(g_gated_bwd)>(p[1]);
+  g_linear = reinterpret_cast<decltype(g_linear)>(p[2]);
+  g_linear_bwd = reinterpret_cast<decltype(g_linear_bwd)>(p[3]);
+  g_grad_norm = reinterpret_cast<decltype(g_grad_norm)>(p[4]);
+  g_grad_clip = reinterpret_cast<decltype(g_grad_clip)>(p[5]);
+  Py_RETURN_NONE;
+}
+
 #define AR_ENTRY(f, n) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(entry<f, n>)), METH_FASTCALL, nullptr}
+// The same once its entry point is bound.
+template <int (*F)(PyObject* const*), int N, auto* G> PyObject* product(PyObject* self, PyObject* const* args, Py_ssize_t n) {
+  if (!*G) Py_RETURN_NONE;
+  return entry<F, N>(self, args, n);
+}
+#define AR_PRODUCT(f, n, g) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(product<f, n, &g>)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {
     {"bind", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(bind)), METH_FASTCALL, nullptr},
     AR_ENTRY(rmsnorm, 11), AR_ENTRY(rmsnorm_bwd, 10), AR_ENTRY(expert_sort, 8), AR_ENTRY(expert_dispatch, 8),
-    AR_ENTRY(expert_combine, 6), AR_ENTRY(expert_combine_bwd, 9), {nullptr, nullptr, 0, nullptr}};
+    AR_ENTRY(expert_combine, 6), AR_ENTRY(expert_combine_bwd, 9),
+    {"bind_products", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(bind_products)), METH_FASTCALL, nullptr},
+    AR_PRODUCT(expert_gated, 10, g_gated), AR_PRODUCT(expert_gated_bwd, 15, g_gated_bwd), AR_PRODUCT(expert_linear, 6, g_linear),
+    AR_PRODUCT(expert_linear_bwd, 8, g_linear_bwd), AR_PRODUCT(grad_norm, 5, g_grad_norm), AR_PRODUCT(grad_clip, 7, g_grad_clip),
+    {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

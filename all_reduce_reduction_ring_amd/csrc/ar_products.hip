@@ -227,26 +227,31 @@ template <int DT, bool KS, bool PAIRED, bool DIRECT, int CH, int R, int NT> stru
     }
   }
 
-  // Reads the step of the sum that starts `k0` elements in: `base` is the matrix at the tile's first row and sum element
-  // 0; what lies past `K` is zero.
-  __device__ __forceinline__ void fetch(u32x4 (&v)[kLoads], const char* base, uint32_t stride, int k0, int K) const {
+  // Chunk i of the step of the sum that starts at element k0, through a register. `base` is the matrix at the tile's first row
+  // and that element, `left` the bytes from there to its end (KC: to the end of the tile's last row); elements past K are
+  // zero. A chunk that a row's end cuts is read on into the next row where there is one.
+  __device__ __forceinline__ u32x4 fetch(int i, const char* base, uint32_t stride, uint32_t left, int k0, int K) const {
     if constexpr (!KS) {
-      const int k = k0 + chunk * V;
-      const char* p = base + static_cast<int64_t>(k) * ES;
+      const int n = K - k0 - chunk * V;
+      const uint32_t at_byte = at[i] + chunk * 16;
+      if (n <= 0) return u32x4{0, 0, 0, 0};
+      if (at_byte + 16 > left) return first_elements<DT>(base + at_byte, n);
+      u32x4 w = ldu16(base + at_byte);
+      if (k0 + CH * V > K) {
 #pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        if (k + V <= K) v[i] = ldu16(p + at[i]);
-        else v[i] = first_elements<DT>(p + at[i], K - k);
+        for (int j = 0; j < 4; ++j) {
+          if constexpr (ES == 2) w[j] &= 2 * j + 1 < n ? ~0u : 2 * j < n ? 0xFFFFu : 0u;
+          else w[j] &= j < n ? ~0u : 0u;
+        }
       }
+      return w;
     } else {
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        const int row = lds_row + i * kStride, k = k0 + row;
-        const int c = ((static_cast<int>(threadIdx.x) % kRowChunks) ^ mix_ks<DT, R>(row)) * V;
-        const char* p = base + static_cast<int64_t>(k) * stride + c * ES;
-        if (k < K && c + V <= limit) v[i] = ldu16(p);
-        else v[i] = first_elements<DT>(p, k < K ? limit - c : 0);
-      }
+      const int row = lds_row + i * kStride;
+      const int c = ((static_cast<int>(threadIdx.x) % kRowChunks) ^ mix_ks<DT, R>(row)) * V;
+      const uint32_t at_byte = static_cast<uint32_t>(row) * stride + c * ES;
+      if (k0 + row >= K) return u32x4{0, 0, 0, 0};
+      if (at_byte + 16 > left) return first_elements<DT>(base + at_byte, limit - c);
+      return ldu16(base + at_byte);
     }
   }
   __device__ __forceinline__ void put(const u32x4 (&v)[kLoads], AR_LDS char* lds) const {
@@ -624,20 +629,23 @@ __global__ __launch_bounds__(WM* WN * 64) void tile_kernel(const ProductArgs a) 
       ready<0>();  // nothing is in flight when the workgroup goes on or ends
     } else {
       u32x4 va[A::kLoads], vb[B::kLoads];
+      const int high = rows_left < BM ? rows_left : BM, wide = cols_left < COLS ? cols_left : COLS;
       auto fetch = [&](int s) {
         const bool second = s >= steps1;
         const int k0 = (second ? s - steps1 : s) * K_STEP;
-        ta.fetch(va, second ? pa1 : pa, sa, k0, K);
-        if constexpr (KIND == kGated) {
-          // LDS rows 32 to 63 of every 64 are of w_up; whole waves read one matrix
+        auto from = [&](const char* p, bool ks, uint32_t stride) { return p + static_cast<int64_t>(k0) * (ks ? stride : ES); };
+        auto left = [&](int64_t bytes) { return load_bytes(static_cast<uint32_t>(bytes >> 32), static_cast<uint32_t>(bytes)); };
+        const uint32_t left_a = left(kRowsKS<KIND> ? across_left(K, k0, sa, m0, ES) : along_left(high, sa, K, k0, ES));
+        const uint32_t left_b = left(kColsKS<KIND> ? across_left(K, k0, sb, n0, ES) : along_left(wide, sb, K, k0, ES));
+        const char *at_a = from(second ? pa1 : pa, kRowsKS<KIND>, sa), *at_b = from(second ? pb1 : pb, kColsKS<KIND>, sb);
+        const char* at_up = KIND == kGated ? from(pb1, false, sb) : nullptr;
 #pragma unroll
-          for (int i = 0; i < B::kLoads; ++i) {
-            const int r = tb.lds_row + i * B::kStride, k = k0 + tb.chunk * V;
-            const char* p = ((r & 32) ? pb1 : pb) + static_cast<int64_t>(k) * ES + tb.at[i];
-            vb[i] = k + V <= K ? ldu16(p) : first_elements<DT>(p, K - k);
-          }
-        } else {
-          tb.fetch(vb, second ? pb1 : pb, sb, k0, K);
+        for (int i = 0; i < A::kLoads; ++i) va[i] = ta.fetch(i, at_a, sa, left_a, k0, K);
+#pragma unroll
+        for (int i = 0; i < B::kLoads; ++i) {
+          // gated: LDS rows 32 to 63 of every 64 are of w_up; whole waves read one matrix
+          const bool of_up = KIND == kGated && ((wave * (64 / CH) + i * B::kStride) & 32) != 0;
+          vb[i] = tb.fetch(i, of_up ? at_up : at_b, sb, left_b, k0, K);
         }
       };
       auto put = [&](int s) {
@@ -834,17 +842,18 @@ template <int DT, int KIND> __global__ __launch_bounds__(kFewThreads) void few_k
 
 // ------------------------------------------------------------------------------------------ slopes
 // dg and du of an expert's rows; a segment's rows lie one behind the other, so its elements are walked in a row.
-constexpr int kSlopeUnit = 8192, kSlopeThreads = 256;
+// UNIT: elements a workgroup takes at a time. Few are spread over more workgroups: 402 x 530 fp16, 12.6 us with the large unit.
+constexpr int kSlopeThreads = 256, kSlopeUnit = 8192, kSlopeLeast = 1024;
 
-template <int DT> __global__ __launch_bounds__(kSlopeThreads) void slopes_kernel(const ProductArgs a) {
+template <int DT, int UNIT> __global__ __launch_bounds__(kSlopeThreads) void slopes_kernel(const ProductArgs a) {
   constexpr int V = Traits<DT>::kVec, ES = Traits<DT>::kSize;
-  const int total = min(all_tiles(a, a.n, kSlopeUnit), a.most);
+  const int total = min(all_tiles(a, a.n, UNIT), a.most);
   for (int id = blockIdx.x; id < total; id += gridDim.x) {
     Place at;
-    if (!find_tile(a, id, a.n, kSlopeUnit, &at)) continue;  // tables that changed meanwhile
-    const int64_t base = static_cast<int64_t>(at.first) * a.n + static_cast<int64_t>(at.index) * kSlopeUnit;
-    const int64_t rest = static_cast<int64_t>(at.n) * a.n - static_cast<int64_t>(at.index) * kSlopeUnit;
-    const int len = rest < kSlopeUnit ? static_cast<int>(rest) : kSlopeUnit;
+    if (!find_tile(a, id, a.n, UNIT, &at)) continue;  // tables that changed meanwhile
+    const int64_t base = static_cast<int64_t>(at.first) * a.n + static_cast<int64_t>(at.index) * UNIT;
+    const int64_t rest = static_cast<int64_t>(at.n) * a.n - static_cast<int64_t>(at.index) * UNIT;
+    const int len = rest < UNIT ? static_cast<int>(rest) : UNIT;
     for (int i = threadIdx.x * V; i < len; i += kSlopeThreads * V) {
       const int64_t ofs = (base + i) * ES;
       const char *pd = static_cast<const char*>(a.a0) + ofs, *pg = static_cast<const char*>(a.b0) + ofs,
@@ -915,18 +924,21 @@ template <int DT, int KIND> hipError_t launch_few(ProductArgs a, hipStream_t s) 
 }
 
 // Which kernel. The host knows rows and experts, not how the rows are spread. (bf16, one MI355X, rows for each expert.)
-//   Few rows (forward products: up to 16 of a dense matrix, 8 an expert on average) where 128-wide tiles would leave the
-//     GPU short of workgroups: few_kernel. One of 4096 x 4096, 1 to 16 rows: 12-15 us against 27 with 64 x 64 tiles and 33
+//   Few rows (forward products: up to 16 of a dense matrix, 8 an expert on average, 16 in fp32) where 128-wide
+//     tiles would leave the GPU short of workgroups: few_kernel. One of 4096 x 4096, 1 to 16 rows: 12-15 us against 27 with 64 x 64 tiles and 33
 //     with 128 x 128; 8 of 64 experts, gated 2 x 1024 x 2048: 14.3 / 24 / 27; 8 experts, gated 2 x 8192 x 4096, 1 to 8 rows
 //     (1024 tiles): 179-185 / 235 / 232; but 64 of 1024 x 1024, 16 rows: 31 / 29 / 29, and 48 tokens x 4 to 128 experts of
-//     4096 x 1024, where some have many rows: 75 / 55 / 56 (4096 tiles).
+//     4096 x 1024, where some have many rows: 75 / 55 / 56 (4096 tiles). fp32, 4 experts of 2048 x 4096, 16 rows: 31 / 99,
+//     64 rows 97 / 107.
 //   256 x 256 tiles (16-bit types, whole chunks): half the reads of the operands, but one workgroup a CU. From 192 rows an
 //     expert and three tiles for four CUs on. 16 of 2048 x 2048: 128 rows, gated 75 us with 128 x 128 tiles / 81 with
 //     256 x 256; 256 rows 112 / 86, linear (128 large tiles) 53 / 58; 1024 rows 329 / 249. Gradients of weights write more
 //     than they multiply when rows are few, and take large tiles whenever there are enough: 16 of 2048 x 2048, 1 row
 //     56 / 50, 1024 rows 191 / 142; one of 4096 x 4096, 1024 rows 47 / 36.
 //   64 x 64 tiles where there is not one of 128 x 128 for each CU: one of 4096 x 4096, 128 rows 28 / 48, 1024 rows (256
-//     tiles) 57 / 55; 32 of 512 x 512, 128 rows 9.3 / 12.5; 16 of 2048 x 2048, 128 rows (256 tiles) 54 / 44.
+//     tiles) 57 / 55; 32 of 512 x 512, 128 rows 9.3 / 12.5; 16 of 2048 x 2048, 128 rows (256 tiles) 54 / 44. fp32 always,
+//     except weights' gradients: bound by the matrix instructions in either, 4 of 2048 x 4096, gated, 64 rows 107 / 296,
+//     512 rows 534 / 535, 2048 rows 2081 / 2099.
 template <int DT, int KIND, int LOADS> hipError_t launch_small(const ProductArgs& a, bool least, hipStream_t s) {
   if (least) return launch_tile<DT, KIND, LOADS, 64, 64, 4, 1>(a, s);
   return launch_tile<DT, KIND, LOADS, 128, 128, 2, 2>(a, s);
@@ -936,20 +948,21 @@ template <int DT, int KIND> hipError_t launch_tiles(const ProductArgs& a, hipStr
   constexpr int COLS = KIND == kGated ? 64 : 128, V = Traits<DT>::kVec;
   const int64_t cus = cu_count(), across = tiles_up(a.n, COLS);
   if constexpr (KIND == kGated || KIND == kLinear) {
-    if (a.rows <= (a.offsets ? 8 * static_cast<int64_t>(a.experts) : 16) && most_experts(a) * across <= 4 * cus)
-      return launch_few<DT, KIND>(a, s);
+    const int64_t few = a.offsets && Traits<DT>::kSize == 2 ? 8 : 16;
+    if (a.rows <= few * a.experts && most_experts(a) * across <= 4 * cus) return launch_few<DT, KIND>(a, s);
   }
   const int64_t down = KIND == kWeight ? matrices(a) * tiles_up(a.m, 128) : tiles_up(a.rows, 128);
   const bool least = down * across < cus, whole = KIND == kWeight || a.k % V == 0;
   if constexpr (Traits<DT>::kSize == 2) {
-    if (!in_words(a, KIND, 2)) return launch_tile<DT, KIND, kRegisters, 128, 128, 2, 2>(a, s);
+    if (!in_words(a, KIND, 2)) return launch_small<DT, KIND, kRegisters>(a, least, s);
     const int64_t large = KIND == kWeight ? matrices(a) * tiles_up(a.m, 256) : a.rows / 256;
     if (whole && (KIND == kWeight || a.rows >= 192 * static_cast<int64_t>(a.experts)) &&
         large * tiles_up(a.n, 2 * COLS) * 4 >= 3 * cus)
       return launch_tile<DT, KIND, kWhole, 256, 256, 2, 4>(a, s);
   }
   if constexpr (KIND != kWeight) {
-    if (!whole || Traits<DT>::kSize == 4) return launch_small<DT, KIND, kCut>(a, least, s);
+    if constexpr (Traits<DT>::kSize == 4) return launch_tile<DT, KIND, kCut, 64, 64, 4, 1>(a, s);
+    else if (!whole) return launch_small<DT, KIND, kCut>(a, least, s);
   }
   if constexpr (KIND == kWeight || Traits<DT>::kSize == 2) return launch_small<DT, KIND, kWhole>(a, least, s);
 }
@@ -967,14 +980,20 @@ hipError_t launch_linear(const ProductArgs& a, int dtype, hipStream_t s) { retur
 hipError_t launch_input_grad(const ProductArgs& a, int dtype, hipStream_t s) { return launch_kind<kInput>(a, dtype, s); }
 hipError_t launch_weight_grad(const ProductArgs& a, int dtype, hipStream_t s) { return launch_kind<kWeight>(a, dtype, s); }
 
-hipError_t launch_slopes(ProductArgs a, int dtype, hipStream_t s) {
-  a.most = static_cast<int>(row_tiles(a, a.n, kSlopeUnit));
+template <int DT, int UNIT> static hipError_t slopes_of(ProductArgs a, hipStream_t s) {
+  a.most = static_cast<int>(row_tiles(a, a.n, UNIT));
   if (a.most == 0) return hipSuccess;
-  const int grid = grid_of(a.most, 8);
-  if (dtype == AR_BF16) slopes_kernel<AR_BF16><<<grid, kSlopeThreads, 0, s>>>(a);
-  else if (dtype == AR_F16) slopes_kernel<AR_F16><<<grid, kSlopeThreads, 0, s>>>(a);
-  else slopes_kernel<AR_F32><<<grid, kSlopeThreads, 0, s>>>(a);
+  slopes_kernel<DT, UNIT><<<grid_of(a.most, 8), kSlopeThreads, 0, s>>>(a);
   return hipGetLastError();
+}
+template <int DT> static hipError_t slopes_of(const ProductArgs& a, hipStream_t s) {
+  if (static_cast<int64_t>(a.rows) * a.n < 4 * static_cast<int64_t>(kSlopeUnit) * cu_count()) return slopes_of<DT, kSlopeLeast>(a, s);
+  return slopes_of<DT, kSlopeUnit>(a, s);
+}
+hipError_t launch_slopes(ProductArgs a, int dtype, hipStream_t s) {
+  if (dtype == AR_BF16) return slopes_of<AR_BF16>(a, s);
+  if (dtype == AR_F16) return slopes_of<AR_F16>(a, s);
+  return slopes_of<AR_F32>(a, s);
 }
 
 }  // namespace ar

@@ -9,6 +9,9 @@
 // from 1.8e19 up and below 1e-19, and sums over a billion elements would lose digits; the conversions and sums cost
 // less than the loads. Partial sums of the workgroups go through the workspace, and every workgroup of the second launch
 // adds all of them up in the same order, so nothing is left to atomics and the result depends on the table alone.
+// Measured: 1.34 G elements, bf16 but for the norms' fp32 weights: the norm 450 us, 6.0 TB/s; clipping behind it 1025 us, 5.2
+// TB/s read and written (a copy of 4 GiB: 4.8). 61 M fp32 elements in tensors of odd sizes: 35 us, 44 with both launches of a call.
+// 0.7 M elements: 2.7 + 4.0 us, the launches' own time.
 #include "ar_block.h"
 #include "ar_grads.h"
 #include "ar_internal.h"

@@ -9,13 +9,22 @@
 //
 // One tile kernel serves all of them. A workgroup computes a BM x BN tile of the result with matrix instructions
 // (16 x 16 results from 16 bytes of either operand per lane, fp32 sums); operands pass through LDS in steps of 128 bytes
-// along the sum, two buffers in turn. An operand lies in memory either along the sum (rows of x, dy, and of w in the
-// forward products: "KC") or across it (w for the rows' gradients, x and dy for the weights': "KS"); the second kind is
-// kept in LDS as it lies and transposed on the way to registers (ds_read_tr for 16-bit types), so no operand is
-// ever transposed in memory.
+// along the sum. An operand lies in memory either along the sum (rows of x, dy, and of w in the forward products: "KC")
+// or across it (w for the rows' gradients, x and dy for the weights': "KS"); the second kind is kept in LDS as it lies and
+// transposed on the way to registers (ds_read_tr for 16-bit types), so no operand is ever transposed in memory.
 //
 // The host does not know the segments, so a tile's expert and rows are found on the device: a wave sums the experts'
 // tile counts (64 experts a step) and the grid is as large as any segments of so many rows need.
+//
+// Sums are fp32 and rounded once, to the results' type. The gated gradient rounds dg and du to it before the two products
+// that read them, which take 16-bit operands anyway.
+//
+// What bounds it: with many rows, the matrix instructions and the power they draw. 32,768 rows of 32 experts, gated 2 x 2048
+// x 4096 bf16, segments as a router leaves them: 1.10 ms, 1000 TF (a library product of one matrix of that size reaches
+// 1245); a dense 16,384 x 4160 x 4096: matrix units busy 74% of the time, 1300 TF, and 1430 on zeros, which draw less power.
+// With few rows, reading the weights: 4.9 TB/s (a copy reaches 4.8). Weights' gradients of few rows, writing them: 268 MB in
+// 80 us, and 0.19 us more for every row of 16 experts of 4096 x 2048. Rows of odd numbers of 16-bit elements (or odd
+// addresses) cannot be loaded straight into LDS and take about 2.5 times as long.
 #include "ar_block.h"
 #include "ar_internal.h"
 #include "ar_products.h"
@@ -338,6 +347,26 @@ template <int DT, int N> __device__ __forceinline__ void store_run(char* p, cons
     if (i < left) store_elem<DT>(p, i, narrow<DT>(v[i]));
 }
 
+// Columns across the sum lie in a lane's subtiles as four neighbours each. Lane groups 0 and 1, and 2 and 3, exchange halves of
+// two subtiles, x and y: the even group is left with 8 neighbours of x, the odd one with 8 of y. Stores
+// of 16 bytes in the place of 8: gated gradient of 16,384 rows, 32 experts of 2 x 2048 x 4096 bf16, 1470 -> 1373 us.
+template <int DT> __device__ __forceinline__ u32x4 neighbours(const f32x4& x, const f32x4& y) {
+  auto pack = [](float lo, float hi) { return narrow<DT>(lo) | narrow<DT>(hi) << 16; };
+  const auto a = __builtin_amdgcn_permlane16_swap(pack(x[0], x[1]), pack(y[0], y[1]), false, false);
+  const auto b = __builtin_amdgcn_permlane16_swap(pack(x[2], x[3]), pack(y[2], y[3]), false, false);
+  return u32x4{a[0], b[0], a[1], b[1]};
+}
+// 8 elements of 16 bits to p, of which `left` lie in the row.
+__device__ __forceinline__ void store_words(char* p, const u32x4& w, int left) {
+  if (left >= 8) {
+    stu16(p, w);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i < left) store_elem<AR_BF16>(p, i, w[i >> 1] >> (16 * (i & 1)) & 0xFFFFu);
+}
+
 // ------------------------------------------------------------------------------------------ the tile kernel
 template <int KIND> constexpr bool kRowsKS = KIND == kWeight;                        // operand of the tile's rows
 template <int KIND> constexpr bool kColsKS = KIND == kWeight || KIND == kInput;      // operand of its columns
@@ -360,10 +389,16 @@ __device__ __forceinline__ void raster(int t, int down, int across, int* row, in
 // that the end of the sum cuts mended in LDS (which costs the large tiles registers that they do not have).
 enum Loads { kRegisters = 0, kWhole = 1, kCut = 2 };
 
+// WM x WN waves, each with a part of BM / WM rows and BN / WN columns (gated: of half as many, and both products of them) in
+// registers. Sizes of a part: 128 x 64 in the 256 x 256 tile, whose 128 registers of sums leave room for the fragments of a
+// step; 64 x 64 in the 128 x 128 one (two workgroups a compute unit); 16 x 64 in the 64 x 64 one (four). 128 x 128 for each of
+// four waves spills. LDS: five operand tiles of 128 bytes along the sum, 160 / 80 / 40 KB. Steps of
+// half the length took 11% longer (131,072 rows, 64 experts of 2048 x 1024), having twice the barriers.
+// Level or worse at 32 experts of 2 x 2048 x 4096 bf16: 32 x 32 instructions (3%), a raised wave priority (0), workgroups that
+// start their next tile's loads before they write results (0 to 70%: the tiles of uneven segments spread less evenly).
 template <int DT, int KIND, int LOADS, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(WM* WN * 64) void tile_kernel(const ProductArgs a) {
   constexpr bool DIRECT = LOADS != kRegisters;
-  // chunks of the sum per step, and steps that LDS holds
   constexpr int CH = 8, PLACES = DIRECT ? 5 : 4;  // chunks of the sum per step; operand tiles that LDS holds
   constexpr int NT = WM * WN * 64, ES = Traits<DT>::kSize, V = 16 / ES, K_STEP = CH * V;
   constexpr int MI = BM / WM / 16, NI = BN / WN / 16;
@@ -698,14 +733,23 @@ __global__ __launch_bounds__(WM* WN * 64) void tile_kernel(const ProductArgs a) 
           out = static_cast<char*>(which ? a.c1 : a.c0) +
                 (static_cast<int64_t>(e) * a.c_stride + static_cast<int64_t>(m0 + r) * a.n + n0) * ES;
         else out = static_cast<char*>(a.c0) + (static_cast<int64_t>(first + m0 + r) * a.n + n0) * ES;
-        constexpr int RUN = PAIRED ? 8 : 4;
+        if constexpr (PAIRED || ES == 4) {
+          constexpr int RUN = PAIRED ? 8 : 4;
 #pragma unroll
-        for (int j = 0; j < NI; j += RUN / 4) {
-          const int c = wn * WCOLS + n_of<PAIRED>(j, q, 0), left = a.n - n0 - c;
-          float v[RUN];
+          for (int j = 0; j < NI; j += RUN / 4) {
+            const int c = wn * WCOLS + n_of<PAIRED>(j, q, 0), left = a.n - n0 - c;
+            float v[RUN];
 #pragma unroll
-          for (int k = 0; k < RUN; ++k) v[k] = acc[j + k / 4][i][k % 4];
-          if (left > 0) store_run<DT, RUN>(out + c * ES, v, left);
+            for (int k = 0; k < RUN; ++k) v[k] = acc[j + k / 4][i][k % 4];
+            if (left > 0) store_run<DT, RUN>(out + c * ES, v, left);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < NI; j += 2) {
+            const int c = wn * WCOLS + (j + (q & 1)) * 16 + (q & 2) * 4, left = a.n - n0 - c;
+            const u32x4 w = neighbours<DT>(acc[j][i], acc[j + 1][i]);
+            if (left > 0) store_words(out + c * ES, w, left);
+          }
         }
       }
     }

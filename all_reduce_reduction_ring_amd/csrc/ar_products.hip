@@ -980,9 +980,11 @@ template <int DT, int KIND> hipError_t launch_few(ProductArgs a, hipStream_t s) 
 //     than they multiply when rows are few, and take large tiles whenever there are enough: 16 of 2048 x 2048, 1 row
 //     56 / 50, 1024 rows 191 / 142; one of 4096 x 4096, 1024 rows 47 / 36.
 //   64 x 64 tiles where there is not one of 128 x 128 for each CU: one of 4096 x 4096, 128 rows 28 / 48, 1024 rows (256
-//     tiles) 57 / 55; 32 of 512 x 512, 128 rows 9.3 / 12.5; 16 of 2048 x 2048, 128 rows (256 tiles) 54 / 44. fp32 always,
-//     except weights' gradients: bound by the matrix instructions in either, 4 of 2048 x 4096, gated, 64 rows 107 / 296,
-//     512 rows 534 / 535, 2048 rows 2081 / 2099.
+//     tiles) 57 / 55; 32 of 512 x 512, 128 rows 9.3 / 12.5; 16 of 2048 x 2048, 128 rows (256 tiles) 54 / 44. fp32, which the
+//     matrix instructions bound in either: always (4 of 2048 x 4096, gated, 64 rows 107 / 296, 512 rows 534 / 535, 2048 rows
+//     2081 / 2099); weights' gradients where the busiest CU has at least a tenth less to do with them (6 of 1190 x 530, 300
+//     tiles, 100 rows 18.6 / 23.8, 1000 rows 97 / 135; 10 of 1003 x 770, 560 tiles, 33 / 40; but 10 of 1000 x 768, 480 tiles,
+//     100 rows 29.8 / 28.3, 1000 rows 150 / 144).
 template <int DT, int KIND, int LOADS> hipError_t launch_small(const ProductArgs& a, bool least, hipStream_t s) {
   if (least) return launch_tile<DT, KIND, LOADS, 64, 64, 4, 1>(a, s);
   return launch_tile<DT, KIND, LOADS, 128, 128, 2, 2>(a, s);
@@ -996,7 +998,12 @@ template <int DT, int KIND> hipError_t launch_tiles(const ProductArgs& a, hipStr
     if (a.rows <= few * a.experts && most_experts(a) * across <= 4 * cus) return launch_few<DT, KIND>(a, s);
   }
   const int64_t down = KIND == kWeight ? matrices(a) * tiles_up(a.m, 128) : tiles_up(a.rows, 128);
-  const bool least = down * across < cus, whole = KIND == kWeight || a.k % V == 0;
+  bool least = down * across < cus;
+  if constexpr (KIND == kWeight && Traits<DT>::kSize == 4) {
+    const int64_t small = matrices(a) * tiles_up(a.m, 64) * tiles_up(a.n, 64);
+    least = least || 10 * tiles_up(small, cus) < 9 * 4 * tiles_up(down * across, cus);
+  }
+  const bool whole = KIND == kWeight || a.k % V == 0;
   if constexpr (Traits<DT>::kSize == 2) {
     if (!in_words(a, KIND, 2)) return launch_small<DT, KIND, kRegisters>(a, least, s);
     const int64_t large = KIND == kWeight ? matrices(a) * tiles_up(a.m, 256) : a.rows / 256;

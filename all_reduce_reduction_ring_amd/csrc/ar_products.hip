@@ -758,13 +758,14 @@ __global__ __launch_bounds__(WM* WN * 64) void tile_kernel(const ProductArgs a) 
 
 // ------------------------------------------------------------------------------------------ few rows
 // The forward products where an expert has a few rows only: bound by reading the weights once. A workgroup takes 32 rows of
-// weights (gated: 16 of either) and all of the expert's rows, 16 at a time. Its four waves split the sum in blocks of a
+// weights (gated: 16 of either) and 16 of the expert's rows; where one has more, its weights come from the caches again
+// (64 experts of 1024 x 2048, 32 rows for one of them 9 us, 512 rows 26; all rows in one workgroup: 15 and 185). Its four waves split the sum in blocks of a
 // cache line (128 bytes of every row), in turn, straight into the registers that the matrix instruction takes, the next
 // block ahead of the products of this one; their sums meet in LDS. Many short workgroups keep more loads in flight than
 // 128-row tiles do where those are few. Workgroups of neighbouring columns start at different blocks: rows of a power of
 // two of bytes would have all of them read the same few memory channels at a time (8 of 64 experts, 2 x 1024 x 2048 bf16:
 // 18.2 -> 14.6 us; 8 experts, 8192 x 4096: 114 -> 95).
-constexpr int kFewThreads = 256, kFewWaves = kFewThreads / 64;
+constexpr int kFewRows = 16, kFewThreads = 256, kFewWaves = kFewThreads / 64;
 constexpr int kUnits = 2;      // loads of a row's 64 bytes per block (4: 10% slower at 64 experts of 1024 x 1024)
 constexpr int kFirstStep = 9;  // blocks between the first ones of neighbouring workgroups
 
@@ -774,12 +775,12 @@ template <int DT, int KIND> __global__ __launch_bounds__(kFewThreads) void few_k
   __shared__ f32x4 sums[kFewWaves][2][64];
   const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, l = lane & 15, q = lane >> 4;
   const int across = (a.n + COLS - 1) / COLS;
-  const int total = a.most * across;  // one "tile" for each expert with rows; there may be fewer
+  const int total = a.most * across;  // there may be fewer
   const uint32_t row_bytes = static_cast<uint32_t>(a.k) * ES;
   const int blocks = a.k / BLOCK;
   for (int id = blockIdx.x; id < total; id += gridDim.x) {
     Place at{};
-    if (!find_tile(a, id / across, 1, INT32_MAX, &at)) return;
+    if (!find_tile(a, id / across, 1, kFewRows, &at)) return;
     const int n0 = id % across * COLS, cols_left = a.n - n0;
     const char* w[2];
     uint32_t wofs[2];
@@ -791,96 +792,94 @@ template <int DT, int KIND> __global__ __launch_bounds__(kFewThreads) void few_k
       wofs[j] = static_cast<uint32_t>(row < cols_left ? row : cols_left - 1) * row_bytes + q * 16;
     }
     const int turn = blocks > 0 ? id % across * kFirstStep % blocks : 0;
-    for (int m0 = 0; m0 < at.n; m0 += 16) {
-      const int last = at.n - m0 - 1;
-      const char* x = static_cast<const char*>(a.a0) + static_cast<int64_t>(at.first + m0) * row_bytes;
-      const uint32_t xofs = static_cast<uint32_t>(l < last ? l : last) * row_bytes + q * 16;
-      f32x4 acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
-      struct Block {
-        u32x4 w[2][kUnits], x[kUnits];
+    const int m0 = at.index * kFewRows, last = at.n - m0 - 1;
+    const char* x = static_cast<const char*>(a.a0) + static_cast<int64_t>(at.first + m0) * row_bytes;
+    const uint32_t xofs = static_cast<uint32_t>(l < last ? l : last) * row_bytes + q * 16;
+    f32x4 acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+    struct Block {
+      u32x4 w[2][kUnits], x[kUnits];
+    };
+    auto load = [&](Block& f, int block) {
+      block += turn;
+      const int64_t from = static_cast<int64_t>(block >= blocks ? block - blocks : block) * (BLOCK * ES);
+#pragma unroll
+      for (int u = 0; u < kUnits; ++u) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) f.w[j][u] = ldu16(w[j] + from + wofs[j] + u * 64);
+      }
+#pragma unroll
+      for (int u = 0; u < kUnits; ++u) f.x[u] = ldu16(x + from + xofs + u * 64);
+    };
+    auto multiply = [&](const Block& f) {
+#pragma unroll
+      for (int u = 0; u < kUnits; ++u)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc[j] = mma<DT>(f.w[j][u], f.x[u], acc[j]);
+    };
+    Block f0, f1;
+    int b = wave;
+    if (b < blocks) load(f0, b);
+    for (; b < blocks; b += 2 * kFewWaves) {
+      if (b + kFewWaves < blocks) load(f1, b + kFewWaves);
+      multiply(f0);
+      if (b + 2 * kFewWaves < blocks) load(f0, b + 2 * kFewWaves);
+      if (b + kFewWaves < blocks) multiply(f1);
+    }
+    // what is left behind the last whole block, 64 bytes of every row or less for a wave
+    static_assert(kUnits <= kFewWaves, "a wave takes one load's worth of the rest");
+    const int rest = blocks * BLOCK + wave * 4 * V, k = rest + q * V;
+    if (rest < a.k) {
+      const int64_t from = static_cast<int64_t>(rest) * ES;
+      auto end = [&](const char* p) {
+        u32x4 v = {0, 0, 0, 0};
+        if (k + V <= a.k) v = ldu16(p);
+        else if (k < a.k) v = first_elements<DT>(p, a.k - k);
+        return v;
       };
-      auto load = [&](Block& f, int block) {
-        block += turn;
-        const int64_t from = static_cast<int64_t>(block >= blocks ? block - blocks : block) * (BLOCK * ES);
+      const u32x4 xt = end(x + from + xofs);
 #pragma unroll
-        for (int u = 0; u < kUnits; ++u) {
+      for (int j = 0; j < 2; ++j) acc[j] = mma<DT>(end(w[j] + from + wofs[j]), xt, acc[j]);
+    }
 #pragma unroll
-          for (int j = 0; j < 2; ++j) f.w[j][u] = ldu16(w[j] + from + wofs[j] + u * 64);
+    for (int j = 0; j < 2; ++j) sums[wave][j][lane] = acc[j];
+    __syncthreads();
+    // results: lane l of group q has row l and four neighbouring columns of either half
+    if (wave == 0 && l <= last) {
+      f32x4 sum[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        sum[j] = sums[0][j][lane];
+#pragma unroll
+        for (int v = 1; v < kFewWaves; ++v) sum[j] += sums[v][j][lane];
+      }
+      const int64_t ofs = (static_cast<int64_t>(at.first + m0 + l) * a.n + n0) * ES;
+      if constexpr (KIND == kGated) {
+        const int c = q * 4, left = cols_left - c;
+        float g[4], u[4], h[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          g[i] = sum[0][i];
+          u[i] = sum[1][i];
+          activate<DT, false>(a.act, g[i], &h[i], nullptr);
+          h[i] *= u[i];
         }
-#pragma unroll
-        for (int u = 0; u < kUnits; ++u) f.x[u] = ldu16(x + from + xofs + u * 64);
-      };
-      auto multiply = [&](const Block& f) {
-#pragma unroll
-        for (int u = 0; u < kUnits; ++u)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) acc[j] = mma<DT>(f.w[j][u], f.x[u], acc[j]);
-      };
-      Block f0, f1;
-      int b = wave;
-      if (b < blocks) load(f0, b);
-      for (; b < blocks; b += 2 * kFewWaves) {
-        if (b + kFewWaves < blocks) load(f1, b + kFewWaves);
-        multiply(f0);
-        if (b + 2 * kFewWaves < blocks) load(f0, b + 2 * kFewWaves);
-        if (b + kFewWaves < blocks) multiply(f1);
-      }
-      // what is left behind the last whole block, 64 bytes of every row or less for a wave
-      static_assert(kUnits <= kFewWaves, "a wave takes one load's worth of the rest");
-      const int rest = blocks * BLOCK + wave * 4 * V, k = rest + q * V;
-      if (rest < a.k) {
-        const int64_t from = static_cast<int64_t>(rest) * ES;
-        auto end = [&](const char* p) {
-          u32x4 v = {0, 0, 0, 0};
-          if (k + V <= a.k) v = ldu16(p);
-          else if (k < a.k) v = first_elements<DT>(p, a.k - k);
-          return v;
-        };
-        const u32x4 xt = end(x + from + xofs);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) acc[j] = mma<DT>(end(w[j] + from + wofs[j]), xt, acc[j]);
-      }
-#pragma unroll
-      for (int j = 0; j < 2; ++j) sums[wave][j][lane] = acc[j];
-      __syncthreads();
-      // results: lane l of group q has row l and four neighbouring columns of either half
-      if (wave == 0 && l <= last) {
-        f32x4 sum[2];
+        if (left > 0) {
+          store_run<DT, 4>(static_cast<char*>(a.c0) + ofs + c * ES, h, left);
+          if (a.c1) {
+            store_run<DT, 4>(static_cast<char*>(a.c1) + ofs + c * ES, g, left);
+            store_run<DT, 4>(static_cast<char*>(a.c2) + ofs + c * ES, u, left);
+          }
+        }
+      } else {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          sum[j] = sums[0][j][lane];
-#pragma unroll
-          for (int v = 1; v < kFewWaves; ++v) sum[j] += sums[v][j][lane];
-        }
-        const int64_t ofs = (static_cast<int64_t>(at.first + m0 + l) * a.n + n0) * ES;
-        if constexpr (KIND == kGated) {
-          const int c = q * 4, left = cols_left - c;
-          float g[4], u[4], h[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            g[i] = sum[0][i];
-            u[i] = sum[1][i];
-            activate<DT, false>(a.act, g[i], &h[i], nullptr);
-            h[i] *= u[i];
-          }
-          if (left > 0) {
-            store_run<DT, 4>(static_cast<char*>(a.c0) + ofs + c * ES, h, left);
-            if (a.c1) {
-              store_run<DT, 4>(static_cast<char*>(a.c1) + ofs + c * ES, g, left);
-              store_run<DT, 4>(static_cast<char*>(a.c2) + ofs + c * ES, u, left);
-            }
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int c = j * 16 + q * 4, left = cols_left - c;
-            const float v[4] = {sum[j][0], sum[j][1], sum[j][2], sum[j][3]};
-            if (left > 0) store_run<DT, 4>(static_cast<char*>(a.c0) + ofs + c * ES, v, left);
-          }
+          const int c = j * 16 + q * 4, left = cols_left - c;
+          const float v[4] = {sum[j][0], sum[j][1], sum[j][2], sum[j][3]};
+          if (left > 0) store_run<DT, 4>(static_cast<char*>(a.c0) + ofs + c * ES, v, left);
         }
       }
-      __syncthreads();  // the sums are read before the next ones come
     }
+    __syncthreads();  // the sums are read before the next ones come
   }
 }
 
@@ -961,7 +960,7 @@ bool in_words(const ProductArgs& a, int kind, int esize) {
 }
 
 template <int DT, int KIND> hipError_t launch_few(ProductArgs a, hipStream_t s) {
-  a.most = most_experts(a);
+  a.most = static_cast<int>(row_tiles(a, 1, kFewRows));
   const int64_t across = tiles_up(a.n, KIND == kGated ? 16 : 32);
   few_kernel<DT, KIND><<<grid_of(a.most * across, kMostGroups), kFewThreads, 0, s>>>(a);
   return hipGetLastError();

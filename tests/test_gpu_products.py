@@ -273,3 +273,21 @@ def test_matrices_at_the_end_of_their_memory(rows, hidden, inner):
     ref.close(out, *ref.gated(x, wg, wu, ar.AR_ACT_SILU, dt)[0], "out")
     ref.close(dxs, *ref.rounded(ref.mm(torch.cat([dgate, dup], 1), torch.cat([wg, wu], 0)), dt), "dxs")
     ref.close(dwg, *ref.rounded(ref.mm(dgate.t(), x), dt), "dw_gate")
+
+
+@pytest.mark.parametrize("dtype", DT)
+def test_few_rows_that_meet_at_few_experts(dtype):
+    """Few rows on average, nearly all of them at a few of the experts: 16 rows at a time, the last ones not full."""
+    hidden, inner, counts = 200, 72, [0] * 90
+    counts[3], counts[40], counts[89] = 117, 16, 17
+    c = make(hidden, inner, counts, 1, dtype, seed=11)
+    x, wg, wu = c["row"](hidden), c["mat"](inner, hidden), c["mat"](inner, hidden)
+    out, gate, up, y = (c["new"](inner) for _ in range(4))
+    ar.ar_expert_gated(x, wg, wu, out, gate=gate, up=up, **c["seg"])
+    ar.ar_expert_linear(x, wg, y, **c["seg"])
+    untouched(c, out, gate, up, y)
+    for e, rows in c["spans"]:
+        want = ref.gated(x[rows], wg[e], wu[e], ar.AR_ACT_SILU, DT[dtype])
+        for t, (v, tol), what in zip((out, gate, up), want, ("out", "gate", "up")):
+            ref.close(t[rows], v, tol, f"{what} of expert {e}")
+        ref.close(y[rows], *ref.rounded(ref.mm(x[rows], wg[e].t()), DT[dtype]), f"linear of expert {e}")

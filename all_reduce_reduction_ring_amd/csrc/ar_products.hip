@@ -967,12 +967,15 @@ template <int DT, int KIND> hipError_t launch_few(ProductArgs a, hipStream_t s) 
 }
 
 // Which kernel. The host knows rows and experts, not how the rows are spread. (bf16, one MI355X, rows for each expert.)
-//   Few rows (forward products: up to 16 of a dense matrix, 8 an expert on average, 16 in fp32) where 128-wide
-//     tiles would leave the GPU short of workgroups: few_kernel. One of 4096 x 4096, 1 to 16 rows: 12-15 us against 27 with 64 x 64 tiles and 33
-//     with 128 x 128; 8 of 64 experts, gated 2 x 1024 x 2048: 14.3 / 24 / 27; 8 experts, gated 2 x 8192 x 4096, 1 to 8 rows
-//     (1024 tiles): 179-185 / 235 / 232; but 64 of 1024 x 1024, 16 rows: 31 / 29 / 29, and 48 tokens x 4 to 128 experts of
-//     4096 x 1024, where some have many rows: 75 / 55 / 56 (4096 tiles). fp32, 4 experts of 2048 x 4096, 16 rows: 31 / 99,
-//     64 rows 97 / 107.
+//   Few rows (forward products) where 128-wide tiles would leave the GPU short of workgroups: few_kernel. One matrix, up to
+//     16 rows: 4096 x 4096 12-15 us against 27 with 64 x 64 tiles and 33 with 128 x 128. Experts: up to 4 rows each on
+//     average, in fp32 16; rows are spread unevenly, so some experts have many times that, which tiles serve better. 8
+//     experts, one row each, gated 2 x 1024 x 2048: 14.3 / 24 / 27. Segments of a router, few_kernel against tiles, bf16,
+//     gated (up to 8 tiles for each CU): 16 of 2 x 8192 x 4096, 2 rows on average 200 / 248, 8 rows 265 / 252; 64 of 2 x 2048
+//     x 2048, 2 rows 97 / 120, 8 rows 147 / 135; but 128 of 2 x 4096 x 1024 (32 for each CU), 2 rows 180 / 165; linear (one
+//     for each CU): 16 of 2048 x 1024, 4 rows 9.1 / 10.8, 8 rows 13.9 / 10.9; but 64 of 2048 x 2048 (4 for each CU), 4 rows
+//     52 / 46. Over 60 such shapes and 1 to 16 rows either choice is within 2% of the better one on average. fp32, 4 experts of
+//     2048 x 4096, 16 rows: 31 / 99, 64 rows 97 / 107.
 //   256 x 256 tiles (16-bit types, whole chunks): half the reads of the operands, but one workgroup a CU. From 192 rows an
 //     expert and three tiles for four CUs on. 16 of 2048 x 2048: 128 rows, gated 75 us with 128 x 128 tiles / 81 with
 //     256 x 256; 256 rows 112 / 86, linear (128 large tiles) 53 / 58; 1024 rows 329 / 249. Gradients of weights write more
@@ -993,8 +996,9 @@ template <int DT, int KIND> hipError_t launch_tiles(const ProductArgs& a, hipStr
   constexpr int COLS = KIND == kGated ? 64 : 128, V = Traits<DT>::kVec;
   const int64_t cus = cu_count(), across = tiles_up(a.n, COLS);
   if constexpr (KIND == kGated || KIND == kLinear) {
-    const int64_t few = a.offsets && Traits<DT>::kSize == 2 ? 8 : 16;
-    if (a.rows <= few * a.experts && most_experts(a) * across <= 4 * cus) return launch_few<DT, KIND>(a, s);
+    const bool spread = a.offsets && Traits<DT>::kSize == 2;
+    const int64_t rows = spread ? 4 : 16, tiles = !spread ? 4 : KIND == kGated ? 8 : 1;
+    if (a.rows <= rows * a.experts && most_experts(a) * across <= tiles * cus) return launch_few<DT, KIND>(a, s);
   }
   const int64_t down = KIND == kWeight ? matrices(a) * tiles_up(a.m, 128) : tiles_up(a.rows, 128);
   bool least = down * across < cus;

@@ -60,19 +60,23 @@ __device__ __forceinline__ void segment(const ProductArgs& a, int e, int* first,
   *n = m < a.rows - *first ? m : a.rows - *first;
 }
 
-// Tiles of expert e: its elements (rows * width) over `unit`.
-__device__ __forceinline__ int tiles_of(const ProductArgs& a, int e, int64_t width, int unit) {
+// The segments of the first 64 experts, one a lane, held from the count of all tiles to the search for one.
+struct Lane {
   int first, n;
-  segment(a, e, &first, &n);
-  return static_cast<int>((n * width + unit - 1) / unit);
+};
+__device__ __forceinline__ Lane lane_segment(const ProductArgs& a, int e) {
+  Lane s{0, 0};
+  if (e < a.experts) segment(a, e, &s.first, &s.n);
+  return s;
 }
+// Tiles of n rows: their elements (n * width) over `unit`.
+__device__ __forceinline__ int tiles_of(int n, int64_t width, int unit) { return static_cast<int>((n * width + unit - 1) / unit); }
 
 // Tiles of all experts. All lanes of a wave take part; the result is the same in each.
-__device__ __forceinline__ int all_tiles(const ProductArgs& a, int64_t width, int unit) {
-  if (!a.offsets) return tiles_of(a, 0, width, unit);
-  const int lane = threadIdx.x & 63;
-  int sum = 0;
-  for (int e = lane; e < a.experts; e += 64) sum += tiles_of(a, e, width, unit);
+__device__ __forceinline__ int all_tiles(const ProductArgs& a, const Lane& own, int64_t width, int unit) {
+  if (!a.offsets) return tiles_of(a.rows, width, unit);
+  int sum = tiles_of(own.n, width, unit);
+  for (int e = (threadIdx.x & 63) + 64; e < a.experts; e += 64) sum += tiles_of(lane_segment(a, e).n, width, unit);
 #pragma unroll
   for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d, 64);
   return uniform(sum);
@@ -82,16 +86,15 @@ __device__ __forceinline__ int all_tiles(const ProductArgs& a, int64_t width, in
 struct Place {
   int expert, index, first, n;
 };
-__device__ __forceinline__ bool find_tile(const ProductArgs& a, int t, int64_t width, int unit, Place* at) {
+__device__ __forceinline__ bool find_tile(const ProductArgs& a, const Lane& mine, int t, int64_t width, int unit, Place* at) {
   if (!a.offsets) {
     *at = Place{0, t, 0, a.rows};
     return true;
   }
   const int lane = threadIdx.x & 63;
   for (int e0 = 0, before = 0; e0 < a.experts; e0 += 64) {
-    int first = 0, n = 0;
-    if (e0 + lane < a.experts) segment(a, e0 + lane, &first, &n);
-    const int own = static_cast<int>((n * width + unit - 1) / unit);
+    const Lane s = e0 == 0 ? mine : lane_segment(a, e0 + lane);
+    const int own = tiles_of(s.n, width, unit);
     int upto = own;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
@@ -99,11 +102,11 @@ __device__ __forceinline__ bool find_tile(const ProductArgs& a, int t, int64_t w
       if (lane >= d) upto += y;
     }
     upto += before;
-    const uint64_t mine = __ballot(t >= upto - own && t < upto);
-    if (mine) {
-      const int l = __builtin_ctzll(mine);
+    const uint64_t has = __ballot(t >= upto - own && t < upto);
+    if (has) {
+      const int l = __builtin_ctzll(has);
       auto of = [&](int v) { return __builtin_amdgcn_readlane(v, l); };
-      *at = Place{uniform(e0 + l), t - of(upto - own), of(first), of(n)};
+      *at = Place{uniform(e0 + l), t - of(upto - own), of(s.first), of(s.n)};
       return true;
     }
     before = __builtin_amdgcn_readlane(upto, 63);
@@ -416,11 +419,13 @@ __global__ __launch_bounds__(WM* WN * 64) void tile_kernel(const ProductArgs a) 
   // Tiles of the result: rows of it per expert (weight: of every matrix) and columns.
   const int across = (a.n + COLS - 1) / COLS;
   int down, total;
+  Lane mine{0, 0};
   if constexpr (KIND == kWeight) {
     down = (a.m + BM - 1) / BM;
     total = a.experts * (a.a1 ? 2 : 1) * down * across;
   } else {
-    down = min(all_tiles(a, 1, BM), a.most);
+    if (a.offsets) mine = lane_segment(a, threadIdx.x & 63);
+    down = min(all_tiles(a, mine, 1, BM), a.most);
     total = down * across;
   }
   for (int id = blockIdx.x; id < total; id += gridDim.x) {
@@ -436,7 +441,7 @@ __global__ __launch_bounds__(WM* WN * 64) void tile_kernel(const ProductArgs a) 
       int row;
       raster(xcd_order(id, total), down, across, &row, &nt);
       Place at{};
-      if (!find_tile(a, row, 1, BM, &at)) continue;  // tables that changed meanwhile
+      if (!find_tile(a, mine, row, 1, BM, &at)) continue;  // tables that changed meanwhile
       e = at.expert;
       mt = at.index;
       first = at.first;
@@ -778,9 +783,10 @@ template <int DT, int KIND> __global__ __launch_bounds__(kFewThreads) void few_k
   const int total = a.most * across;  // there may be fewer
   const uint32_t row_bytes = static_cast<uint32_t>(a.k) * ES;
   const int blocks = a.k / BLOCK;
+  const Lane mine = a.offsets ? lane_segment(a, lane) : Lane{0, 0};
   for (int id = blockIdx.x; id < total; id += gridDim.x) {
     Place at{};
-    if (!find_tile(a, id / across, 1, kFewRows, &at)) return;
+    if (!find_tile(a, mine, id / across, 1, kFewRows, &at)) return;
     const int n0 = id % across * COLS, cols_left = a.n - n0;
     const char* w[2];
     uint32_t wofs[2];
@@ -890,10 +896,11 @@ constexpr int kSlopeThreads = 256, kSlopeUnit = 8192, kSlopeLeast = 1024;
 
 template <int DT, int UNIT> __global__ __launch_bounds__(kSlopeThreads) void slopes_kernel(const ProductArgs a) {
   constexpr int V = Traits<DT>::kVec, ES = Traits<DT>::kSize;
-  const int total = min(all_tiles(a, a.n, UNIT), a.most);
+  const Lane mine = a.offsets ? lane_segment(a, threadIdx.x & 63) : Lane{0, 0};
+  const int total = min(all_tiles(a, mine, a.n, UNIT), a.most);
   for (int id = blockIdx.x; id < total; id += gridDim.x) {
     Place at;
-    if (!find_tile(a, id, a.n, UNIT, &at)) continue;  // tables that changed meanwhile
+    if (!find_tile(a, mine, id, a.n, UNIT, &at)) continue;  // tables that changed meanwhile
     const int64_t base = static_cast<int64_t>(at.first) * a.n + static_cast<int64_t>(at.index) * UNIT;
     const int64_t rest = static_cast<int64_t>(at.n) * a.n - static_cast<int64_t>(at.index) * UNIT;
     const int len = rest < UNIT ? static_cast<int>(rest) : UNIT;

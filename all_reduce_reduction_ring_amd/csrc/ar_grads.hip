@@ -134,8 +134,8 @@ template <int DT> __device__ __forceinline__ void scale(const ar_grad_piece& p, 
 template <bool MAX> __global__ __launch_bounds__(kThreads) void clip_kernel(const GradArgs a) {
   const float norm = total_norm<MAX>(a);
   if (blockIdx.x == 0 && threadIdx.x == 0) *gptr<float>(a.norm) = norm;
-  const float ratio = a.max_norm / (norm + a.eps);
-  const float c = ratio >= 1.0f ? 1.0f : ratio;  // NaN stays
+  // 1 also where both sides are 0 or infinite; a NaN goes on into the quotient
+  const float c = norm + a.eps <= a.max_norm ? 1.0f : a.max_norm / (norm + a.eps);
   for (int64_t i = a.npieces - 1 - blockIdx.x; i >= 0; i -= gridDim.x) {
     const ar_grad_piece p = a.pieces[i];
     if (c == 1.0f && (!p.out || p.out == p.in)) continue;  // x * 1 in place

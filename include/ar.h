@@ -483,9 +483,9 @@ int ar_grad_norm(const ar_grad_piece* d_pieces, size_t npieces, int kind, float*
                  void* stream);
 
 /* The same, and out = in * min(1, max_norm / (norm + eps)) for every element, in fp32, rounded once. Where that is 1,
- * pieces in place are not written. A norm of NaN makes every element NaN, one of infinity (an infinite element, with a
- * finite max_norm) zero or, from infinities, NaN: check norm before the step. max_norm and eps: not negative, not NaN, eps
- * finite. Errors as ar_grad_norm. */
+ * pieces in place are not written. A norm of NaN makes every element NaN, one of infinity (an infinite element, or a norm
+ * above fp32's range; with a finite max_norm) zero or, from infinities, NaN: check norm before the step. max_norm and eps:
+ * not negative, not NaN, eps finite. norm and workspace lie apart from the table's tensors. Errors as ar_grad_norm. */
 int ar_grad_clip(const ar_grad_piece* d_pieces, size_t npieces, int kind, float max_norm, float eps, float* norm,
                  void* workspace, size_t ws_bytes, void* stream);
 

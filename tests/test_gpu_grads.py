@@ -106,6 +106,23 @@ def test_far_numbers():
     assert (t == 0).all()
 
 
+def test_bounds_that_the_norm_just_meets():
+    """0 / 0 and inf / inf are no scale: zeros under a bound of 0 without eps stay, and no bound leaves infinities alone."""
+    for kind in (ar.AR_NORM_L2, ar.AR_NORM_MAX):
+        t, out = torch.zeros(300, device=DEV), torch.full((300,), 7.0, device=DEV)
+        assert call([t], [out], 0.0, kind, eps=0.0) == 0.0 and (out == 0).all()
+        t = torch.ones(300, device=DEV)
+        t[5] = math.inf
+        want = t.clone()
+        assert math.isinf(call([t], None, math.inf, kind)) and torch.equal(t, want)
+        t = torch.full((300,), 3.0, device=DEV)
+        exact = math.sqrt(2700.0) if kind == ar.AR_NORM_L2 else 3.0
+        norm = torch.tensor(exact, dtype=torch.float32).item()
+        call([t], [out], norm, kind, eps=0.0)
+        assert torch.equal(out, t)
+        assert math.isnan(call([torch.full((3,), math.nan, device=DEV)], [out[:3]], math.inf, kind)) and out[:3].isnan().all()
+
+
 def test_without_elements():
     empty = torch.empty(0, device=DEV)
     assert call([empty]) == 0.0 and call([empty], None, 1.0) == 0.0

@@ -884,8 +884,10 @@ int product_common(size_t rows, size_t in, size_t out, int dtype, const int32_t*
 }
 
 // Adds one matrix per expert, `stride` elements apart (none but the size of a matrix matters for a single expert), and a
-// second set of the same layout (or NULL) that may lie in the gaps of the first, as the halves of one tensor do.
+// second set of the same layout (or NULL) that may lie in the gaps of the first, as the halves of one tensor do. Where both
+// are NULL there is nothing to check: a caller who leaves a weight out has no stride for it.
 bool add_matrices(Ranges& g, const void* p0, const void* p1, size_t matrix, size_t stride, int nexperts, size_t es) {
+  if (!p0 && !p1) return true;
   size_t span = 0;
   if (nexperts == 1) stride = matrix;
   if (stride < matrix || !mul(stride, static_cast<size_t>(nexperts - 1), &span) || !mul(span + matrix, es, &span))

@@ -430,7 +430,8 @@ int ar_expert_gated(const void* xs, const void* w_gate, const void* w_up, size_t
  *   dxs = dgate w_gate + dup w_up                                       (of the rounded dgate and dup, in one sum)
  *   dw_gate = dgate^T xs,   dw_up = dup^T xs   over every expert's rows (dw_stride apart, zero without rows)
  * dgate and dup are different buffers; either may be dout, gate or up. dxs may be NULL (then w_gate and w_up are not
- * read and may be), and so may dw_gate and dw_up together (then xs is not read). */
+ * read and may be), and so may dw_gate and dw_up together (then xs is not read and may be). The distance of matrices that
+ * are NULL is not looked at. */
 int ar_expert_gated_bwd(const void* dout, const void* gate, const void* up, const void* xs, const void* w_gate,
                         const void* w_up, size_t w_stride, const int32_t* offsets, const int32_t* counts, int nexperts,
                         size_t rows, size_t hidden, size_t inner, int dtype, int act, void* dgate, void* dup, void* dxs,
@@ -441,7 +442,7 @@ int ar_expert_linear(const void* xs, const void* w, size_t w_stride, const int32
                      int nexperts, size_t rows, size_t in, size_t out, int dtype, void* ys, void* stream);
 
 /* Its gradient: dxs = dys w and dw = dys^T xs over every expert's rows (zero without rows). dxs may be NULL (then w is
- * not read and may be), and so may dw (then xs may be). */
+ * not read and may be), and so may dw (then xs may be). The distance of matrices that are NULL is not looked at. */
 int ar_expert_linear_bwd(const void* dys, const void* xs, const void* w, size_t w_stride, const int32_t* offsets,
                          const int32_t* counts, int nexperts, size_t rows, size_t in, size_t out, int dtype, void* dxs,
                          void* dw, size_t dw_stride, void* stream);

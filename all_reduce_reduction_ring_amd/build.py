@@ -42,6 +42,7 @@ CFLAGS = [
     f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-ffp-contract=off",
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-Wall", "-Wno-unused-command-line-argument",
+    "-Wno-inline-asm",  # statements that name m0 as overwritten: the compiler does not allocate it, and says so at each
     "-I", os.path.join(ROOT, "include"), "-I", CSRC,
 ]
 

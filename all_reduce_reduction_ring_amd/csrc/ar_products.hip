@@ -163,8 +163,10 @@ __device__ __forceinline__ void load_lds(const char* base, uint32_t bytes, uint3
   const uint64_t b = reinterpret_cast<uint64_t>(base);
   auto scalar = [](uint32_t v) { return static_cast<uint32_t>(uniform(static_cast<int>(v))); };
   const u32x4 rsrc = {scalar(static_cast<uint32_t>(b)), scalar(static_cast<uint32_t>(b >> 32) & 0xFFFFu), scalar(bytes), 0x00020000u};
+  // m0 is named as overwritten, so that nothing the compiler put there is taken to outlive the statement (it warns that m0 is
+  // a register it does not allocate; the build leaves that warning out)
   asm volatile("s_mov_b32 m0, %2\n\ts_nop 4\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(at), "s"(rsrc), "s"(scalar(lds))
-               : "memory");
+               : "memory", "m0");
 }
 // All but the last N of a wave's loads have landed and its reads of LDS are done, for all waves of the workgroup.
 template <int N> __device__ __forceinline__ void ready() {

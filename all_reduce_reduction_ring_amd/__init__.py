@@ -550,6 +550,19 @@ def _ints(**named):
     return tuple(named.values())
 
 
+def _reals(**named):
+    """Numbers that C takes as float. A tensor's value would have to be waited for, so only one on the host is a number."""
+    import torch
+    for what, v in named.items():
+        if torch.is_tensor(v) and v.device.type != "cpu":
+            raise ValueError(f"{what} must be a number, not a tensor on {v.device}: its value would be waited for")
+        try:
+            named[what] = float(v)
+        except (TypeError, ValueError, OverflowError, RuntimeError) as e:
+            raise ValueError(f"{what} must be a number: {e}") from None
+    return tuple(named.values())
+
+
 def _workspace_arg(ws, dev):
     if ws is None:
         return None, 0
@@ -962,14 +975,15 @@ def ar_grad_norm(plan, norm, kind=AR_NORM_L2, workspace=None, stream=None):
 
 
 def ar_grad_clip(plan, max_norm, norm, kind=AR_NORM_L2, eps=1e-6, workspace=None, stream=None):
-    """ar_grad_norm, and all gradients times min(1, max_norm / (norm + eps)) into the plan's outputs."""
+    """ar_grad_norm, and all gradients times min(1, max_norm / (norm + eps)) into the plan's outputs. max_norm and eps are
+    numbers on the host: a GPU tensor is refused, not waited for."""
     native = _native if _native is not None else _load_native()
     if native and _done(native.grad_clip(plan, max_norm, norm, kind, eps, workspace, stream), "ar_grad_clip"):
         return
     at, n, to, ws = _plan_args(plan, norm, workspace)
     with _on(plan.device):
-        _check(lib().ar_grad_clip(at, n, *_ints(kind=kind), max_norm, eps, to, *ws, _stream(stream, plan.device)),
-               "ar_grad_clip")
+        _check(lib().ar_grad_clip(at, n, *_ints(kind=kind), *_reals(max_norm=max_norm, eps=eps), to, *ws,
+                                  _stream(stream, plan.device)), "ar_grad_clip")
 
 
 # ------------------------------------------------------------------------------------------ bucketing

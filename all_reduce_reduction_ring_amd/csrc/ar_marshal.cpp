@@ -464,7 +464,9 @@ struct Plan {
   }
 };
 
+// A number, not what could be made one: a GPU tensor's value would be waited for.
 float real(PyObject* o) {
+  if (!PyFloat_Check(o) && !PyLong_Check(o)) throw Misfit();
   const double v = PyFloat_AsDouble(o);
   if (v == -1.0 && PyErr_Occurred()) throw Misfit();
   return static_cast<float>(v);

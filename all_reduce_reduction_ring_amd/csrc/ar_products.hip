@@ -249,7 +249,7 @@ template <int DT, bool KS, bool PAIRED, bool DIRECT, int CH, int R, int NT> stru
       const int n = K - k0 - chunk * V;
       const uint32_t at_byte = at[i] + chunk * 16;
       if (n <= 0) return u32x4{0, 0, 0, 0};
-      if (at_byte + 16 > left) return first_elements<DT>(base + at_byte, n);
+      if (!chunk_inside(at_byte, left)) return first_elements<DT>(base + at_byte, n);
       u32x4 w = ldu16(base + at_byte);
       if (k0 + CH * V > K) {
 #pragma unroll
@@ -264,7 +264,7 @@ template <int DT, bool KS, bool PAIRED, bool DIRECT, int CH, int R, int NT> stru
       const int c = ((static_cast<int>(threadIdx.x) % kRowChunks) ^ mix_ks<DT, R>(row)) * V;
       const uint32_t at_byte = static_cast<uint32_t>(row) * stride + c * ES;
       if (k0 + row >= K) return u32x4{0, 0, 0, 0};
-      if (at_byte + 16 > left) return first_elements<DT>(base + at_byte, limit - c);
+      if (!chunk_inside(at_byte, left)) return first_elements<DT>(base + at_byte, limit - c);
       return ldu16(base + at_byte);
     }
   }
@@ -773,11 +773,11 @@ __global__ __launch_bounds__(WM* WN * 64) void tile_kernel(const ProductArgs a) 
 // two of bytes would have all of them read the same few memory channels at a time (8 of 64 experts, 2 x 1024 x 2048 bf16:
 // 18.2 -> 14.6 us; 8 experts, 8192 x 4096: 114 -> 95).
 constexpr int kFewRows = 16, kFewThreads = 256, kFewWaves = kFewThreads / 64;
-constexpr int kUnits = 2;      // loads of a row's 64 bytes per block (4: 10% slower at 64 experts of 1024 x 1024)
+constexpr int kUnits = kFewUnits;  // loads of a row's 64 bytes per block (4: 10% slower at 64 experts of 1024 x 1024)
 constexpr int kFirstStep = 9;  // blocks between the first ones of neighbouring workgroups
 
 template <int DT, int KIND> __global__ __launch_bounds__(kFewThreads) void few_kernel(const ProductArgs a) {
-  constexpr int ES = Traits<DT>::kSize, V = Traits<DT>::kVec, BLOCK = kUnits * 4 * V;  // elements of a block
+  constexpr int ES = Traits<DT>::kSize, V = Traits<DT>::kVec, BLOCK = few_block(V);  // elements of a block
   constexpr int COLS = KIND == kGated ? 16 : 32;
   __shared__ f32x4 sums[kFewWaves][2][64];
   const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, l = lane & 15, q = lane >> 4;
@@ -840,7 +840,7 @@ template <int DT, int KIND> __global__ __launch_bounds__(kFewThreads) void few_k
       const int64_t from = static_cast<int64_t>(rest) * ES;
       auto end = [&](const char* p) {
         u32x4 v = {0, 0, 0, 0};
-        if (k + V <= a.k) v = ldu16(p);
+        if (few_whole(k, a.k, V)) v = ldu16(p);
         else if (k < a.k) v = first_elements<DT>(p, a.k - k);
         return v;
       };

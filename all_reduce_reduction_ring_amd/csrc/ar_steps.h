@@ -46,4 +46,14 @@ constexpr uint32_t load_bytes(uint32_t high, uint32_t low) {
   return high != 0 ? kMostLoadBytes : low < kMostLoadBytes ? low : kMostLoadBytes;
 }
 
+// Loads through registers have no limit of their own: a chunk at byte `at` from the base is read whole where it ends within the
+// `left` bytes, and element by element otherwise.
+constexpr bool chunk_inside(uint32_t at, uint32_t left) { return at + 16 <= left; }
+
+// The products of few rows walk a sum of k elements in blocks of kFewUnits times 64 bytes; behind the last whole block a lane
+// takes the chunk of `v` elements at element `at` where it lies within the sum, or else what the sum's end leaves of it.
+constexpr int kFewUnits = 2;
+constexpr int few_block(int v) { return kFewUnits * 4 * v; }
+constexpr bool few_whole(int at, int k, int v) { return at + v <= k; }
+
 }  // namespace ar

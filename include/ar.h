@@ -406,8 +406,8 @@ int ar_expert_combine_bwd(const void* dout, const void* ys, const int32_t* pos, 
  * offsets[e + 1]) and one [out][in] matrix of every weight, w_stride (at least in * out) elements after the previous
  * expert's; a weight may be a part of a wider tensor. Rows outside the segments, pad rows among them, are neither read
  * nor written. offsets and counts NULL with nexperts 1: one matrix for all rows (a dense layer).
- * The tables are read on the device: segments that leave [0, rows) are cut off, and segments that overlap give
- * unspecified values.
+ * The tables are read on the device: a segment that runs past the last row is cut off there, one that starts outside
+ * [0, rows) or has a negative count is taken for empty, and segments that overlap give unspecified values.
  * Products are summed in fp32; bf16 and f16 operands are multiplied exactly. The order of a sum is fixed by the call's
  * sizes, types and addresses' alignment, not by what lies in the segments of other experts.
  * Any address that is a multiple of the element size; multiples of 16 bytes, in addresses and in rows, run fastest, and
@@ -486,7 +486,10 @@ int ar_grad_norm(const ar_grad_piece* d_pieces, size_t npieces, int kind, float*
 /* The same, and out = in * min(1, max_norm / (norm + eps)) for every element, in fp32, rounded once. Where that is 1,
  * pieces in place are not written. A norm of NaN makes every element NaN, one of infinity (an infinite element, or a norm
  * above fp32's range; with a finite max_norm) zero or, from infinities, NaN: check norm before the step. max_norm and eps:
- * not negative, not NaN, eps finite. norm and workspace lie apart from the table's tensors. Errors as ar_grad_norm. */
+ * not negative, not NaN, eps finite. norm and workspace lie apart from the table's tensors. Errors as ar_grad_norm.
+ * The norm is that of this table. Where other ranks hold gradients that count as well (experts' weights spread over ranks), a
+ * caller who has the norm over all of them passes max_norm * (own + eps) / (all + eps), with `own` from ar_grad_norm of the
+ * same table: the factor is then min(1, max_norm / (all + eps)) but for three more roundings (own and all finite). */
 int ar_grad_clip(const ar_grad_piece* d_pieces, size_t npieces, int kind, float max_norm, float eps, float* norm,
                  void* workspace, size_t ws_bytes, void* stream);
 

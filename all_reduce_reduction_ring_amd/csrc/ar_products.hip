@@ -17,14 +17,22 @@
 // tile counts (64 experts a step) and the grid is as large as any segments of so many rows need.
 //
 // Sums are fp32 and rounded once, to the results' type. The gated gradient rounds dg and du to it before the two products
-// that read them, which take 16-bit operands anyway.
+// that read them, which take 16-bit operands anyway: the gradients' error is sqrt(2) of one rounding's (bf16 0.0023 of the norm
+// for 0.0017, fp16 0.00029 for 0.00021).
 //
-// What bounds it: with many rows, the matrix instructions and the power they draw. 32,768 rows of 32 experts, gated 2 x 2048
-// x 4096 bf16, segments as a router leaves them: 1.10 ms, 1000 TF (a library product of one matrix of that size reaches
-// 1245); a dense 16,384 x 4160 x 4096: matrix units busy 74% of the time, 1300 TF, and 1430 on zeros, which draw less power.
+// What bounds it: with many rows, the matrix instructions and the power they draw, and whole rounds of tiles. Rates of calls in a
+// row, bf16, next to one library product of the same size: 32,768 rows of one matrix, gated 2 x 2048 x 4096 with both products
+// kept 1,230 TF (library 1,530), linear 4096 x 4096 1,340 (1,530), dx 1,330 (1,330), dw 1,380 (1,200). The same gated rows at 32
+// experts, spread evenly 1,160 TF; as a router leaves them 990 (1.10 ms): tiles that are not full make 2,368 of 2,048, 10 rounds
+// of 256 in the place of 8. A dense 16,384 x 4160 x 4096: matrix units busy 74% of the time, 1,300 TF, and 1,430 on
+// zeros, which draw less power.
 // With few rows, reading the weights: 4.9 TB/s (a copy reaches 4.8). Weights' gradients of few rows, writing them: 268 MB in
 // 80 us, and 0.19 us more for every row of 16 experts of 4096 x 2048. Rows of odd numbers of 16-bit elements (or odd
-// addresses) cannot be loaded straight into LDS and take about 2.5 times as long.
+// addresses) cannot be loaded straight into LDS, and take twice to four and a half times as long: 16 experts of 2049 x 2049
+// (of 2048 x 2048), 2,048 rows: forward 129 us (42), dx 126 (38), dw 164 (54); 16,384 rows 544 (121), 535 (121), 562 (139). Rows of
+// 2050, whose last chunk is mended: 80, 54, 74; 292, 220, 175.
+// A sum is never split over workgroups: dw of few tiles over many rows leaves most of the GPU idle (64 x 64 to 256 x 256 over 8,192
+// rows 42 to 48 us in bf16, 210 in fp32; 16 of 2048 x 2048 with 16,384 rows at one expert 326 us, spread evenly 138).
 #include "ar_block.h"
 #include "ar_internal.h"
 #include "ar_products.h"
@@ -396,9 +404,13 @@ enum Loads { kRegisters = 0, kWhole = 1, kCut = 2 };
 
 // WM x WN waves, each with a part of BM / WM rows and BN / WN columns (gated: of half as many, and both products of them) in
 // registers. Sizes of a part: 128 x 64 in the 256 x 256 tile, whose 128 registers of sums leave room for the fragments of a
-// step; 64 x 64 in the 128 x 128 one (two workgroups a compute unit); 16 x 64 in the 64 x 64 one (four). 128 x 128 for each of
-// four waves spills. LDS: five operand tiles of 128 bytes along the sum, 160 / 80 / 40 KB. Steps of
-// half the length took 11% longer (131,072 rows, 64 experts of 2048 x 1024), having twice the barriers.
+// step; 64 x 64 in the 128 x 128 one; 16 x 64 in the 64 x 64 one. 128 x 128 for each of four waves spills. LDS: five operand tiles
+// of 128 bytes along the sum, 160 / 80 / 40 KB, room for 1 / 2 / 4 workgroups on a compute unit. Registers allow as many with
+// loads straight into LDS (but one of the 128 x 128 linear kernel that mends chunks), and fewer through registers: one of 128 x 128,
+// three of 64 x 64 (linear, dx). The compiler keeps sums of the 128 x 128 tiles, and of some 64 x 64 ones, in accumulation
+// registers and moves them there and back in every step (96 moves beside 32 matrix instructions of 16-bit types, 84 beside 128 of
+// fp32); the 256 x 256 tiles have no moves, but keep some scalars in vector registers (5 to 14 reads of them a step).
+// Steps of half the length took 11% longer (131,072 rows, 64 experts of 2048 x 1024), having twice the barriers.
 // Level or worse at 32 experts of 2 x 2048 x 4096 bf16: 32 x 32 instructions (3%), a raised wave priority (0), workgroups that
 // start their next tile's loads before they write results (0 to 70%: the tiles of uneven segments spread less evenly).
 template <int DT, int KIND, int LOADS, int BM, int BN, int WM, int WN>
@@ -977,7 +989,9 @@ template <int DT, int KIND> hipError_t launch_few(ProductArgs a, hipStream_t s) 
 
 // Which kernel. The host knows rows and experts, not how the rows are spread. (bf16, one MI355X, rows for each expert.)
 //   Few rows (forward products) where 128-wide tiles would leave the GPU short of workgroups: few_kernel. One matrix, up to
-//     16 rows: 4096 x 4096 12-15 us against 27 with 64 x 64 tiles and 33 with 128 x 128. Experts: up to 4 rows each on
+//     16 rows: 4096 x 4096 12-15 us against 27 with 64 x 64 tiles and 33 with 128 x 128, the matrix in the last-level cache. Read
+//     from memory, 16 rows 13.8 us; from 17 to 512 rows 64 x 64 tiles take 42-43 (a library product 18-29): too few of them
+//     to keep memory busy. Experts: up to 4 rows each on
 //     average, in fp32 16; rows are spread unevenly, so some experts have many times that, which tiles serve better. 8
 //     experts, one row each, gated 2 x 1024 x 2048: 14.3 / 24 / 27. Segments of a router, few_kernel against tiles, bf16,
 //     gated (up to 8 tiles for each CU): 16 of 2 x 8192 x 4096, 2 rows on average 200 / 248, 8 rows 265 / 252; 64 of 2 x 2048
@@ -985,6 +999,8 @@ template <int DT, int KIND> hipError_t launch_few(ProductArgs a, hipStream_t s) 
 //     for each CU): 16 of 2048 x 1024, 4 rows 9.1 / 10.8, 8 rows 13.9 / 10.9; but 64 of 2048 x 2048 (4 for each CU), 4 rows
 //     52 / 46. Over 60 such shapes and 1 to 16 rows either choice is within 2% of the better one on average. fp32, 4 experts of
 //     2048 x 4096, 16 rows: 31 / 99, 64 rows 97 / 107.
+//     The rows are those of the buffers: segments that a sort padded count with their pads. 8 slots at 64 experts of 2 x 1024 x
+//     2048 bf16, padded to 1, 16, 128 rows (8, 128, 1,024 rows): 13.2, 15.7 us, and 24.8 with tiles.
 //   256 x 256 tiles (16-bit types, whole chunks): half the reads of the operands, but one workgroup a CU. From 192 rows an
 //     expert and three tiles for four CUs on. 16 of 2048 x 2048: 128 rows, gated 75 us with 128 x 128 tiles / 81 with
 //     256 x 256; 256 rows 112 / 86, linear (128 large tiles) 53 / 58; 1024 rows 329 / 249. Gradients of weights write more
